@@ -25,6 +25,8 @@ __all__ = [
     "codebook", "FORMATS", "SCALES", "status_string", "kernel_launches", "set_gemm_events",
     "debug_stall_next_gemm", "read_status", "storage_bytes", "LIB_PATH", "QLoRAError",
     "adapter_merge", "adamw_step", "PagedBuffer", "paged_empty",
+    "MXTensor", "MXWeight", "Dropout", "mx_storage_bytes", "mx_quantize", "mx_dequant", "mx_matmul", "mx_weight",
+    "mx_linear_fwd", "mx_linear_bwd", "mx_linear_workspace_bytes", "dropout",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqlora_nf4.so")
@@ -97,7 +99,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise QLoRAError(f"{LIB_PATH} is missing: build it with `python -m bit_nf4_quantized_15_b200.build`")
         h = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in {**_SIGS, **mx.SIGS}.items():
             f = getattr(h, name)
             f.restype = res
             f.argtypes = args
@@ -362,3 +364,10 @@ def paged_empty(n: int, device="cuda") -> "PagedBuffer":
     b = PagedBuffer(n, device)
     b.tensor.zero_()
     return b
+
+
+from . import mx  # noqa: E402  (the MXFP4 calls use the helpers above)
+from .mx import (  # noqa: E402
+    Dropout, MXTensor, MXWeight, dropout, mx_dequant, mx_linear_bwd, mx_linear_fwd, mx_linear_workspace_bytes,
+    mx_matmul, mx_quantize, mx_storage_bytes, mx_weight,
+)

@@ -13,13 +13,7 @@
 
 using namespace qnf4;
 
-namespace {
-
-// --------------------------------------------------------------- device info
-struct DevInfo {
-  int ok = 0;
-  int sms = 148;
-};
+namespace qnf4 {
 
 int current_device_info(DevInfo* out) {
   int dev = 0;
@@ -43,7 +37,7 @@ int current_device_info(DevInfo* out) {
 }
 
 // ----------------------------------------------------------------- TMA maps
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -56,19 +50,31 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2-D map over a row-major matrix [outer][inner] of `esize`-byte elements.
 int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t inner, uint64_t outer,
-             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
+             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw, uint64_t pitch) {
   auto fn = encode_fn();
   if (!fn) return QLORA_ERR_CUDA;
   const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {inner * (uint64_t)esize};
+  const cuuint64_t strides[1] = {pitch ? pitch : inner * (uint64_t)esize};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
 }
+
+int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows,
+                uint64_t pitch) {
+  if (!mn_major)
+    return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k_extent, mn_extent, 64, (uint32_t)rows,
+                    CU_TENSOR_MAP_SWIZZLE_128B, pitch);
+  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, mn_extent, k_extent, 64, 64,
+                  CU_TENSOR_MAP_SWIZZLE_128B, pitch);
+}
+
+}  // namespace qnf4
+
+namespace {
 
 // 3-D map over a row-major matrix [rows][cols] of bf16 viewed as
 // (64, rows, cols / 64): element (x, y, z) is [y][64 z + x]; box 64 x
@@ -86,16 +92,6 @@ int map_blocks3d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
-}
-
-// bf16 operand of the engine.  K-major: matrix [mn][k] (k contiguous), box
-// 64 k x `rows` mn.  MN-major: matrix [k][mn] (mn contiguous), box 64 x 64.
-int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows) {
-  if (!mn_major)
-    return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k_extent, mn_extent, 64, (uint32_t)rows,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
-  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, mn_extent, k_extent, 64, 64,
-                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int map_codes(CUtensorMap* m, const uint8_t* codes, int64_t N, int64_t K, int mn_mode) {
@@ -232,6 +228,12 @@ bool shape_ok(int64_t M, int64_t N, int64_t K) {
 
 }  // namespace
 
+uint64_t qnf4::take_stall_request() {
+  const uint64_t ns = g_stall_ns;
+  g_stall_ns = 0;
+  return ns;
+}
+
 extern "C" {
 
 const char* qlora_status_string(int code) {
@@ -248,6 +250,11 @@ const char* qlora_status_string(int code) {
     case QLORA_ERR_DEVICE: return "current device is not an sm_100 GPU";
     case QLORA_ERR_FORMAT: return "unknown code format (QLORA_FMT_*) or scale codec (QLORA_SCALE_*)";
     case QLORA_ERR_SCRATCH_LIMIT: return "problem needs more workspace than the library's 8 MiB static scratch";
+    case QLORA_ERR_DTYPE: return "unknown or unsupported element type (QLORA_DTYPE_*)";
+    case QLORA_ERR_DROPOUT: return "dropout probability outside [0, 1)";
+    case QLORA_ERR_MX_SHAPE:
+      return "invalid MXFP4 shape (need a block axis that is a multiple of 32, other axes a multiple of 8 where "
+             "they are contiguous, equal reduction lengths)";
   }
   return "unknown status";
 }

@@ -8,6 +8,23 @@
 
 namespace qnf4 {
 
+// ------------------------------------------------- host helpers (api.cu)
+struct DevInfo {
+  int ok = 0;
+  int sms = 148;
+};
+int current_device_info(DevInfo* out);
+// 2-D map over a matrix [outer][inner] of `esize`-byte elements, rows
+// `pitch` bytes apart (0: contiguous).
+int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t inner, uint64_t outer,
+             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw, uint64_t pitch = 0);
+// bf16 operand of the engines.  K-major: matrix [mn][k] (k contiguous), box
+// 64 k x `rows` mn.  MN-major: matrix [k][mn] (mn contiguous), box 64 x 64.
+int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows,
+                uint64_t pitch = 0);
+// Takes the pending request of qlora_debug_stall_next_gemm (0: none).
+uint64_t take_stall_request();
+
 // NF4 codebook and decision thresholds as the kernels use them.
 //   q[i] : the 16 levels (fp32), ascending, q[7] = 0 exactly.
 //   t[i] : RD32 of the exact midpoint (q[i] + q[i+1]) / 2; for an fp32 x,
@@ -89,6 +106,7 @@ struct GemmPlan {
   size_t partial_bytes;
 };
 
+int bn_for_cols(int cols);  // token-tile width: the smallest of 16 ... 256 that holds `cols`, else 256
 GemmPlan plan_gemm(int rows, int cols, int kb_main, int num_sms);
 size_t engine_smem_bytes(int BN, int amode);
 cudaError_t launch_engine(const EngineArgs& a, int amode, const GemmPlan& p, cudaStream_t st);
@@ -215,5 +233,65 @@ cudaError_t launch_adapter_merge(const uint8_t* codes, const uint8_t* c2, const 
 // AdamW step; sc = lr, b1, 1-b1, b2, 1-b2, eps, wd, 1-b1^t, 1-b2^t (fp32).
 cudaError_t launch_adamw(float* p, uint16_t* pb, const float* g, float* m, float* v, int64_t n, const float* sc,
                          cudaStream_t st);
+
+// ------------------------------------------------ MXFP4 and dropout kernels
+// Dropout as the kernels take it: keep where the element's 16 random bits are
+// at least `threshold`; `inv` = 65536 / (65536 - threshold).
+struct DropArgs {
+  uint32_t threshold;  // 0: nothing is dropped
+  float inv;
+  uint64_t seed, offset;
+  const uint64_t* offset_dev;  // added to offset when not null
+};
+
+cudaError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                               int* status, cudaStream_t st);
+// X [R][C] -> the MXFP4 form of its transpose [C][R].
+cudaError_t launch_mx_quantize_t(const void* X, int dtype, int64_t R, int64_t C, uint8_t* codes, uint8_t* scales,
+                                 int* status, cudaStream_t st);
+cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int dtype,
+                              void* out, cudaStream_t st);
+cudaError_t launch_dropout(const void* X, int dtype, int64_t n, const DropArgs& d, void* out, cudaStream_t st);
+
+// D[col][row] = sum_k A[row, k] B[col, k] (+ the LoRA term, masked when
+// drop.threshold > 0), A and B in MXFP4.
+struct MxGemmArgs {
+  CUtensorMap tmA;   // codes of A, uint8 [rows][K/2], box 128 x 128, 128-byte swizzle
+  CUtensorMap tmB;   // codes of B, uint8 [cols][K/2], box 128 x BN
+  CUtensorMap tmAx;  // LoRA term: A side, bf16 (K- or MN-major per a_mn_ext)
+  CUtensorMap tmBx;  // LoRA term: B side, bf16 [cols][r], K-major
+  const uint8_t* sfA;  // tiled scales
+  const uint8_t* sfB;
+  int rows, cols;
+  int64_t K;
+  int kt;            // scale tiles along K
+  int kb;            // 256-wide reduction blocks
+  int kb_ext;        // 64-wide reduction blocks of the LoRA term (0: none)
+  int a_mn_ext;
+  void* out;         // [cols][ldo]
+  int64_t ldo;
+  int out_f32;
+  DropArgs drop;     // mask of the LoRA term at element col * ldo + row
+  int* status;
+  uint64_t wait_ns;
+  int stall;
+};
+
+struct MxGemmPlan {
+  int BN;
+  int m_tiles, n_tiles, cluster;
+};
+MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms);
+size_t mx_gemm_smem_bytes(int BN);
+cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st);
+
+// ------------------------------------------- adapter side of the MX linear
+// out[i] = hi, out[i + r] = lo: v = scale * in split into two bf16 terms (the
+// rest of v below 2^-17 of it); in [M][r] fp32, out [M][2r].
+cudaError_t launch_split_hi_lo(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st);
+// out(row, j) = alpha * sum_z (p[z][j][row] + p[z][r + j][row]) with p fp32
+// [splits][2r][rows], stored at out[row * rs + j * cs].
+cudaError_t launch_sum_hi_lo(const float* partial, int splits, int rows, int r, float alpha, float* out, int64_t rs,
+                             int64_t cs, cudaStream_t st);
 
 }  // namespace qnf4

@@ -1,0 +1,383 @@
+// The C ABI of the MXFP4 calls and of dropout (include/qlora_nf4.h):
+// argument checks, tensor maps, workspace layout and launches.
+#include <cmath>
+#include <cstring>
+
+#include "../../include/qlora_nf4.h"
+#include "internal.h"
+
+using namespace qnf4;
+
+namespace {
+
+bool ok16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool all16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!ok16(p)) return false;
+  return true;
+}
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+constexpr int64_t kMaxDim = 1 << 24;
+
+bool mx_shape_ok(int64_t rows, int64_t cols) {
+  return rows >= 1 && cols >= 32 && cols % 32 == 0 && rows <= kMaxDim && cols <= kMaxDim &&
+         ((rows + 127) / 128) * ((cols + 127) / 128) <= 0x7FFFFFFF;
+}
+bool rank_ok(int r) { return r == 0 || (r >= 8 && r <= 128 && r % 8 == 0); }
+bool dtype_ok(int d) { return d == QLORA_DTYPE_BF16 || d == QLORA_DTYPE_F16 || d == QLORA_DTYPE_F32; }
+
+size_t codes_bytes(int64_t rows, int64_t cols) { return (size_t)(rows * (cols / 2)); }
+size_t scales_bytes(int64_t rows, int64_t cols) {
+  return (size_t)((rows + 127) / 128) * (size_t)((cols + 127) / 128) * 512;
+}
+
+// Kernel arguments of a dropout configuration (NULL: none).
+int drop_args(const qlora_dropout_config* c, DropArgs* d) {
+  std::memset(d, 0, sizeof(*d));
+  d->inv = 1.0f;
+  if (!c) return QLORA_OK;
+  if (!(c->p >= 0.0 && c->p < 1.0)) return QLORA_ERR_DROPOUT;
+  const long t = std::lrint(c->p * 65536.0);
+  if (t >= 65536) return QLORA_ERR_DROPOUT;
+  d->threshold = (uint32_t)t;
+  d->inv = (float)(65536.0 / (double)(65536 - t));
+  d->seed = c->seed;
+  d->offset = c->offset;
+  d->offset_dev = c->offset_dev;
+  if (reinterpret_cast<uintptr_t>(c->offset_dev) & 7u) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+// The tensor cores' fp32 accumulation truncates, an error that grows with
+// the length of the sum (measured on normal data: 3.8e-7 of the result after
+// 410 terms, 1.65e-6 after 1638).  The adapter sums are fp32 results, so
+// they run in pieces of at most kAdapterSum terms that are added with
+// rounding.
+constexpr int kAdapterSum = 1024;
+
+GemmPlan plan_adapter(int64_t rows, int cols, int64_t red, int sms) {
+  const int kb = (int)((red + 63) / 64);
+  GemmPlan p = plan_gemm((int)rows, cols, kb, sms);
+  const int need = (int)((red + kAdapterSum - 1) / kAdapterSum);
+  if (p.splits < need) p.splits = need;
+  p.partial_bytes = (size_t)p.splits * (size_t)rows * cols * sizeof(float);
+  return p;
+}
+
+int run_adapter(EngineArgs& a, const GemmPlan& p, float* partial, cudaStream_t st) {
+  a.splits = p.splits;
+  a.partial = partial;
+  return launch_engine(a, A_TMA, p, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+void engine_args(EngineArgs* a, int* status, int64_t rows, int cols, int64_t red) {
+  std::memset(a, 0, sizeof(*a));
+  a->status = status;
+  a->rows = (int)rows;
+  a->cols = cols;
+  a->kb_main = (int)((red + 63) / 64);
+  a->epi.alpha = a->epi.alpha2 = 1.0f;
+}
+
+// Product launch: A = the [rows][K] side on the lanes, B = the [cols][K] side.
+int product(MxGemmArgs& g, const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, const uint8_t* b_codes,
+            const uint8_t* b_scales, int64_t cols, int64_t K, const MxGemmPlan& p, cudaStream_t st) {
+  if (make_map(&g.tmA, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)K / 2, (uint64_t)rows, 128, 128,
+               CU_TENSOR_MAP_SWIZZLE_128B) ||
+      make_map(&g.tmB, b_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)K / 2, (uint64_t)cols, 128, (uint32_t)p.BN,
+               CU_TENSOR_MAP_SWIZZLE_128B))
+    return QLORA_ERR_CUDA;
+  g.sfA = a_scales;
+  g.sfB = b_scales;
+  g.rows = (int)rows;
+  g.cols = (int)cols;
+  g.K = K;
+  g.kt = (int)((K + 127) / 128);
+  g.kb = (int)((K + 255) / 256);
+  g.ldo = rows;
+  if (const uint64_t ns = take_stall_request()) {
+    g.stall = 1;
+    g.wait_ns = ns;
+  }
+  return launch_mx_gemm(g, p, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+// Workspace of the linear layer (offsets in bytes).  Forward and backward use
+// the same regions for their own data:
+//   q      MXFP4 of X (forward) or dY (backward): codes, then scales
+//   t      fp32 [M][r]: dT (backward)
+//   u, v   bf16 [M][2r]: hi | lo of the scaled dT (u) and of s T (v); the
+//          forward keeps RNbf16(s T) in u
+//   xm     bf16 [M][K]: X with the dropped elements zeroed
+//   part   fp32 partial sums of the adapter products
+struct MxWs {
+  size_t q_scales, t, u, v, xm, part, total;
+  GemmPlan t_fwd, dt, dl1, dl2;
+};
+
+MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, bool drop, int sms) {
+  MxWs w{};
+  const size_t qk = up256(codes_bytes(M, K)), qn = up256(codes_bytes(M, N));
+  w.q_scales = qk > qn ? qk : qn;
+  const size_t sk = up256(scales_bytes(M, K)), sn = up256(scales_bytes(M, N));
+  size_t o = w.q_scales + (sk > sn ? sk : sn);
+  if (r) {
+    w.t = o;
+    o += up256((size_t)M * r * 4);
+    w.u = o;
+    o += up256((size_t)M * r * 4);
+    w.v = o;
+    o += up256((size_t)M * r * 4);
+    w.xm = o;
+    if (drop) o += up256((size_t)M * K * 2);
+    w.part = o;
+    w.t_fwd = plan_adapter(M, r, K, sms);
+    w.dt = plan_adapter(M, r, N, sms);
+    w.dl1 = plan_adapter(K, 2 * r, M, sms);
+    w.dl2 = plan_adapter(N, 2 * r, M, sms);
+    size_t part = 0;
+    for (const GemmPlan* p : {&w.t_fwd, &w.dt, &w.dl1, &w.dl2})
+      part = p->partial_bytes > part ? p->partial_bytes : part;
+    o += up256(part);
+  }
+  w.total = o;
+  return w;
+}
+
+bool linear_shape_ok(int64_t M, int64_t N, int64_t K, int64_t n_mult) {
+  return M >= 1 && M <= kMaxDim && N >= n_mult && N % n_mult == 0 && N <= kMaxDim && mx_shape_ok(M, K) &&
+         mx_shape_ok(N, K);
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_mx_storage_bytes(int64_t rows, int64_t cols, size_t* cb, size_t* sb) {
+  if (!mx_shape_ok(rows, cols)) return QLORA_ERR_MX_SHAPE;
+  if (cb) *cb = codes_bytes(rows, cols);
+  if (sb) *sb = scales_bytes(rows, cols);
+  return QLORA_OK;
+}
+
+int qlora_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int transpose,
+                      const qlora_mx_tensor* out, int* status_dev, qlora_stream_t stream) {
+  if (!X || !out || !out->codes || !out->scales) return QLORA_ERR_NULL;
+  if (!dtype_ok(dtype)) return QLORA_ERR_DTYPE;
+  if (!(transpose ? mx_shape_ok(cols, rows) && cols % 8 == 0 : mx_shape_ok(rows, cols))) return QLORA_ERR_MX_SHAPE;
+  if (!all16({X, out->codes, out->scales})) return QLORA_ERR_ALIGN;
+  DevInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = transpose
+                            ? launch_mx_quantize_t(X, dtype, rows, cols, out->codes, out->scales, status_dev, st)
+                            : launch_mx_quantize(X, dtype, rows, cols, out->codes, out->scales, status_dev, st);
+  return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+int qlora_mx_dequant(const qlora_mx_tensor* t, void* out, int dtype, qlora_stream_t stream) {
+  if (!t || !t->codes || !t->scales || !out) return QLORA_ERR_NULL;
+  if (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_F32) return QLORA_ERR_DTYPE;
+  if (!mx_shape_ok(t->rows, t->cols)) return QLORA_ERR_MX_SHAPE;
+  if (!all16({t->codes, t->scales, out})) return QLORA_ERR_ALIGN;
+  DevInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return launch_mx_dequant(t->codes, t->scales, t->rows, t->cols, dtype, out, st) == cudaSuccess ? QLORA_OK
+                                                                                                 : QLORA_ERR_CUDA;
+}
+
+int qlora_mx_matmul(const qlora_mx_tensor* a, const qlora_mx_tensor* b, void* out, int dtype, int* status_dev,
+                    qlora_stream_t stream) {
+  if (!a || !b || !a->codes || !a->scales || !b->codes || !b->scales || !out) return QLORA_ERR_NULL;
+  if (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_F32) return QLORA_ERR_DTYPE;
+  if (a->cols != b->cols || !linear_shape_ok(a->rows, b->rows, a->cols, 8)) return QLORA_ERR_MX_SHAPE;
+  if (!all16({a->codes, a->scales, b->codes, b->scales, out})) return QLORA_ERR_ALIGN;
+  DevInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  MxGemmArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.out = out;
+  g.out_f32 = dtype == QLORA_DTYPE_F32;
+  g.status = status_dev;
+  return product(g, b->codes, b->scales, b->rows, a->codes, a->scales, a->rows, a->cols,
+                 plan_mx_gemm(b->rows, a->rows, a->cols, di.sms), reinterpret_cast<cudaStream_t>(stream));
+}
+
+int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_config* cfg, void* out,
+                  qlora_stream_t stream) {
+  if (!X || !cfg || !out) return QLORA_ERR_NULL;
+  if (!dtype_ok(dtype)) return QLORA_ERR_DTYPE;
+  if (n < 0) return QLORA_ERR_SHAPE;
+  DropArgs d;
+  if (int rc = drop_args(cfg, &d)) return rc;
+  if (!all16({X, out})) return QLORA_ERR_ALIGN;
+  if (n == 0) return QLORA_OK;
+  DevInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  return launch_dropout(X, dtype, n, d, out, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QLORA_OK
+                                                                                                    : QLORA_ERR_CUDA;
+}
+
+size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int dropout) {
+  if (!linear_shape_ok(M, N, K, 8) || !rank_ok(r)) return 0;
+  DevInfo di;
+  if (current_device_info(&di)) di.sms = 148;
+  return mx_ws(M, N, K, r, dropout != 0, di.sms).total;
+}
+
+int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, const uint16_t* L1,
+                        const uint16_t* L2, int r, float s, const qlora_dropout_config* drop, uint16_t* Y,
+                        float* T_save, void* ws, size_t ws_bytes, int* status_dev, qlora_stream_t stream) {
+  if (!X || !w || !w->codes || !w->scales || !Y || !ws) return QLORA_ERR_NULL;
+  if (!rank_ok(r)) return QLORA_ERR_RANK;
+  if (r && (!L1 || !L2 || !T_save)) return QLORA_ERR_NULL;
+  const int64_t N = w->rows, K = w->cols;
+  if (!linear_shape_ok(M, N, K, 8)) return QLORA_ERR_MX_SHAPE;
+  DropArgs d;
+  if (int rc = drop_args(drop, &d)) return rc;
+  if (!all16({X, w->codes, w->scales, L1, L2, Y, T_save, ws})) return QLORA_ERR_ALIGN;
+  DevInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  const bool masked = r && d.threshold;
+  const MxWs lay = mx_ws(M, N, K, r, masked, di.sms);
+  if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  uint16_t* sT = reinterpret_cast<uint16_t*>(wb + lay.u);
+
+  if (launch_mx_quantize(X, QLORA_DTYPE_BF16, M, K, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  const MxGemmPlan p = plan_mx_gemm(N, M, K, di.sms);
+  MxGemmArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.out = Y;
+  g.status = status_dev;
+  if (r) {
+    const uint16_t* Xa = X;  // the adapter's input, its dropped elements zero (the scale goes on T)
+    if (masked) {
+      DropArgs d1 = d;
+      d1.inv = 1.0f;
+      uint16_t* xm = reinterpret_cast<uint16_t*>(wb + lay.xm);
+      if (launch_dropout(X, QLORA_DTYPE_BF16, M * K, d1, xm, st) != cudaSuccess) return QLORA_ERR_CUDA;
+      Xa = xm;
+    }
+    EngineArgs a;
+    engine_args(&a, status_dev, M, r, K);
+    const GemmPlan& pt = lay.t_fwd;
+    if (map_operand(&a.tmA, Xa, 0, M, K, 128) || map_operand(&a.tmB, L1, 1, r, K, pt.BN)) return QLORA_ERR_CUDA;
+    a.b_mn_main = 1;
+    a.epi.out = T_save;
+    a.epi.alpha = d.inv;
+    a.epi.rs = r;
+    a.epi.cs = 1;
+    a.epi.out2 = sT;
+    a.epi.alpha2 = s * d.inv;
+    a.epi.rs2 = r;
+    a.epi.cs2 = 1;
+    float* part = reinterpret_cast<float*>(wb + lay.part);
+    if (int rc = run_adapter(a, pt, part, st)) return rc;
+    if (pt.splits > 1 && launch_split_reduce(part, pt.splits, a.rows, a.cols, a.epi, st) != cudaSuccess)
+      return QLORA_ERR_CUDA;
+    if (map_operand(&g.tmAx, L2, 1, N, r, 128) || map_operand(&g.tmBx, sT, 0, M, r, p.BN)) return QLORA_ERR_CUDA;
+    g.kb_ext = (r + 63) / 64;
+    g.a_mn_ext = 1;
+  }
+  return product(g, w->codes, w->scales, N, wb, wb + lay.q_scales, M, K, p, st);
+}
+
+int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const float* T_saved,
+                        const qlora_mx_tensor* wt, int64_t N, int64_t K, const uint16_t* L1, const uint16_t* L2,
+                        int r, float s, const qlora_dropout_config* drop, uint16_t* dX, float* dL1, float* dL2,
+                        void* ws, size_t ws_bytes, int* status_dev, qlora_stream_t stream) {
+  if (!dY || !ws) return QLORA_ERR_NULL;
+  if (!rank_ok(r)) return QLORA_ERR_RANK;
+  if (dX && (!wt || !wt->codes || !wt->scales)) return QLORA_ERR_NULL;
+  if (!r && (dL1 || dL2)) return QLORA_ERR_RANK;
+  if (r && (!L1 || !L2 || (dL1 && !X) || (dL2 && !T_saved))) return QLORA_ERR_NULL;
+  if (!linear_shape_ok(M, N, K, 32)) return QLORA_ERR_MX_SHAPE;
+  if (dX && (wt->rows != K || wt->cols != N)) return QLORA_ERR_MX_SHAPE;
+  DropArgs d;
+  if (int rc = drop_args(drop, &d)) return rc;
+  if (!all16({dY, X, T_saved, L1, L2, dX, dL1, dL2, ws})) return QLORA_ERR_ALIGN;
+  if (dX && !all16({wt->codes, wt->scales})) return QLORA_ERR_ALIGN;
+  DevInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  const bool masked = r && d.threshold;
+  const MxWs lay = mx_ws(M, N, K, r, masked, di.sms);
+  if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  float* dT = reinterpret_cast<float*>(wb + lay.t);
+  uint16_t* sdT = reinterpret_cast<uint16_t*>(wb + lay.u);
+  uint16_t* sT = reinterpret_cast<uint16_t*>(wb + lay.v);
+  float* part = reinterpret_cast<float*>(wb + lay.part);
+
+  // dT = dY.L2^T, then s dT / (1 - p) as two bf16 terms [hi | lo]
+  if (r && (dX || dL1)) {
+    EngineArgs a;
+    engine_args(&a, status_dev, M, r, N);
+    const GemmPlan& p = lay.dt;
+    if (map_operand(&a.tmA, dY, 0, M, N, 128) || map_operand(&a.tmB, L2, 0, r, N, p.BN)) return QLORA_ERR_CUDA;
+    a.epi.out = dT;
+    a.epi.rs = r;
+    a.epi.cs = 1;
+    if (int rc = run_adapter(a, p, part, st)) return rc;
+    if (p.splits > 1 && launch_split_reduce(part, p.splits, a.rows, a.cols, a.epi, st) != cudaSuccess)
+      return QLORA_ERR_CUDA;
+    if (launch_split_hi_lo(dT, M, r, s * d.inv, sdT, st) != cudaSuccess) return QLORA_ERR_CUDA;
+  }
+  if (dX) {
+    if (launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess)
+      return QLORA_ERR_CUDA;
+    const MxGemmPlan p = plan_mx_gemm(K, M, N, di.sms);
+    MxGemmArgs g;
+    std::memset(&g, 0, sizeof(g));
+    g.out = dX;
+    g.status = status_dev;
+    if (r) {
+      if (map_operand(&g.tmAx, L1, 0, K, r, 128) || map_operand(&g.tmBx, sdT, 0, M, r, p.BN, (uint64_t)r * 4))
+        return QLORA_ERR_CUDA;
+      g.kb_ext = (r + 63) / 64;
+      g.drop = d;
+    }
+    if (int rc = product(g, wt->codes, wt->scales, K, wb, wb + lay.q_scales, M, N, p, st)) return rc;
+  }
+  if (dL1) {
+    const uint16_t* Xa = X;
+    if (masked) {
+      DropArgs d1 = d;
+      d1.inv = 1.0f;
+      uint16_t* xm = reinterpret_cast<uint16_t*>(wb + lay.xm);
+      if (launch_dropout(X, QLORA_DTYPE_BF16, M * K, d1, xm, st) != cudaSuccess) return QLORA_ERR_CUDA;
+      Xa = xm;
+    }
+    EngineArgs a;
+    engine_args(&a, status_dev, K, 2 * r, M);
+    const GemmPlan& p = lay.dl1;
+    if (map_operand(&a.tmA, Xa, 1, K, M, 128) || map_operand(&a.tmB, sdT, 1, 2 * r, M, p.BN)) return QLORA_ERR_CUDA;
+    a.a_mn_main = a.b_mn_main = 1;
+    a.epi.out = part;  // one split: the same [2r][rows] layout
+    a.epi.rs = 1;
+    a.epi.cs = K;
+    if (int rc = run_adapter(a, p, part, st)) return rc;
+    if (launch_sum_hi_lo(part, p.splits, (int)K, r, 1.0f, dL1, r, 1, st) != cudaSuccess) return QLORA_ERR_CUDA;
+  }
+  if (dL2) {
+    if (launch_split_hi_lo(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    EngineArgs a;
+    engine_args(&a, status_dev, N, 2 * r, M);
+    const GemmPlan& p = lay.dl2;
+    if (map_operand(&a.tmA, dY, 1, N, M, 128) || map_operand(&a.tmB, sT, 1, 2 * r, M, p.BN)) return QLORA_ERR_CUDA;
+    a.a_mn_main = a.b_mn_main = 1;
+    a.epi.out = part;
+    a.epi.rs = 1;
+    a.epi.cs = N;
+    if (int rc = run_adapter(a, p, part, st)) return rc;
+    if (launch_sum_hi_lo(part, p.splits, (int)N, r, 1.0f, dL2, 1, N, st) != cudaSuccess) return QLORA_ERR_CUDA;
+  }
+  return QLORA_OK;
+}
+
+}  // extern "C"

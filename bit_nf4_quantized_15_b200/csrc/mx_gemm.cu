@@ -1,0 +1,429 @@
+// Product of two MXFP4 matrices on the block-scaled tensor cores.
+//
+//   out[col, row] = RN( sum_k A^[row, k] B^[col, k] + mask sum_j Ax[row, j] Bx[col, j] )
+//
+// tcgen05.mma kind::mxf4 takes the 4-bit codes as they are stored, 64 of them
+// a step, and multiplies each 32-block's exact product sum by both E8M0
+// scales in the MMA; the accumulator is fp32 in tensor memory.  So nothing is
+// dequantised: codes and scales go HBM -> shared memory by TMA, the scales
+// on to tensor memory by tcgen05.cp, and the loop has no arithmetic of its
+// own.  The optional second sum is the LoRA term (bf16, kind::f16) of the
+// linear layer; it is formed first, so that it can be masked by the dropout
+// of the adapter path in tensor memory before the main sum is added to it.
+//
+// This kernel gives a 128 (rows) x BN (cols) tile to a cluster of 1, 2, 4 or
+// 8 CTAs that split the reduction; the partial tiles meet through distributed
+// shared memory and are added in rank order, so results do not depend on
+// timing and no workspace is needed.  A is the side with more rows to give
+// (the weight), B the tokens: with few tokens BN shrinks to 16 and a call
+// streams the weight once through all SMs.
+//
+// Roles: warp 0 TMA producer, warp 1 MMA issuer, then 4 epilogue warps (8 for
+// BN >= 128).
+#include "engine_util.cuh"
+#include "philox.cuh"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kMxKB = 256;  // reduction elements of a stage: 128 bytes of codes
+
+template <int BN>
+struct MxCfg {
+  static constexpr int S = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 4 : 5;  // stages
+  static constexpr int EW = BN >= 128 ? 8 : 4;                                 // epilogue warps
+  static constexpr int THREADS = 64 + 32 * EW;
+  static constexpr int A = 16384;                      // 128 rows x 128 bytes
+  static constexpr int B = BN * 128;
+  static constexpr int FB = BN > 128 ? 2 : 1;          // B scale tiles (128 rows each)
+  static constexpr int STAGE = A + B + 1024 + FB * 1024;
+  static constexpr int BAR = S * STAGE;
+  static constexpr int TOTAL = BAR + 256 + 1024;       // barriers + alignment slack
+  static constexpr uint32_t ACC = BN < 32 ? 32 : BN;   // accumulator columns
+  static constexpr uint32_t SF = 8 + 8 * FB;           // scale columns of a stage: A, then B
+  static constexpr uint32_t NEED = ACC + S * SF;
+  static constexpr uint32_t COLS = NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
+  static_assert(NEED <= 512 && STAGE % 1024 == 0 && TOTAL <= 232448 && BN * 512 <= S * STAGE, "budget");
+};
+
+// Instruction descriptor, kind::mxf4: E2M1 x E2M1, E8M0 scales; the scale ids
+// pick bytes 0-1 or 2-3 of each scale column word (two 32-blocks a step).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf_id) {
+  return ((uint32_t)sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 7) << 27) | ((uint32_t)sf_id << 29);
+}
+QDEV void umma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      : "memory");
+}
+// One scale tile (512 bytes: 32 lanes x 16 bytes, repeated to the four lane
+// quarters) from shared to tensor memory: 4 columns.
+QDEV void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Unswizzled matrix of 16-byte rows, 8-row groups 128 bytes apart.
+QDEV uint64_t sdesc_scales(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
+}
+QDEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+QDEV uint32_t mx_cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+QDEV uint32_t mx_cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+QDEV void mx_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+QDEV float2 ld_peer_f2(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// Zero the dropped entries of this warp's 32 lanes x 16 columns of the LoRA
+// term.  Lanes are consecutive output rows (elements), so 8 lanes share one
+// generator evaluation per column: lane l evaluates column c + (l & 7) for
+// its group of 8 and the byte is shuffled to the lane that needs it.
+QDEV void mask_chunk(uint32_t (&v)[16], const MxGemmArgs& a, const PhiloxKey& key, int row_base, int col, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t m = (int64_t)col + 8 * h + (lane & 7);
+    const uint32_t byte = keep8((uint64_t)(m * a.ldo + row_base + (lane & ~7)) >> 3, key, a.drop.threshold);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = __shfl_sync(0xFFFFFFFFu, byte, (lane & ~7) | j);
+      if (!((b >> (lane & 7)) & 1u)) v[8 * h + j] = 0u;
+    }
+  }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __grid_constant__ MxGemmArgs args) {
+  using C = MxCfg<BN>;
+  constexpr int kS = C::S;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR);
+  uint64_t* empty = full + kS;
+  uint64_t* ext_done = empty + kS;    // the LoRA term is in tensor memory
+  uint64_t* ext_masked = ext_done + 1;  // ... and masked
+  uint64_t* accum = ext_masked + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)mx_cluster_rank(), csize = (int)mx_cluster_size();
+  const int id = (int)(blockIdx.x / (unsigned)csize);
+  const int n_tiles = (args.cols + BN - 1) / BN;
+  const int row_tile = id / n_tiles, col_tile = id % n_tiles;
+  const int row0 = row_tile * 128, col0 = col_tile * BN;
+  const int kb_lo = (int)((int64_t)rank * args.kb / csize), kb_hi = (int)((int64_t)(rank + 1) * args.kb / csize);
+  const int n_ext = rank == 0 ? args.kb_ext : 0;
+  const int n_iters = n_ext + kb_hi - kb_lo;
+  const bool masked = n_ext && args.drop.threshold;
+  const uint64_t lim = args.wait_ns ? args.wait_ns : QNF4_WAIT_NS;
+
+  if (tid == 0) {
+    for (int s = 0; s < kS; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(ext_done, 1);
+    mbar_init(ext_masked, C::EW);
+    mbar_init(accum, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&args.tmA);
+    tma_prefetch_desc(&args.tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool committed = false;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0 && !args.stall) {
+      for (int it = 0; it < n_iters; ++it) {
+        const int s = it % kS;
+        if (!mbar_wait(empty + s, ((uint32_t)(it / kS) & 1u) ^ 1u, abort_flag, args.status, lim)) break;
+        uint8_t* sa = smem + s * C::STAGE;
+        uint8_t* sb = sa + C::A;
+        if (it < n_ext) {
+          mbar_arrive_expect_tx(full + s, tx_bytes(args.a_mn_ext, 128) + tx_bytes(0, BN));
+          load_operand(sa, &args.tmAx, full + s, args.a_mn_ext, row0, it * 64, 128);
+          load_operand(sb, &args.tmBx, full + s, 0, col0, it * 64, BN);
+        } else {
+          const int kb = kb_lo + it - n_ext;
+          const int nt = min(2, args.kt - 2 * kb);  // scale tiles along K of this stage
+          uint8_t* sfa = sb + C::B;
+          uint8_t* sfb = sfa + 1024;
+          const int nb = C::FB == 2 && col0 + 128 < args.cols ? 2 : 1;
+          const uint32_t sbytes = 512u * (uint32_t)nt;
+          mbar_arrive_expect_tx(full + s, (uint32_t)C::A + (uint32_t)C::B + sbytes * (1u + (uint32_t)nb));
+          tma_load_2d(sa, &args.tmA, full + s, kb * 128, row0);
+          tma_load_2d(sb, &args.tmB, full + s, kb * 128, col0);
+          bulk_load(sfa, args.sfA + ((int64_t)(row0 >> 7) * args.kt + 2 * kb) * 512, sbytes, full + s);
+          for (int j = 0; j < nb; ++j)
+            bulk_load(sfb + 1024 * j, args.sfB + ((int64_t)((col0 >> 7) + j) * args.kt + 2 * kb) * 512, sbytes,
+                      full + s);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      const uint32_t id_ext = idesc_bf16(128, BN, args.a_mn_ext, 0);
+      for (int it = 0; it < n_iters; ++it) {
+        const int s = it % kS;
+        if (!mbar_wait(full + s, (uint32_t)(it / kS) & 1u, abort_flag, args.status, lim)) break;
+        tc_fence_after();
+        const uint8_t* sa = smem + s * C::STAGE;
+        const uint8_t* sb = sa + C::A;
+        if (it < n_ext) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem, operand_desc(sa, args.a_mn_ext, kk), operand_desc(sb, 0, kk), id_ext, (it | kk) != 0);
+          umma_commit(empty + s);
+          if (it == n_ext - 1) {
+            // MMAs of another kind follow: let these finish (and be masked)
+            umma_commit(ext_done);
+            if (!mbar_wait(masked ? ext_masked : ext_done, 0, abort_flag, args.status, lim)) break;
+            tc_fence_after();
+          }
+          continue;
+        }
+        const int64_t left = args.K - (int64_t)(kb_lo + it - n_ext) * kMxKB;
+        const int steps = left >= kMxKB ? 4 : (int)((left + 63) / 64);
+        const uint32_t sf = tmem + C::ACC + (uint32_t)s * C::SF;  // this stage's scale columns
+        const uint32_t ssf = smem_u32(sb + C::B);
+        // A stage's scale columns are free again with the stage: its barrier
+        // says that the MMAs that read them have finished.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (2 * h >= steps) break;
+          tmem_cp_scales(sf + 4 * h, sdesc_scales(ssf + 512 * h));
+#pragma unroll
+          for (int j = 0; j < C::FB; ++j)
+            tmem_cp_scales(sf + 8 + 4 * (C::FB * h + j), sdesc_scales(ssf + 1024 + 1024 * j + 512 * h));
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk >= steps) break;
+          umma_mxf4(tmem, operand_desc(sa, 0, kk), operand_desc(sb, 0, kk), idesc_mxf4(128, BN, 2 * (kk & 1)),
+                    sf + 4 * (kk >> 1), sf + 8 + 4 * C::FB * (kk >> 1), (it | kk) != 0);
+        }
+        umma_commit(empty + s);
+      }
+      umma_commit(accum);
+      committed = true;
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q4 = warp & 3, grp = (warp - 2) >> 2;
+    constexpr int G = C::EW / 4;
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    const int row = row0 + q4 * 32 + lane;
+    if (masked) {
+      const PhiloxKey key = philox_key(args.drop);
+      if (warp_wait(ext_done, 0, abort_flag, args.status, lane, lim)) {
+        tc_fence_after();
+        for (int c = grp * 16; c < BN; c += G * 16) {
+          uint32_t v[16];
+          tmem_ld16(tl + (uint32_t)c, v);
+          tmem_wait_ld();
+          mask_chunk(v, args, key, row0 + q4 * 32, col0 + c, lane);
+          tmem_st16(tl + (uint32_t)c, v);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ext_masked);
+    }
+    const bool ok = warp_wait(accum, 0, abort_flag, args.status, lane, lim);
+    tc_fence_after();
+    for (int c = grp * 16; c < BN; c += G * 16) {
+      uint32_t v[16];
+      tmem_ld16(tl + (uint32_t)c, v);
+      tmem_wait_ld();
+      if (csize > 1) {  // this CTA's partial tile, over the stages (all read by now)
+        float* red = reinterpret_cast<float*>(smem) + c * 128 + q4 * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) red[j * 128] = __uint_as_float(v[j]);
+        continue;
+      }
+      if (!ok || *abort_flag || row >= args.rows) continue;
+      const int ncol = min(16, args.cols - (col0 + c));
+      const int64_t o = (int64_t)(col0 + c) * args.ldo + row;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (j >= ncol) continue;
+        if (args.out_f32) reinterpret_cast<float*>(args.out)[o + j * args.ldo] = __uint_as_float(v[j]);
+        else reinterpret_cast<__nv_bfloat16*>(args.out)[o + j * args.ldo] = __float2bfloat16_rn(__uint_as_float(v[j]));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // Error path: let MMAs and loads still in flight finish before shared and
+    // tensor memory are given back.
+    if (warp == 1 && lane == 0 && committed) mbar_wait_drain(accum, 0, 10000000ull);
+    if (tid == 0) {
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 2000000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::COLS);
+  }
+  if (csize > 1) {
+    mx_cluster_sync();  // every partial tile is in place
+    const int per = (BN + csize - 1) / csize;
+    const int c0 = rank * per, nc = min(per, BN - c0);
+    const uint32_t red = smem_u32(smem);
+    const bool good = !*abort_flag;
+    for (int i = tid; i < nc * 64; i += C::THREADS) {
+      const int c = c0 + (i >> 6), rp = (i & 63) * 2;
+      if (!good || col0 + c >= args.cols || row0 + rp >= args.rows) continue;
+      float2 acc = ld_peer_f2(red + (uint32_t)(c * 128 + rp) * 4u, 0);
+      for (int p = 1; p < csize; ++p) {
+        const float2 v = ld_peer_f2(red + (uint32_t)(c * 128 + rp) * 4u, (uint32_t)p);
+        acc.x += v.x;
+        acc.y += v.y;
+      }
+      const int64_t o = (int64_t)(col0 + c) * args.ldo + row0 + rp;
+      if (args.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(args.out) + o) = acc;
+      else *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(args.out) + o) = pack_bf16x2(acc.x, acc.y);
+    }
+    mx_cluster_sync();  // peers may still be reading this CTA's tile
+  }
+}
+
+template <int BN>
+cudaError_t launch_bn(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st) {
+  using C = MxCfg<BN>;
+  auto kern = mx_gemm_kernel<BN>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.m_tiles * p.n_tiles * p.cluster));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::TOTAL;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, kern, a);
+  if (err != cudaSuccess) return err;
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------ adapter-side small kernels
+__global__ void split_hi_lo_kernel(const float* __restrict__ in, int64_t n, int r, float scale,
+                                   __nv_bfloat16* __restrict__ out) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t m = i / r;
+    const float v = __fmul_rn(in[i], scale);
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    out[i + m * r] = hi;
+    out[i + m * r + r] = __float2bfloat16_rn(__fsub_rn(v, __bfloat162float(hi)));
+  }
+}
+
+__global__ void sum_hi_lo_kernel(const float* __restrict__ p, int splits, int rows, int r, float alpha,
+                                 float* __restrict__ out, int64_t rs, int64_t cs) {
+  const int64_t n = (int64_t)rows * r;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i % rows, j = i / rows;
+    float hi = 0.0f, lo = 0.0f;
+    for (int z = 0; z < splits; ++z) {
+      hi += p[((int64_t)z * 2 * r + j) * rows + row];
+      lo += p[((int64_t)z * 2 * r + r + j) * rows + row];
+    }
+    out[row * rs + j * cs] = __fmul_rn(alpha, hi + lo);
+  }
+}
+
+}  // namespace
+
+MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms) {
+  MxGemmPlan p{};
+  p.BN = bn_for_cols((int)(cols < 256 ? cols : 256));
+  p.m_tiles = (int)((rows + 127) / 128);
+  p.n_tiles = (int)((cols + p.BN - 1) / p.BN);
+  const int kb = (int)((K + kMxKB - 1) / kMxKB);
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+  const int64_t slots = (int64_t)num_sms * (p.BN <= 64 ? 2 : 1);
+  p.cluster = 1;
+  while (p.cluster < 8 && tiles * p.cluster * 2 <= slots && 2 * p.cluster <= kb) p.cluster *= 2;
+  return p;
+}
+
+size_t mx_gemm_smem_bytes(int BN) {
+  return BN >= 256 ? MxCfg<256>::TOTAL : BN >= 128 ? MxCfg<128>::TOTAL : BN >= 64 ? MxCfg<64>::TOTAL
+         : BN >= 32 ? MxCfg<32>::TOTAL : MxCfg<16>::TOTAL;
+}
+
+cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st) {
+  switch (p.BN) {
+    case 16: return launch_bn<16>(a, p, st);
+    case 32: return launch_bn<32>(a, p, st);
+    case 64: return launch_bn<64>(a, p, st);
+    case 128: return launch_bn<128>(a, p, st);
+    case 256: return launch_bn<256>(a, p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+static int small_grid(int64_t n) {
+  const int64_t want = (n + 255) / 256;
+  return (int)(want < 2368 ? (want > 0 ? want : 1) : 2368);
+}
+
+cudaError_t launch_split_hi_lo(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {
+  split_hi_lo_kernel<<<small_grid(M * r), 256, 0, st>>>(in, M * r, r, scale, reinterpret_cast<__nv_bfloat16*>(out));
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_sum_hi_lo(const float* partial, int splits, int rows, int r, float alpha, float* out, int64_t rs,
+                             int64_t cs, cudaStream_t st) {
+  sum_hi_lo_kernel<<<small_grid((int64_t)rows * r), 256, 0, st>>>(partial, splits, rows, r, alpha, out, rs, cs);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace qnf4

@@ -1,0 +1,337 @@
+"""Microscaled 4-bit floating point (MXFP4) and counter-based dropout: binding.
+
+MXFP4 is the 4-bit format the sm_100 tensor cores multiply natively: E2M1
+codes and one power-of-two scale for each 32 elements of a row.
+
+    w = mx_weight(W)                                   # W^ for the forward, W^T's form for the backward
+    Y, T = mx_linear_fwd(X, w, L1, L2, s, dropout=Dropout(0.1, seed, offset))
+    dX, dL1, dL2 = mx_linear_bwd(dY, X, T, w, L1, L2, s, dropout=Dropout(0.1, seed, offset))
+    C = mx_matmul(mx_quantize(A), mx_quantize(B))      # A.B^T, both sides in 4 bits
+
+Calls are asynchronous on the current stream of their tensors' device and do
+not depend on which device is current.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+import bit_nf4_quantized_15_b200 as _q
+
+__all__ = ["MXTensor", "MXWeight", "Dropout", "mx_storage_bytes", "mx_quantize", "mx_dequant", "mx_matmul", "mx_weight",
+           "mx_linear_fwd", "mx_linear_bwd", "mx_linear_workspace_bytes", "dropout"]
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_U64 = (1 << 64) - 1
+
+
+class qlora_mx_tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
+class qlora_dropout_config(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("offset_dev", ctypes.c_void_p)]
+
+
+_P, _I64, _INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+_T, _D, _SZ = ctypes.POINTER(qlora_mx_tensor), ctypes.POINTER(qlora_dropout_config), ctypes.c_size_t
+SIGS = {
+    "qlora_mx_storage_bytes": (_INT, [_I64, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]),
+    "qlora_mx_quantize": (_INT, [_P, _INT, _I64, _I64, _INT, _T, _P, _P]),
+    "qlora_mx_dequant": (_INT, [_T, _P, _INT, _P]),
+    "qlora_mx_matmul": (_INT, [_T, _T, _P, _INT, _P, _P]),
+    "qlora_dropout": (_INT, [_P, _INT, _I64, _D, _P, _P]),
+    "qlora_mx_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT, _INT]),
+    "qlora_mx_linear_fwd": (_INT, [_P, _I64, _T, _P, _P, _INT, ctypes.c_float, _D, _P, _P, _P, _SZ, _P, _P]),
+    "qlora_mx_linear_bwd": (_INT, [_P, _P, _I64, _P, _T, _I64, _I64, _P, _P, _INT, ctypes.c_float, _D, _P, _P, _P, _P,
+                                   _SZ, _P, _P]),
+}
+
+
+def _need(ok, what):
+    if not ok:
+        raise _q.QLoRAError(what)
+
+
+def _tensor(t, name, shape, dtype, device):
+    """`t` is a contiguous tensor of this shape, type and device."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dtype == dtype
+          and tuple(t.shape) == tuple(shape) and t.device == device,
+          f"{name} must be a contiguous {str(dtype).removeprefix('torch.')} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _matrix(t, name, dtypes):
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.is_contiguous() and t.dtype in dtypes,
+          f"{name} must be a contiguous CUDA matrix of "
+          + " or ".join(str(d).removeprefix("torch.") for d in dtypes))
+    return t
+
+
+class _on:
+    """Makes a device current for a call that launches on it."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _status_ptr(status, device):
+    return (status if status is not None else _q._status(device)).data_ptr()
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def mx_storage_bytes(rows: int, cols: int):
+    """(codes, scales) bytes of an MXFP4 matrix: 4.25 bits an element, the
+    scales padded to tiles of 128 x 128."""
+    a, b = _SZ(), _SZ()
+    _q._check(_q.lib().qlora_mx_storage_bytes(rows, cols, ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
+@dataclass
+class MXTensor:
+    """An MXFP4 matrix [rows, cols]: codes uint8 [rows * cols / 2] and tiled
+    E8M0 scales uint8 (layout: qlora_mx_tensor in include/qlora_nf4.h)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+
+    @staticmethod
+    def empty(rows: int, cols: int, device="cuda") -> "MXTensor":
+        nc, ns = mx_storage_bytes(rows, cols)
+        return MXTensor(torch.empty(nc, dtype=torch.uint8, device=device),
+                        torch.empty(ns, dtype=torch.uint8, device=device), rows, cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def descriptor(self) -> qlora_mx_tensor:
+        c, s, dev = self.codes, self.scales, self.codes.device
+        tiles = ((self.rows + 127) // 128) * ((self.cols + 127) // 128)
+        _need(c.is_cuda and c.dtype == torch.uint8 and s.dtype == torch.uint8 and s.device == dev
+              and c.is_contiguous() and s.is_contiguous() and 2 * c.numel() >= self.rows * self.cols
+              and s.numel() >= 512 * tiles,
+              f"codes and scales must be contiguous uint8 tensors on one device that hold {self.rows} x {self.cols}")
+        return qlora_mx_tensor(c.data_ptr(), s.data_ptr(), self.rows, self.cols)
+
+
+@dataclass
+class MXWeight:
+    """A frozen weight [N, K] in MXFP4: ``fwd`` quantised along K for
+    X.W^T, ``bwd`` (its transpose [K, N], quantised along N) for dY.W."""
+    fwd: MXTensor
+    bwd: MXTensor | None = None
+
+
+@dataclass
+class Dropout:
+    """Dropout of probability p from the counter-based generator; (seed,
+    offset) names the mask.  ``offset`` may be an int64 CUDA tensor of one
+    element, read when the kernel runs (advance it between the replays of a
+    captured graph)."""
+    p: float
+    seed: int
+    offset: int | torch.Tensor = 0
+
+    def config(self, device) -> qlora_dropout_config:
+        off, dev_ptr = self.offset, None
+        if isinstance(off, torch.Tensor):
+            _tensor(off.reshape(-1), "offset", (1,), torch.int64, device)
+            off, dev_ptr = 0, off.data_ptr()
+        _need(0 <= self.seed <= _U64 and 0 <= off <= _U64, "seed and offset must be 64-bit unsigned integers")
+        return qlora_dropout_config(float(self.p), int(self.seed), int(off), dev_ptr)
+
+
+def mx_quantize(X, transpose: bool = False, out: MXTensor | None = None, status=None) -> MXTensor:
+    """MXFP4 form of a bf16, fp16 or fp32 CUDA matrix [R, C], blocks of 32
+    along its rows (C % 32 == 0); ``transpose``: of X^T, [C, R] (R % 32 == 0,
+    C % 8 == 0)."""
+    _matrix(X, "X", DTYPES)
+    R, C = X.shape
+    shape = (C, R) if transpose else (R, C)
+    if out is None:
+        out = MXTensor.empty(*shape, device=X.device)
+    _need((out.rows, out.cols) == shape and out.device == X.device, f"out must be {shape[0]} x {shape[1]} on {X.device}")
+    d = out.descriptor()
+    with _on(X.device):
+        _q._check(_q.lib().qlora_mx_quantize(X.data_ptr(), DTYPES[X.dtype], R, C, int(transpose), ctypes.byref(d),
+                                             _status_ptr(status, X.device), _stream(X.device)))
+    return out
+
+
+def mx_dequant(t: MXTensor, dtype=torch.bfloat16, out=None) -> torch.Tensor:
+    """The values of an MXFP4 matrix, [rows, cols] in bf16 or fp32 (both exact)."""
+    _need(dtype in (torch.bfloat16, torch.float32), "dtype must be bfloat16 or float32")
+    d = t.descriptor()
+    if out is None:
+        out = torch.empty((t.rows, t.cols), dtype=dtype, device=t.device)
+    _tensor(out, "out", (t.rows, t.cols), dtype, t.device)
+    with _on(t.device):
+        _q._check(_q.lib().qlora_mx_dequant(ctypes.byref(d), out.data_ptr(), DTYPES[dtype], _stream(t.device)))
+    return out
+
+
+def mx_matmul(a: MXTensor, b: MXTensor, dtype=torch.bfloat16, out=None, status=None) -> torch.Tensor:
+    """A.B^T of two MXFP4 matrices with equal cols, [a.rows, b.rows] in bf16
+    or fp32; accumulated in fp32 (b.rows % 8 == 0)."""
+    _need(dtype in (torch.bfloat16, torch.float32), "dtype must be bfloat16 or float32")
+    _need(a.device == b.device, "a and b must be on one device")
+    da, db = a.descriptor(), b.descriptor()
+    if out is None:
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.device)
+    _tensor(out, "out", (a.rows, b.rows), dtype, a.device)
+    with _on(a.device):
+        _q._check(_q.lib().qlora_mx_matmul(ctypes.byref(da), ctypes.byref(db), out.data_ptr(), DTYPES[dtype],
+                                           _status_ptr(status, a.device), _stream(a.device)))
+    return out
+
+
+def mx_weight(W, backward: bool = True, status=None) -> MXWeight:
+    """The MXFP4 forms of a weight [N, K] (bf16, fp16 or fp32) that the linear
+    layer multiplies with; backward=False leaves out the one of dX (4.25 bits
+    a weight)."""
+    return MXWeight(mx_quantize(W, status=status), mx_quantize(W, transpose=True, status=status) if backward else None)
+
+
+def mx_linear_workspace_bytes(M: int, N: int, K: int, r: int = 0, dropout: bool = False) -> int:
+    """Workspace of mx_linear_fwd and mx_linear_bwd (the larger of the two)."""
+    n = _q.lib().qlora_mx_linear_workspace_bytes(M, N, K, r, int(dropout))
+    _need(n, "invalid shape or rank for mx_linear_workspace_bytes")
+    return n
+
+
+def _linear_args(M, N, K, L1, L2, dropout, ws, device):
+    """(r, dropout config or None, workspace) after checking the adapter."""
+    _need((L1 is None) == (L2 is None), "L1 and L2 come together")
+    r = 0
+    if L1 is not None:
+        r = _matrix(L1, "L1", (torch.bfloat16,)).shape[1]
+        _tensor(L1, "L1", (K, r), torch.bfloat16, device)
+        _tensor(L2, "L2", (r, N), torch.bfloat16, device)
+    cfg = dropout.config(device) if dropout is not None else None
+    need = mx_linear_workspace_bytes(M, N, K, r, cfg is not None and cfg.p > 0)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    _need(ws.is_cuda and ws.device == device and ws.is_contiguous() and ws.numel() * ws.element_size() >= need,
+          f"ws must be a contiguous tensor of {need} bytes on {device}")
+    return r, cfg, ws
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def mx_linear_fwd(X, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropout: Dropout | None = None, ws=None, Y=None,
+                  T=None, status=None):
+    """Y = Q(X).W^T + s.T.L2 and T = drop(X).L1 (fp32, for the backward; None
+    without an adapter).  X bf16 [M, K], quantised to MXFP4 on the way."""
+    _matrix(X, "X", (torch.bfloat16,))
+    M, K = X.shape
+    dev = X.device
+    _need(w.fwd.cols == K and w.fwd.device == dev, f"the weight must have {K} columns and be on {dev}")
+    N = w.fwd.rows
+    if M == 0:
+        r = 0 if L1 is None else L1.shape[1]
+        return (torch.empty((0, N), dtype=torch.bfloat16, device=dev) if Y is None else Y,
+                None if L1 is None else torch.empty((0, r), dtype=torch.float32, device=dev) if T is None else T)
+    r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(Y, "Y", (M, N), torch.bfloat16, dev)
+    if not r:
+        T = None
+    elif T is None:
+        T = torch.empty((M, r), dtype=torch.float32, device=dev)
+    else:
+        _tensor(T, "T", (M, r), torch.float32, dev)
+    d = w.fwd.descriptor()
+    with _on(dev):
+        _q._check(_q.lib().qlora_mx_linear_fwd(X.data_ptr(), M, ctypes.byref(d), _ptr(L1), _ptr(L2), r, float(s),
+                                               None if cfg is None else ctypes.byref(cfg), Y.data_ptr(), _ptr(T),
+                                               ws.data_ptr(), ws.numel() * ws.element_size(),
+                                               _status_ptr(status, dev), _stream(dev)))
+    return Y, T
+
+
+def mx_linear_bwd(dY, X, T, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropout: Dropout | None = None, ws=None,
+                  need_dX=True, need_dL1=True, need_dL2=True, status=None, dX=None, dL1=None, dL2=None):
+    """dX = Q(dY).W + drop(s.dT.L1^T), dL1 = s.drop(X)^T.dT, dL2 = s.T^T.dY
+    with dT = dY.L2^T; ``dropout`` names the forward's mask.  Without an
+    adapter: dX alone.  dX needs ``w.bwd``."""
+    _matrix(dY, "dY", (torch.bfloat16,))
+    M, N = dY.shape
+    dev = dY.device
+    K = w.fwd.cols
+    _need(w.fwd.rows == N and w.fwd.device == dev, f"the weight must have {N} rows and be on {dev}")
+    need_dX, adapter = need_dX or dX is not None, L1 is not None
+    need_dL1, need_dL2 = adapter and (need_dL1 or dL1 is not None), adapter and (need_dL2 or dL2 is not None)
+    _need(not need_dX or (w.bwd is not None and (w.bwd.rows, w.bwd.cols) == (K, N) and w.bwd.device == dev),
+          "dX needs the weight's backward form (mx_weight(W), w.bwd)")
+    r = L1.shape[1] if adapter else 0
+    if need_dL1:
+        _tensor(X, "X", (M, K), torch.bfloat16, dev)
+    if need_dL2:
+        _tensor(T, "T", (M, r), torch.float32, dev)
+
+    def output(t, name, shape, dtype, wanted):
+        if not wanted:
+            return None
+        return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, name, shape, dtype, dev)
+
+    dX = output(dX, "dX", (M, K), torch.bfloat16, need_dX)
+    dL1 = output(dL1, "dL1", (K, r), torch.float32, need_dL1)
+    dL2 = output(dL2, "dL2", (r, N), torch.float32, need_dL2)
+    if M == 0:
+        for g in (dL1, dL2):
+            if g is not None:
+                g.zero_()
+        return dX, dL1, dL2
+    r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, dev)
+    d = w.bwd.descriptor() if need_dX else None
+    with _on(dev):
+        _q._check(_q.lib().qlora_mx_linear_bwd(dY.data_ptr(), _ptr(X), M, _ptr(T),
+                                               None if d is None else ctypes.byref(d), N, K, _ptr(L1), _ptr(L2), r,
+                                               float(s), None if cfg is None else ctypes.byref(cfg), _ptr(dX),
+                                               _ptr(dL1), _ptr(dL2), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                               _status_ptr(status, dev), _stream(dev)))
+    return dX, dL1, dL2
+
+
+def dropout(X, p: float, seed: int, offset=0, out=None) -> torch.Tensor:
+    """X with elements zeroed with probability p and the others scaled by
+    1 / (1 - p) (p in steps of 2^-16), the mask named by (seed, offset) and
+    never stored; the gradient is the same call on the upstream gradient.
+    X: contiguous bf16, fp16 or fp32 CUDA tensor of any shape; out may be X."""
+    _need(isinstance(X, torch.Tensor) and X.is_cuda and X.is_contiguous() and X.dtype in DTYPES,
+          "X must be a contiguous bfloat16, float16 or float32 CUDA tensor")
+    cfg = Dropout(p, seed, offset).config(X.device)
+    if out is None:
+        out = torch.empty_like(X)
+    _tensor(out, "out", X.shape, X.dtype, X.device)
+    if X.numel() == 0:
+        return out
+    with _on(X.device):
+        _q._check(_q.lib().qlora_dropout(X.data_ptr(), DTYPES[X.dtype], X.numel(), ctypes.byref(cfg), out.data_ptr(),
+                                         _stream(X.device)))
+    return out

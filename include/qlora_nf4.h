@@ -59,7 +59,10 @@ enum {
   QLORA_ERR_TIMEOUT = -8,     /* device status: an internal wait expired */
   QLORA_ERR_DEVICE = -9,      /* current device is not sm_100 */
   QLORA_ERR_SCRATCH_LIMIT = -10, /* problem needs more than the library's static scratch */
-  QLORA_ERR_FORMAT = -11        /* unknown code format or scale codec */
+  QLORA_ERR_FORMAT = -11,       /* unknown code format or scale codec */
+  QLORA_ERR_DTYPE = -12,        /* unknown or unsupported element type */
+  QLORA_ERR_DROPOUT = -13,      /* dropout probability outside [0, 1) */
+  QLORA_ERR_MX_SHAPE = -14      /* invalid MXFP4 shape */
 };
 
 /*
@@ -286,6 +289,138 @@ QLORA_API int qlora_linear_fwd_noalloc(const uint16_t* X, int64_t M, const qlora
                                        const uint16_t* L1, const uint16_t* L2, int r, float s,
                                        uint16_t* Y, float* T_save, int* status_dev,
                                        qlora_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MXFP4) and dropout.
+ *
+ * MXFP4 (OCP Microscaling Formats v1.0) is the 4-bit format the tensor cores
+ * multiply natively: E2M1 codes and one power-of-two scale for each 32
+ * elements of a row.  The calls below quantise to it, multiply two MXFP4
+ * matrices, and run the LoRA linear layer on an MXFP4 weight with the
+ * activations (forward) and upstream gradients (backward) quantised on the
+ * way, so that both large products run at the 4-bit rate.
+ *
+ * The same conventions as above: plain device pointers, 16-byte aligned,
+ * asynchronous on the caller's stream, nothing allocated.
+ */
+
+/* Element types of the calls that take more than one. */
+enum {
+  QLORA_DTYPE_BF16 = 0,
+  QLORA_DTYPE_F16 = 1,
+  QLORA_DTYPE_F32 = 2
+};
+
+/*
+ * An MXFP4 matrix [rows][cols], cols a multiple of 32.
+ *   codes  : uint8[rows * cols / 2]  E2M1 codes (sign, 2 exponent bits, 1
+ *            mantissa bit: 0, 1/2, 1, 3/2, 2, 3, 4, 6), element 2j of a row
+ *            in the low nibble, 2j + 1 in the high.
+ *   scales : uint8, E8M0 (2^(b - 127); 255 is NaN), one for each 32 elements,
+ *            in tiles of 128 rows x 4 blocks of 512 bytes, the
+ *            ceil(cols / 128) tiles of a row range consecutive; in a tile the
+ *            scale of row i and block j is byte (i % 32) * 16 + (i / 32) * 4
+ *            + j.  Bytes that belong to no block must be finite scales (the
+ *            quantiser writes 0).
+ */
+typedef struct qlora_mx_tensor {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows;
+  int64_t cols;
+} qlora_mx_tensor;
+
+/* Bytes of codes and scales.  QLORA_ERR_MX_SHAPE for an invalid shape. */
+QLORA_API int qlora_mx_storage_bytes(int64_t rows, int64_t cols, size_t* codes_bytes, size_t* scales_bytes);
+
+/*
+ * Quantise X[rows][cols] (dtype: any QLORA_DTYPE_*) to `out`:
+ *   b    = max(floor(log2(max |x|)) - 2 + 127, 0) over each block of 32
+ *   code = E2M1(x * 2^(127 - b)), nearest, ties to even, saturated to 6
+ * transpose = 0: blocks along the rows; out is rows x cols, cols % 32 == 0.
+ * transpose = 1: the matrix X^T; out is cols x rows, rows % 32 == 0 and
+ * cols % 8 == 0 (the weight of a backward product, whose reduction runs
+ * over the output features).
+ * A block that holds an Inf or NaN gets scale 255 (its values read as NaN)
+ * and sets *status_dev = QLORA_ERR_NONFINITE; other blocks are unaffected.
+ * out->rows / out->cols are ignored.
+ */
+QLORA_API int qlora_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int transpose,
+                                const qlora_mx_tensor* out, int* status_dev, qlora_stream_t stream);
+
+/* The values an MXFP4 matrix stands for, [rows][cols]: bf16 (exact) or fp32
+ * (exact). */
+QLORA_API int qlora_mx_dequant(const qlora_mx_tensor* t, void* out, int dtype, qlora_stream_t stream);
+
+/*
+ * out[a->rows][b->rows] = RN( A^ . B^T ), bf16 or fp32: the product of two
+ * MXFP4 matrices with the same cols, accumulated in fp32.  b->rows % 8 == 0.
+ * The order of summation is fixed by the shapes: equal calls give equal bits.
+ */
+QLORA_API int qlora_mx_matmul(const qlora_mx_tensor* a, const qlora_mx_tensor* b, void* out, int dtype,
+                              int* status_dev, qlora_stream_t stream);
+
+/*
+ * Dropout from a counter-based generator (Philox4x32-10), the mask never
+ * stored.  Element i of a tensor takes 16 bits of the generator's output for
+ * key `seed` and counter (i / 8, offset): word (i % 8) / 2, its low half for
+ * an even i.  With t = round(65536 p) (ties to even) it is kept where those
+ * bits are >= t and then scaled by 65536 / (65536 - t); a dropped element is
+ * 0 whatever it held.  The same (seed, offset) gives the same mask in every
+ * call, so a backward pass names the forward's; another call takes another
+ * offset.  offset_dev, when not NULL, is a device word added to offset when
+ * the kernel runs: a captured graph draws a new mask at each replay if it
+ * is advanced in between.
+ */
+typedef struct qlora_dropout_config {
+  double p; /* in [0, 1) with round(65536 p) < 65536 */
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* offset_dev;
+} qlora_dropout_config;
+
+/* out[n] = dropout(X[n]), any QLORA_DTYPE_*; out may be X.  The gradient is
+ * the same call on the upstream gradient. */
+QLORA_API int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_config* cfg, void* out,
+                            qlora_stream_t stream);
+
+/* Workspace bytes of qlora_mx_linear_fwd and qlora_mx_linear_bwd (the maximum
+ * of both) for M tokens, an N x K weight, rank r (0: no adapter) and dropout
+ * on the adapter's input or not.  0 for an invalid shape. */
+QLORA_API size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int dropout);
+
+/*
+ * Forward of the LoRA linear layer on an MXFP4 weight W^ [N][K]:
+ *   T = drop(X) . L1                      (fp32, saved for the backward)
+ *   Y = RNbf16( Q(X) . W^T + RNbf16(s T) . L2 )
+ * Q is the MXFP4 quantisation along K, drop the dropout of element m K + k of
+ * X (drop = NULL: none).  r = 0 (L1, L2, T_save NULL): no adapter.
+ *   X : bf16[M][K]   L1 : bf16[K][r]   L2 : bf16[r][N]   Y : bf16[M][N]
+ * Requires K % 32 == 0, N % 8 == 0 and r = 0 or r % 8 == 0, 8 <= r <= 128.
+ * A non-finite X sets *status_dev = QLORA_ERR_NONFINITE and gives NaN in its
+ * row of Y.
+ */
+QLORA_API int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, const uint16_t* L1,
+                                  const uint16_t* L2, int r, float s, const qlora_dropout_config* drop, uint16_t* Y,
+                                  float* T_save, void* ws, size_t ws_bytes, int* status_dev, qlora_stream_t stream);
+
+/*
+ * Backward of the same layer.  wt is the weight quantised along the output
+ * features, the MXFP4 form of W^T, [K][N] (qlora_mx_quantize, transpose = 1).
+ *   dT  = s dY . L2^T
+ *   dX  = RNbf16( Q(dY) . Wt^T + drop(RNbf16(dT) . L1^T) )
+ *   dL1 = drop(X)^T . dT        (fp32)
+ *   dL2 = s T^T . dY            (fp32)
+ * dT and s T enter the products of dL1 and dL2 as two bf16 terms each (2^-17
+ * relative).  drop names the forward's mask.  dX, dL1 or dL2 may be NULL to
+ * skip that output (wt may then be NULL with dX, L1 and L2 must not).  Requires
+ * K % 32 == 0, N % 32 == 0; r as in the forward; r = 0: dX alone.
+ */
+QLORA_API int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const float* T_saved,
+                                  const qlora_mx_tensor* wt, int64_t N, int64_t K, const uint16_t* L1,
+                                  const uint16_t* L2, int r, float s, const qlora_dropout_config* drop, uint16_t* dX,
+                                  float* dL1, float* dL2, void* ws, size_t ws_bytes, int* status_dev,
+                                  qlora_stream_t stream);
 
 /* Diagnostic timing hook.  When both are non-NULL (cudaEvent_t handles),
  * the next qlora_linear_fwd / qlora_linear_bwd records `ev_start` on its

@@ -1,0 +1,130 @@
+"""Host-side checks of the MXFP4 and dropout calls (no GPU): storage sizes,
+and every refusal before a device is touched.  The pointers are fake and never
+dereferenced; a launch with them would fault."""
+
+import ctypes
+
+import pytest
+import torch
+
+P = ctypes.c_void_p
+FAKE, ODD = P(0x10000), P(0x10008)
+NULL, ALIGN, SHAPE, RANK, WORKSPACE, DTYPE, DROPOUT, MX_SHAPE = -1, -2, -3, -4, -5, -12, -13, -14
+
+
+@pytest.fixture(scope="module")
+def q():
+    import bit_nf4_quantized_15_b200 as q
+    from bit_nf4_quantized_15_b200 import build
+    build.build()
+    return q
+
+
+def _t(q, rows, cols, codes=0x1000, scales=0x2000):
+    return ctypes.byref(q.mx.qlora_mx_tensor(codes, scales, rows, cols))
+
+
+def _d(q, p=0.1, offset_dev=None):
+    return ctypes.byref(q.mx.qlora_dropout_config(p, 1, 2, offset_dev))
+
+
+def test_storage_bytes(q):
+    assert q.mx_storage_bytes(128, 128) == (8192, 512)
+    assert q.mx_storage_bytes(129, 160) == (129 * 80, 2 * 2 * 512)
+    assert q.mx_storage_bytes(1, 32) == (16, 512)
+    for bad in ((0, 32), (1, 0), (1, 48), (1 << 25, 32), (1, 1 << 25)):
+        with pytest.raises(q.QLoRAError):
+            q.mx_storage_bytes(*bad)
+
+
+def test_quantise_and_dequant_refusals(q):
+    L = q.lib()
+    t = _t(q, 4, 64)
+    assert L.qlora_mx_quantize(None, 0, 4, 64, 0, t, None, None) == NULL
+    assert L.qlora_mx_quantize(FAKE, 0, 4, 64, 0, None, None, None) == NULL
+    assert L.qlora_mx_quantize(FAKE, 0, 4, 64, 0, _t(q, 4, 64, codes=None), None, None) == NULL
+    assert L.qlora_mx_quantize(FAKE, 3, 4, 64, 0, t, None, None) == DTYPE
+    assert L.qlora_mx_quantize(FAKE, 0, 4, 48, 0, t, None, None) == MX_SHAPE
+    assert L.qlora_mx_quantize(FAKE, 0, 0, 64, 0, t, None, None) == MX_SHAPE
+    assert L.qlora_mx_quantize(FAKE, 0, 48, 64, 1, t, None, None) == MX_SHAPE       # blocks along 48 rows
+    assert L.qlora_mx_quantize(FAKE, 0, 64, 12, 1, t, None, None) == MX_SHAPE
+    assert L.qlora_mx_quantize(ODD, 0, 4, 64, 0, t, None, None) == ALIGN
+    assert L.qlora_mx_quantize(FAKE, 0, 4, 64, 0, _t(q, 4, 64, scales=0x2004), None, None) == ALIGN
+    assert L.qlora_mx_dequant(t, None, 0, None) == NULL
+    assert L.qlora_mx_dequant(t, FAKE, 1, None) == DTYPE
+    assert L.qlora_mx_dequant(_t(q, 4, 40), FAKE, 0, None) == MX_SHAPE
+    assert L.qlora_mx_dequant(t, ODD, 0, None) == ALIGN
+
+
+def test_matmul_refusals(q):
+    L = q.lib()
+    a, b = _t(q, 4, 64), _t(q, 16, 64)
+    assert L.qlora_mx_matmul(None, b, FAKE, 0, None, None) == NULL
+    assert L.qlora_mx_matmul(a, b, None, 0, None, None) == NULL
+    assert L.qlora_mx_matmul(a, b, FAKE, 1, None, None) == DTYPE
+    assert L.qlora_mx_matmul(a, _t(q, 16, 96), FAKE, 0, None, None) == MX_SHAPE
+    assert L.qlora_mx_matmul(a, _t(q, 12, 64), FAKE, 0, None, None) == MX_SHAPE
+    assert L.qlora_mx_matmul(_t(q, 0, 64), b, FAKE, 0, None, None) == MX_SHAPE
+    assert L.qlora_mx_matmul(a, b, ODD, 0, None, None) == ALIGN
+    assert L.qlora_mx_matmul(a, _t(q, 16, 64, codes=0x1008), FAKE, 0, None, None) == ALIGN
+
+
+def test_dropout_refusals(q):
+    L = q.lib()
+    assert L.qlora_dropout(None, 0, 8, _d(q), FAKE, None) == NULL
+    assert L.qlora_dropout(FAKE, 0, 8, None, FAKE, None) == NULL
+    assert L.qlora_dropout(FAKE, 7, 8, _d(q), FAKE, None) == DTYPE
+    assert L.qlora_dropout(FAKE, 0, -1, _d(q), FAKE, None) == SHAPE
+    for p in (-0.1, 1.0, 2.0, float("nan"), 1 - 2.0 ** -18):
+        assert L.qlora_dropout(FAKE, 0, 8, _d(q, p), FAKE, None) == DROPOUT
+    assert L.qlora_dropout(FAKE, 0, 8, _d(q, 0.1, 0x1004), FAKE, None) == ALIGN
+    assert L.qlora_dropout(FAKE, 0, 8, _d(q), ODD, None) == ALIGN
+    assert L.qlora_dropout(FAKE, 0, 0, _d(q), FAKE, None) == 0
+
+
+def test_linear_refusals(q):
+    L = q.lib()
+    big = 1 << 40
+
+    def fwd(X=FAKE, M=4, w=_t(q, 32, 64), L1=FAKE, L2=FAKE, r=16, drop=None, Y=FAKE, T=FAKE, ws=FAKE, n=big):
+        return L.qlora_mx_linear_fwd(X, M, w, L1, L2, r, 1.0, drop, Y, T, ws, n, None, None)
+
+    assert fwd(X=None) == NULL and fwd(w=None) == NULL and fwd(Y=None) == NULL and fwd(ws=None) == NULL
+    assert fwd(L1=None) == NULL and fwd(L2=None) == NULL and fwd(T=None) == NULL
+    assert fwd(r=12) == RANK and fwd(r=136) == RANK and fwd(r=-8) == RANK
+    assert fwd(M=0) == MX_SHAPE and fwd(w=_t(q, 12, 64)) == MX_SHAPE and fwd(w=_t(q, 32, 72)) == MX_SHAPE
+    assert fwd(X=ODD) == ALIGN and fwd(T=ODD) == ALIGN and fwd(drop=_d(q, 1.5)) == DROPOUT
+
+    def bwd(dY=FAKE, X=FAKE, M=4, T=FAKE, wt=_t(q, 64, 32), N=32, K=64, L1=FAKE, L2=FAKE, r=16, drop=None, dX=FAKE,
+            dL1=FAKE, dL2=FAKE, ws=FAKE, n=big):
+        return L.qlora_mx_linear_bwd(dY, X, M, T, wt, N, K, L1, L2, r, 1.0, drop, dX, dL1, dL2, ws, n, None, None)
+
+    assert bwd(dY=None) == NULL and bwd(ws=None) == NULL and bwd(wt=None) == NULL
+    assert bwd(X=None) == NULL and bwd(T=None) == NULL and bwd(L1=None) == NULL
+    assert bwd(r=0) == RANK                                   # adapter gradients without an adapter
+    assert bwd(N=40, wt=_t(q, 64, 40)) == MX_SHAPE            # no backward form: N % 32
+    assert bwd(wt=_t(q, 32, 64)) == MX_SHAPE                  # the forward's form in its place
+    assert bwd(M=0) == MX_SHAPE
+    assert bwd(dL1=ODD) == ALIGN and bwd(drop=_d(q, -1.0)) == DROPOUT
+
+
+def test_workspace_bytes(q):
+    n = q.mx_linear_workspace_bytes
+    assert n(16, 4096, 4096) > 0 and n(16, 4096, 4096, 16) > n(16, 4096, 4096)
+    assert n(4096, 4096, 4096, 64, True) > n(4096, 4096, 4096, 64)
+    for bad in ((0, 64, 64, 16), (4, 60, 64, 16), (4, 64, 80, 16), (4, 64, 64, 12)):
+        with pytest.raises(q.QLoRAError):
+            n(*bad)
+
+
+def test_binding_refuses_what_is_not_a_cuda_tensor(q):
+    X = torch.zeros((4, 64), dtype=torch.bfloat16)
+    t = q.MXTensor(torch.zeros(128, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 4, 64)
+    for call in (lambda: q.mx_quantize(X), lambda: q.dropout(X, 0.1, 1), lambda: q.mx_dequant(t),
+                 lambda: q.mx_matmul(t, t), lambda: q.mx_linear_fwd(X, q.MXWeight(t)),
+                 lambda: q.mx_linear_bwd(X, X, None, q.MXWeight(t))):
+        with pytest.raises(q.QLoRAError):
+            call()
+    for p, seed, off in ((0.1, -1, 0), (0.1, 0, -1), (0.1, 1 << 64, 0)):
+        with pytest.raises(q.QLoRAError):
+            q.Dropout(p, seed, off).config(X.device)
