@@ -285,6 +285,30 @@ MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms);
 size_t mx_gemm_smem_bytes(int BN);
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st);
 
+
+// The same product on persistent CTA pairs, tokens on the lanes:
+// out[row][col] = sum_k A[row, k] B[col, k] (+ LoRA term), 256 x 256 tiles.
+struct MxPairArgs {
+  CUtensorMap tmA;   // codes of A (tokens), box 128 x 128, 128-byte swizzle
+  CUtensorMap tmB;   // codes of B (weight), the same
+  CUtensorMap tmSA;  // tiled scales as uint32 [row tiles][kt * 128], box 256 x 1
+  CUtensorMap tmSB;  // the same, box 256 x 2
+  CUtensorMap tmAx;  // LoRA term: bf16 [rows][r], K-major
+  CUtensorMap tmBx;  // LoRA term: B side (K- or MN-major per b_mn_ext)
+  int rows, cols;
+  int64_t K;
+  int kb;            // 256-wide reduction blocks
+  int kb_ext;
+  int b_mn_ext;
+  void* out;         // [rows][ldo]
+  int64_t ldo;
+  int out_f32;
+  DropArgs drop;     // mask of the LoRA term at element row * ldo + col
+  int* status;
+};
+size_t mx_pair_smem_bytes();
+cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, cudaStream_t st);
+
 // ------------------------------------------- adapter side of the MX linear
 // out[i] = hi, out[i + r] = lo: v = scale * in split into two bf16 terms (the
 // rest of v below 2^-17 of it); in [M][r] fp32, out [M][2r].

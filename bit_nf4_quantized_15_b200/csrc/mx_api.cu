@@ -80,26 +80,85 @@ void engine_args(EngineArgs* a, int* status, int64_t rows, int cols, int64_t red
   a->epi.alpha = a->epi.alpha2 = 1.0f;
 }
 
-// Product launch: A = the [rows][K] side on the lanes, B = the [cols][K] side.
-int product(MxGemmArgs& g, const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, const uint8_t* b_codes,
-            const uint8_t* b_scales, int64_t cols, int64_t K, const MxGemmPlan& p, cudaStream_t st) {
-  if (make_map(&g.tmA, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)K / 2, (uint64_t)rows, 128, 128,
-               CU_TENSOR_MAP_SWIZZLE_128B) ||
-      make_map(&g.tmB, b_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)K / 2, (uint64_t)cols, 128, (uint32_t)p.BN,
-               CU_TENSOR_MAP_SWIZZLE_128B))
+// The LoRA term of a product: u [M][r] bf16 (rows `u_pitch` bytes apart) times
+// the feature side v, MN-major ([r][features]) or K-major ([features][r]).
+struct LoraTerm {
+  const uint16_t* u;
+  uint64_t u_pitch;
+  const uint16_t* v;
+  int v_mn, r;
+};
+
+// Scales as a map of uint32 [row tiles][kt * 128]: a box is two tiles of
+// `tiles` row ranges.
+int map_scales(CUtensorMap* m, const uint8_t* scales, int64_t rows, int64_t K, int tiles) {
+  return make_map(m, scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, (uint64_t)((K + 127) / 128) * 128,
+                  (uint64_t)((rows + 127) / 128), 256, (uint32_t)tiles, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// out [M][N] = x w^T (+ the LoRA term), x = (xc, xs) the tokens, w = (wc, ws)
+// the features.
+//
+// CTA pairs when their 256 x 256 tiles fill the machine, else tiles of 128
+// features split over clusters.
+int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, const uint8_t* ws, int64_t N,
+            int64_t K, const LoraTerm* lora, const DropArgs& drop, void* out, int out_f32, int* status, int sms,
+            cudaStream_t st) {
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t stall_ns = take_stall_request();
+  if (((M + 255) / 256) * ((N + 255) / 256) >= sms / 2 && !stall_ns) {
+    MxPairArgs g;
+    std::memset(&g, 0, sizeof(g));
+    if (make_map(&g.tmA, xc, u8, 1, (uint64_t)K / 2, (uint64_t)M, 128, 128, sw) ||
+        make_map(&g.tmB, wc, u8, 1, (uint64_t)K / 2, (uint64_t)N, 128, 128, sw) || map_scales(&g.tmSA, xs, M, K, 1) ||
+        map_scales(&g.tmSB, ws, N, K, 2))
+      return QLORA_ERR_CUDA;
+    if (lora) {
+      if (map_operand(&g.tmAx, lora->u, 0, M, lora->r, 128, lora->u_pitch) ||
+          map_operand(&g.tmBx, lora->v, lora->v_mn, N, lora->r, 128))
+        return QLORA_ERR_CUDA;
+      g.kb_ext = (lora->r + 63) / 64;
+      g.b_mn_ext = lora->v_mn;
+      g.drop = drop;
+    }
+    g.rows = (int)M;
+    g.cols = (int)N;
+    g.K = K;
+    g.kb = (int)((K + 255) / 256);
+    g.out = out;
+    g.ldo = N;
+    g.out_f32 = out_f32;
+    g.status = status;
+    return launch_mx_gemm_pair(g, sms, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  }
+  const MxGemmPlan p = plan_mx_gemm(N, M, K, sms);
+  MxGemmArgs g;
+  std::memset(&g, 0, sizeof(g));
+  if (make_map(&g.tmA, wc, u8, 1, (uint64_t)K / 2, (uint64_t)N, 128, 128, sw) ||
+      make_map(&g.tmB, xc, u8, 1, (uint64_t)K / 2, (uint64_t)M, 128, (uint32_t)p.BN, sw))
     return QLORA_ERR_CUDA;
-  g.sfA = a_scales;
-  g.sfB = b_scales;
-  g.rows = (int)rows;
-  g.cols = (int)cols;
+  if (lora) {
+    if (map_operand(&g.tmAx, lora->v, lora->v_mn, N, lora->r, 128) ||
+        map_operand(&g.tmBx, lora->u, 0, M, lora->r, p.BN, lora->u_pitch))
+      return QLORA_ERR_CUDA;
+    g.kb_ext = (lora->r + 63) / 64;
+    g.a_mn_ext = lora->v_mn;
+    g.drop = drop;
+  }
+  g.sfA = ws;
+  g.sfB = xs;
+  g.rows = (int)N;
+  g.cols = (int)M;
   g.K = K;
   g.kt = (int)((K + 127) / 128);
   g.kb = (int)((K + 255) / 256);
-  g.ldo = rows;
-  if (const uint64_t ns = take_stall_request()) {
-    g.stall = 1;
-    g.wait_ns = ns;
-  }
+  g.out = out;
+  g.ldo = N;
+  g.out_f32 = out_f32;
+  g.status = status;
+  g.stall = stall_ns != 0;
+  g.wait_ns = stall_ns;
   return launch_mx_gemm(g, p, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
@@ -196,13 +255,8 @@ int qlora_mx_matmul(const qlora_mx_tensor* a, const qlora_mx_tensor* b, void* ou
   if (!all16({a->codes, a->scales, b->codes, b->scales, out})) return QLORA_ERR_ALIGN;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  MxGemmArgs g;
-  std::memset(&g, 0, sizeof(g));
-  g.out = out;
-  g.out_f32 = dtype == QLORA_DTYPE_F32;
-  g.status = status_dev;
-  return product(g, b->codes, b->scales, b->rows, a->codes, a->scales, a->rows, a->cols,
-                 plan_mx_gemm(b->rows, a->rows, a->cols, di.sms), reinterpret_cast<cudaStream_t>(stream));
+  return product(a->codes, a->scales, a->rows, b->codes, b->scales, b->rows, a->cols, nullptr, DropArgs{}, out,
+                 dtype == QLORA_DTYPE_F32, status_dev, di.sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_config* cfg, void* out,
@@ -249,11 +303,6 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
 
   if (launch_mx_quantize(X, QLORA_DTYPE_BF16, M, K, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess)
     return QLORA_ERR_CUDA;
-  const MxGemmPlan p = plan_mx_gemm(N, M, K, di.sms);
-  MxGemmArgs g;
-  std::memset(&g, 0, sizeof(g));
-  g.out = Y;
-  g.status = status_dev;
   if (r) {
     const uint16_t* Xa = X;  // the adapter's input, its dropped elements zero (the scale goes on T)
     if (masked) {
@@ -280,11 +329,10 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
     if (int rc = run_adapter(a, pt, part, st)) return rc;
     if (pt.splits > 1 && launch_split_reduce(part, pt.splits, a.rows, a.cols, a.epi, st) != cudaSuccess)
       return QLORA_ERR_CUDA;
-    if (map_operand(&g.tmAx, L2, 1, N, r, 128) || map_operand(&g.tmBx, sT, 0, M, r, p.BN)) return QLORA_ERR_CUDA;
-    g.kb_ext = (r + 63) / 64;
-    g.a_mn_ext = 1;
   }
-  return product(g, w->codes, w->scales, N, wb, wb + lay.q_scales, M, K, p, st);
+  const LoraTerm lora{sT, 0, L2, 1, r};
+  return product(wb, wb + lay.q_scales, M, w->codes, w->scales, N, K, r ? &lora : nullptr, DropArgs{}, Y, 0,
+                 status_dev, di.sms, st);
 }
 
 int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const float* T_saved,
@@ -331,18 +379,10 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   if (dX) {
     if (launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess)
       return QLORA_ERR_CUDA;
-    const MxGemmPlan p = plan_mx_gemm(K, M, N, di.sms);
-    MxGemmArgs g;
-    std::memset(&g, 0, sizeof(g));
-    g.out = dX;
-    g.status = status_dev;
-    if (r) {
-      if (map_operand(&g.tmAx, L1, 0, K, r, 128) || map_operand(&g.tmBx, sdT, 0, M, r, p.BN, (uint64_t)r * 4))
-        return QLORA_ERR_CUDA;
-      g.kb_ext = (r + 63) / 64;
-      g.drop = d;
-    }
-    if (int rc = product(g, wt->codes, wt->scales, K, wb, wb + lay.q_scales, M, N, p, st)) return rc;
+    const LoraTerm lora{sdT, (uint64_t)r * 4, L1, 0, r};
+    if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d, dX, 0,
+                         status_dev, di.sms, st))
+      return rc;
   }
   if (dL1) {
     const uint16_t* Xa = X;

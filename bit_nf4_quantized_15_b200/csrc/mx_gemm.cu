@@ -21,12 +21,12 @@
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, then 4 epilogue warps (8 for
 // BN >= 128).
 #include "engine_util.cuh"
+#include "mx_util.cuh"
+#include "pair_util.cuh"
 #include "philox.cuh"
 
 namespace qnf4 {
 namespace {
-
-constexpr int kMxKB = 256;  // reduction elements of a stage: 128 bytes of codes
 
 template <int BN>
 struct MxCfg {
@@ -46,12 +46,6 @@ struct MxCfg {
   static_assert(NEED <= 512 && STAGE % 1024 == 0 && TOTAL <= 232448 && BN * 512 <= S * STAGE, "budget");
 };
 
-// Instruction descriptor, kind::mxf4: E2M1 x E2M1, E8M0 scales; the scale ids
-// pick bytes 0-1 or 2-3 of each scale column word (two 32-blocks a step).
-__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf_id) {
-  return ((uint32_t)sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(M >> 7) << 27) | ((uint32_t)sf_id << 29);
-}
 QDEV void umma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -65,34 +59,23 @@ QDEV void umma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32
 QDEV void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-// Unswizzled matrix of 16-byte rows, 8-row groups 128 bytes apart.
-QDEV uint64_t sdesc_scales(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
-}
 QDEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
-QDEV uint32_t mx_cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 QDEV uint32_t mx_cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-QDEV void mx_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 QDEV float2 ld_peer_f2(uint32_t addr, uint32_t rank) {
-  uint32_t a;
   float2 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(mapa_shared(addr, rank))
+               : "memory");
   return v;
 }
 
@@ -128,7 +111,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)mx_cluster_rank(), csize = (int)mx_cluster_size();
+  const int rank = (int)cluster_ctarank(), csize = (int)mx_cluster_size();
   const int id = (int)(blockIdx.x / (unsigned)csize);
   const int n_tiles = (args.cols + BN - 1) / BN;
   const int row_tile = id / n_tiles, col_tile = id % n_tiles;
@@ -305,7 +288,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
     tmem_dealloc(tmem, C::COLS);
   }
   if (csize > 1) {
-    mx_cluster_sync();  // every partial tile is in place
+    cluster_sync_all();  // every partial tile is in place
     const int per = (BN + csize - 1) / csize;
     const int c0 = rank * per, nc = min(per, BN - c0);
     const uint32_t red = smem_u32(smem);
@@ -323,7 +306,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
       if (args.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(args.out) + o) = acc;
       else *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(args.out) + o) = pack_bf16x2(acc.x, acc.y);
     }
-    mx_cluster_sync();  // peers may still be reading this CTA's tile
+    cluster_sync_all();  // peers may still be reading this CTA's tile
   }
 }
 

@@ -1,0 +1,350 @@
+// Large products of two MXFP4 matrices: persistent CTA pairs (tcgen05
+// cta_group::2), one 256 x 256 output tile at a time.
+//
+//   out[row, col] = RN( sum_k A^[row, k] B^[col, k] + mask sum_j Ax[row, j] Bx[col, j] )
+//
+// rows are tokens, cols weight rows (features).  Each CTA of a pair loads 128
+// of the tile's token rows, 128 of its weight rows, the scales of its tokens
+// and the scales of all 256 weight rows; the even CTA's MMA thread issues
+// 256 x 256 x 64 kind::mxf4 MMAs that read both CTAs' shared memory, and each
+// CTA ends with 128 rows x 256 columns of fp32 in its tensor memory.  A CTA
+// pulls 35 KB for 256 reduction steps of 128 x 256 outputs, where the
+// single-CTA kernel pulls 51 KB: at the 4-bit rate the L2 is what a tile
+// shape has to spare.
+//
+// Tensor memory: the accumulator (256 columns), then the scales of each ring
+// stage (8 columns of A, 16 of B).  It has no room for two accumulators of
+// this size, so the epilogue drains the tile into registers (bf16, 64 a
+// thread), releases the accumulator, and stores while the next tile's MMAs
+// run.  The LoRA term comes first in a tile, see mx_gemm.cu; with dropout
+// the epilogue warps have the tile's mask ready (128 bits a thread, evaluated
+// during the previous tile's main loop).
+//
+// Barriers (same offsets in both CTAs; "even" ones are used in the even CTA):
+//   full[s]   even: both CTAs' bytes of stage s
+//   empty[s]  each: the MMAs that read stage s have finished
+//   ext       each: the LoRA term of the tile is in tensor memory
+//   masked    even: 16 epilogue warps have masked it
+//   accum     each: the tile's accumulator is final
+//   drained   even: 16 epilogue warps hold it in registers
+// Every wait is bounded; the pair meets at a cluster barrier before tensor
+// memory is freed.
+#include "engine_util.cuh"
+#include "mx_util.cuh"
+#include "pair_util.cuh"
+#include "philox.cuh"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kXS = 6;                                  // stages
+constexpr int kXA = 16384, kXB = 16384;                 // 128 rows x 128 bytes of codes each
+constexpr int kXStage = kXA + kXB + 1024 + 2048;        // + scales of 128 token rows, 256 weight rows
+constexpr int kXBar = kXS * kXStage;
+constexpr int kXTotal = kXBar + 256 + 1024;
+constexpr int kXEpi = 8;                                // epilogue warps: 2 (column halves) x 4 lane quarters
+constexpr int kXThreads = 64 + 32 * kXEpi;
+constexpr uint32_t kXAcc = 256, kXSf = 24;              // accumulator columns, scale columns of a stage
+constexpr int kXGroup = 8;                              // row tiles of a raster group
+static_assert(kXTotal <= 232448 && kXStage % 1024 == 0 && kXAcc + kXS * kXSf <= 512, "budget");
+
+QDEV void umma_mxf4_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                         uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      : "memory");
+}
+// One scale tile of each CTA's shared memory to its own tensor memory.
+QDEV void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+struct TileXY {
+  int m, n;
+};
+// Grouped raster: the pairs that run at a time share a few token and weight
+// tiles in L2.
+QDEV TileXY tile_of(int id, int m_tiles, int n_tiles) {
+  const int per = kXGroup * n_tiles, g = id / per, local = id % per;
+  const int gs = min(kXGroup, m_tiles - g * kXGroup);
+  return TileXY{g * kXGroup + local % gs, local / gs};
+}
+
+// Keep bits of 128 consecutive columns of one row, 32 a word.
+QDEV void mask_row(uint32_t (&w)[4], const MxPairArgs& a, const PhiloxKey& key, int64_t row, int col) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[i] |= keep8((uint64_t)(row * a.ldo + col + 32 * i + 8 * j) >> 3, key, a.drop.threshold) << (8 * j);
+  }
+}
+
+template <bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
+    mx_gemm_pair_kernel(const __grid_constant__ MxPairArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kXBar);
+  uint64_t* empty = full + kXS;
+  uint64_t* ext = empty + kXS;
+  uint64_t* masked = ext + 1;
+  uint64_t* accum = masked + 1;
+  uint64_t* drained = accum + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int pair = (int)(blockIdx.x >> 1), n_pairs = (int)(gridDim.x >> 1);
+  const int m_tiles = (args.rows + 255) / 256, n_tiles = (args.cols + 255) / 256, tiles = m_tiles * n_tiles;
+  const int n_ext = args.kb_ext, n_main = args.kb;
+  const bool use_mask = n_ext && args.drop.threshold;
+
+  if (tid == 0) {
+    for (int s = 0; s < kXS; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(ext, 1);
+    mbar_init(masked, 2 * kXEpi);
+    mbar_init(accum, 1);
+    mbar_init(drained, 2 * kXEpi);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&args.tmA);
+    tma_prefetch_desc(&args.tmB);
+    tma_prefetch_desc(&args.tmSA);
+    tma_prefetch_desc(&args.tmSB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers and tensor memory exist from here on
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+  const uint32_t masked0 = mapa_shared(smem_u32(masked), 0);
+  const uint32_t drained0 = mapa_shared(smem_u32(drained), 0);
+  bool committed = false;
+  int last_tile_no = 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += n_pairs) {
+        const TileXY xy = tile_of(t, m_tiles, n_tiles);
+        const int row0 = xy.m * 256 + (int)rank * 128, col0 = xy.n * 256, bcol0 = col0 + (int)rank * 128;
+        for (int i = 0; i < n_ext + n_main; ++i, ++it) {
+          const int s = it % kXS;
+          if (!(ok = mbar_wait(empty + s, ((uint32_t)(it / kXS) & 1u) ^ 1u, abort_flag, args.status))) break;
+          uint8_t* sa = smem + s * kXStage;
+          uint8_t* sb = sa + kXA;
+          const uint32_t bar = full0 + 8u * (uint32_t)s;
+          if (i < n_ext) {
+            if (leader) mbar_arrive_expect_tx(full + s, 2u * (kXA + kXB));
+            tma_load_2d_pair(sa, &args.tmAx, bar, i * 64, row0);
+            if (args.b_mn_ext) {
+              tma_load_2d_pair(sb, &args.tmBx, bar, bcol0, i * 64);
+              tma_load_2d_pair(sb + 8192, &args.tmBx, bar, bcol0 + 64, i * 64);
+            } else {
+              tma_load_2d_pair(sb, &args.tmBx, bar, i * 64, bcol0);
+            }
+          } else {
+            const int kb = i - n_ext;
+            if (leader) mbar_arrive_expect_tx(full + s, 2u * kXStage);
+            tma_load_2d_pair(sa, &args.tmA, bar, kb * 128, row0);
+            tma_load_2d_pair(sb, &args.tmB, bar, kb * 128, bcol0);
+            tma_load_2d_pair(sb + kXB, &args.tmSA, bar, kb * 256, row0 >> 7);
+            tma_load_2d_pair(sb + kXB + 1024, &args.tmSB, bar, kb * 256, col0 >> 7);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA (even CTA)
+    if (leader && lane == 0) {
+      const uint32_t id_ext = idesc_bf16(256, 256, 0, args.b_mn_ext);
+      const int64_t tail = args.K - (int64_t)(n_main - 1) * kMxKB;
+      const int tail_steps = (int)((tail + 63) / 64);
+      int it = 0, no = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += n_pairs, ++no) {
+        const uint32_t ph = (uint32_t)no & 1u;
+        if (!(ok = mbar_wait_cluster(drained, ph ^ 1u, abort_flag, args.status))) break;
+        tc_fence_after();
+        for (int i = 0; i < n_ext + n_main; ++i, ++it) {
+          const int s = it % kXS;
+          if (!(ok = mbar_wait(full + s, (uint32_t)(it / kXS) & 1u, abort_flag, args.status))) break;
+          tc_fence_after();
+          const uint8_t* sa = smem + s * kXStage;
+          const uint8_t* sb = sa + kXA;
+          if (i < n_ext) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_pair(tmem, operand_desc(sa, 0, kk), operand_desc(sb, args.b_mn_ext, kk), id_ext, (i | kk) != 0);
+            umma_commit_both(empty + s);
+            if (i == n_ext - 1) {
+              // MMAs of another kind follow: let these finish (and be masked)
+              umma_commit_both(ext);
+              ok = use_mask ? mbar_wait_cluster(masked, ph, abort_flag, args.status)
+                            : mbar_wait(ext, ph, abort_flag, args.status);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            continue;
+          }
+          const int steps = i == n_ext + n_main - 1 ? tail_steps : 4;
+          const uint32_t sf = tmem + kXAcc + (uint32_t)s * kXSf;
+          const uint32_t ssf = smem_u32(sb + kXB);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_cp_scales_pair(sf + 4 * h, sdesc_scales(ssf + 512 * h));
+            tmem_cp_scales_pair(sf + 8 + 8 * h, sdesc_scales(ssf + 1024 + 512 * h));
+            tmem_cp_scales_pair(sf + 12 + 8 * h, sdesc_scales(ssf + 2048 + 512 * h));
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk >= steps) break;
+            umma_mxf4_pair(tmem, operand_desc(sa, 0, kk), operand_desc(sb, 0, kk), idesc_mxf4(256, 256, 2 * (kk & 1)),
+                           sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (i | kk) != 0);
+          }
+          umma_commit_both(empty + s);
+        }
+        umma_commit_both(accum);
+        committed = true;
+        last_tile_no = no;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q4 = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(half * 128);
+    const int rl = (int)rank * 128 + q4 * 32 + lane;
+    const PhiloxKey key = use_mask ? philox_key(args.drop) : PhiloxKey{0, 0, 0, 0};
+    uint32_t mw[4] = {0, 0, 0, 0};
+    if (use_mask && pair < tiles) {
+      const TileXY xy = tile_of(pair, m_tiles, n_tiles);
+      mask_row(mw, args, key, (int64_t)xy.m * 256 + rl, xy.n * 256 + half * 128);
+    }
+    int no = 0;
+    for (int t = pair; t < tiles; t += n_pairs, ++no) {
+      const uint32_t ph = (uint32_t)no & 1u;
+      const TileXY xy = tile_of(t, m_tiles, n_tiles);
+      if (use_mask) {
+        if (!warp_wait(ext, ph, abort_flag, args.status, lane)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[16];
+            tmem_ld16(tl + 32 * i + 16 * h, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (!((mw[i] >> (16 * h + j)) & 1u)) v[j] = 0u;
+            tmem_st16(tl + 32 * i + 16 * h, v);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(masked0);
+        if (t + n_pairs < tiles) {  // the next tile's mask, while this one's MMAs run
+          const TileXY nx = tile_of(t + n_pairs, m_tiles, n_tiles);
+          mask_row(mw, args, key, (int64_t)nx.m * 256 + rl, nx.n * 256 + half * 128);
+        }
+      }
+      if (!warp_wait(accum, ph, abort_flag, args.status, lane)) break;
+      tc_fence_after();
+      const int64_t row = (int64_t)xy.m * 256 + rl;
+      const int col = xy.n * 256 + half * 128;
+      if constexpr (F32) {
+        float* dst = reinterpret_cast<float*>(args.out) + row * args.ldo + col;
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tl + (uint32_t)c, v);
+          tmem_wait_ld();
+          if (row >= args.rows) continue;
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            if (col + c + j < args.cols)
+              *reinterpret_cast<uint4*>(dst + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(drained0);
+      } else {
+        uint32_t o[64];
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tl + (uint32_t)c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[c / 2 + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(drained0);
+        if (row < args.rows) {
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(args.out) + row * args.ldo + col;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (col + 8 * c < args.cols)
+              *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // Error path: let MMAs and loads still in flight finish before the pair
+    // meets and frees its memory.
+    if (warp == 1 && lane == 0 && committed) mbar_wait_drain(accum, (uint32_t)last_tile_no & 1u, 10000000ull);
+    if (tid == 0) {
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 2000000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+}  // namespace
+
+size_t mx_pair_smem_bytes() { return kXTotal; }
+
+cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, cudaStream_t st) {
+  auto kern = a.out_f32 ? mx_gemm_pair_kernel<true> : mx_gemm_pair_kernel<false>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kXTotal);
+  if (err != cudaSuccess) return err;
+  const int64_t tiles = (int64_t)((a.rows + 255) / 256) * ((a.cols + 255) / 256);
+  const int pairs = num_sms / 2;
+  const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
+  kern<<<grid, kXThreads, kXTotal, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace qnf4

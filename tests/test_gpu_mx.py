@@ -107,7 +107,8 @@ def test_quantise_special_values(lib, transpose):
 # ---------------------------------------------------------------- product
 MATMULS = [(1, 8, 32), (1, 128, 64), (3, 136, 4096), (16, 64, 96), (17, 136, 160), (32, 1032, 2048), (33, 200, 256),
            (64, 1000, 288), (65, 8, 512), (128, 264, 1056), (129, 128, 2080), (256, 256, 256), (257, 520, 320),
-           (300, 2056, 1568), (1000, 264, 4128), (513, 3000, 416)]
+           (300, 2056, 1568), (1000, 264, 4128), (513, 3000, 416),
+           (2300, 2312, 416), (2433, 2184, 64), (4100, 1288, 2336), (2304, 4864, 32)]   # CTA pairs, ragged in each direction
 
 
 @pytest.mark.parametrize("M,N,K", MATMULS)
@@ -205,7 +206,8 @@ def _problem(lib, M, N, K, r, seed):
 
 LINEARS = [(1, 64, 64, 8, 0.0), (5, 160, 288, 16, 0.5), (16, 1056, 512, 64, 0.1), (33, 96, 4128, 24, 0.0),
            (64, 320, 96, 128, 0.25), (129, 544, 1056, 72, 0.1), (300, 128, 2080, 64, 0.05), (777, 288, 320, 128, 0.1),
-           (520, 2080, 1056, 16, 0.0), (1100, 96, 64, 8, 0.5), (70, 64, 96, 0, 0.0)]
+           (520, 2080, 1056, 16, 0.0), (1100, 96, 64, 8, 0.5), (70, 64, 96, 0, 0.0),
+           (2100, 2336, 2400, 64, 0.1), (2400, 2080, 2528, 128, 0.0), (2049, 2304, 2304, 8, 0.25)]   # CTA pairs
 
 
 @pytest.mark.parametrize("M,N,K,r,p", LINEARS)
