@@ -100,7 +100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
 
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const int pair = (int)(blockIdx.x >> 1), n_pairs = (int)(gridDim.x >> 1);
   const int m_tiles = (args.rows + 255) / 256, n_tiles = (args.cols + 255) / 256, tiles = m_tiles * n_tiles;
   const int n_ext = args.kb_ext, n_main = args.kb;
@@ -129,12 +129,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
   tc_fence_before();
   cluster_sync_all();  // both CTAs' barriers and tensor memory exist from here on
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const uint32_t full0 = mapa_shared(smem_u32(full), 0);
   const uint32_t masked0 = mapa_shared(smem_u32(masked), 0);
   const uint32_t drained0 = mapa_shared(smem_u32(drained), 0);
   bool committed = false;
-  int last_tile_no = 0;
+  uint32_t last_ph = 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -173,57 +173,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA (even CTA)
-    if (leader && lane == 0) {
+    if (leader) {
       const uint32_t id_ext = idesc_bf16(256, 256, 0, args.b_mn_ext);
       const int64_t tail = args.K - (int64_t)(n_main - 1) * kMxKB;
       const int tail_steps = (int)((tail + 63) / 64);
-      int it = 0, no = 0;
+      const uint32_t base = smem_u32(smem), a0 = kdesc_lo(base), f0 = (uint32_t)sdesc_scales(base + kXA + kXB);
+      const uint32_t fhi = (uint32_t)(sdesc_scales(0) >> 32);
+      const bool one = elect_one();
+      int s = 0;
+      uint32_t sph = 0, ph = 0;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += n_pairs, ++no) {
-        const uint32_t ph = (uint32_t)no & 1u;
-        if (!(ok = mbar_wait_cluster(drained, ph ^ 1u, abort_flag, args.status))) break;
+      for (int t = pair; t < tiles && ok; t += n_pairs, ph ^= 1u) {
+        if (!(ok = warp_poll(drained, ph ^ 1u, abort_flag, args.status, lane))) break;
         tc_fence_after();
-        for (int i = 0; i < n_ext + n_main; ++i, ++it) {
-          const int s = it % kXS;
-          if (!(ok = mbar_wait(full + s, (uint32_t)(it / kXS) & 1u, abort_flag, args.status))) break;
+        for (int i = 0; i < n_ext + n_main; ++i) {
+          if (!(ok = warp_poll(full + s, sph, abort_flag, args.status, lane))) break;
           tc_fence_after();
-          const uint8_t* sa = smem + s * kXStage;
-          const uint8_t* sb = sa + kXA;
           if (i < n_ext) {
+            const uint8_t* sa = smem + s * kXStage;
+            if (one) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_pair(tmem, operand_desc(sa, 0, kk), operand_desc(sb, args.b_mn_ext, kk), id_ext, (i | kk) != 0);
-            umma_commit_both(empty + s);
+              for (int kk = 0; kk < 4; ++kk)
+                umma_pair(tmem, operand_desc(sa, 0, kk), operand_desc(sa + kXA, args.b_mn_ext, kk), id_ext,
+                          (i | kk) != 0);
+              umma_commit_both(empty + s);
+              if (i == n_ext - 1) umma_commit_both(ext);
+            }
+            // MMAs of another kind follow: let these finish (and be masked)
             if (i == n_ext - 1) {
-              // MMAs of another kind follow: let these finish (and be masked)
-              umma_commit_both(ext);
-              ok = use_mask ? mbar_wait_cluster(masked, ph, abort_flag, args.status)
-                            : mbar_wait(ext, ph, abort_flag, args.status);
-              if (!ok) break;
+              if (!(ok = warp_poll(use_mask ? masked : ext, ph, abort_flag, args.status, lane))) break;
               tc_fence_after();
             }
-            continue;
-          }
-          const int steps = i == n_ext + n_main - 1 ? tail_steps : 4;
-          const uint32_t sf = tmem + kXAcc + (uint32_t)s * kXSf;
-          const uint32_t ssf = smem_u32(sb + kXB);
+          } else if (one) {
+            const int steps = i == n_ext + n_main - 1 ? tail_steps : 4;
+            const uint32_t so = (uint32_t)s * (kXStage >> 4);
+            const uint32_t sf = tmem + kXAcc + (uint32_t)s * kXSf;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_cp_scales_pair(sf + 4 * h, sdesc_scales(ssf + 512 * h));
-            tmem_cp_scales_pair(sf + 8 + 8 * h, sdesc_scales(ssf + 1024 + 512 * h));
-            tmem_cp_scales_pair(sf + 12 + 8 * h, sdesc_scales(ssf + 2048 + 512 * h));
-          }
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t f = ((uint64_t)fhi << 32) | (f0 + so + 32 * h);
+              tmem_cp_scales_pair(sf + 4 * h, f);
+              tmem_cp_scales_pair(sf + 8 + 8 * h, f + 64);
+              tmem_cp_scales_pair(sf + 12 + 8 * h, f + 128);
+            }
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk >= steps) break;
-            umma_mxf4_pair(tmem, operand_desc(sa, 0, kk), operand_desc(sb, 0, kk), idesc_mxf4(256, 256, 2 * (kk & 1)),
-                           sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (i | kk) != 0);
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk < steps)
+                umma_mxf4_pair(tmem, kdesc(a0 + so + 2 * kk), kdesc(a0 + so + (kXA >> 4) + 2 * kk),
+                               idesc_mxf4(256, 256, 2 * (kk & 1)), sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1),
+                               (i | kk) != 0);
+            }
+            umma_commit_both(empty + s);
           }
-          umma_commit_both(empty + s);
+          __syncwarp();
+          if (++s == kXS) {
+            s = 0;
+            sph ^= 1u;
+          }
         }
-        umma_commit_both(accum);
+        if (one) umma_commit_both(accum);
         committed = true;
-        last_tile_no = no;
+        last_ph = ph;
       }
     }
     __syncwarp();
@@ -290,12 +299,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
       } else {
         uint32_t o[64];
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(tl + (uint32_t)c, v);
+        for (int c = 0; c < 128; c += 64) {  // four loads in flight
+          uint32_t v[4][16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld16(tl + (uint32_t)(c + 16 * q), v[q]);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[c / 2 + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              o[c / 2 + 8 * q + j] = pack_bf16x2(__uint_as_float(v[q][2 * j]), __uint_as_float(v[q][2 * j + 1]));
         }
         tc_fence_before();
         __syncwarp();
@@ -316,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
   if (*abort_flag) {
     // Error path: let MMAs and loads still in flight finish before the pair
     // meets and frees its memory.
-    if (warp == 1 && lane == 0 && committed) mbar_wait_drain(accum, (uint32_t)last_tile_no & 1u, 10000000ull);
+    if (warp == 1 && lane == 0 && committed) mbar_wait_drain(accum, last_ph, 10000000ull);
     if (tid == 0) {
       const uint64_t t0 = globaltimer();
       while (globaltimer() - t0 < 2000000ull) {

@@ -19,5 +19,27 @@ QDEV uint64_t sdesc_scales(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
 }
 
+// One elected lane of a converged warp.  The MMA warps below run their loops
+// with all 32 lanes and only predicate the tensor-core instructions with it:
+// their addresses and descriptors then stay in uniform registers.  (With a
+// loop in a lane == 0 branch every operand is moved there one by one: 100
+// cycles an MMA and 62 a scale copy were measured, which made the issuing
+// thread the bound, 1140 cycles a stage of 512 cycles of tensor work.)
+QDEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// K-major, 128-byte-swizzled operand tile: the descriptor's constant half and
+// its address half (advance by 2 for each 32 bytes of K).
+constexpr uint32_t kDescHi = (uint32_t)((1024u >> 4) | (1u << 14) | (2u << 29));
+QDEV uint64_t kdesc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+QDEV uint32_t kdesc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+
 }  // namespace
 }  // namespace qnf4

@@ -54,6 +54,26 @@ QDEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_
     }
   }
 }
+// Warp-wide bounded wait of a warp that stays converged: every lane polls.
+QDEV bool warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status, int lane,
+                    uint64_t limit_ns = QNF4_WAIT_NS) {
+  const uint32_t a = smem_u32(bar);
+  if (__all_sync(0xFFFFFFFFu, mbar_test_wait_cluster(a, parity))) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_test_wait_cluster(a, parity))) return true;
+    if ((i & 63) == 0) {
+      const bool late = globaltimer() - t0 > limit_ns;
+      if (__any_sync(0xFFFFFFFFu, late || *abort_flag)) {
+        if (lane == 0 && !*abort_flag) {
+          *abort_flag = 1;
+          report(status, QLORA_ERR_TIMEOUT);
+        }
+        return false;
+      }
+    }
+  }
+}
 // 2-D TMA tile load into this CTA's shared memory whose bytes complete on an
 // mbarrier of either CTA of the pair (`bar` is a cluster address).
 QDEV void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
