@@ -310,12 +310,11 @@ size_t mx_pair_smem_bytes();
 cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, cudaStream_t st);
 
 // ------------------------------------------- adapter side of the MX linear
-// out[i] = hi, out[i + r] = lo: v = scale * in split into two bf16 terms (the
-// rest of v below 2^-17 of it); in [M][r] fp32, out [M][2r].
-cudaError_t launch_split_hi_lo(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st);
-// out(row, j) = alpha * sum_z (p[z][j][row] + p[z][r + j][row]) with p fp32
-// [splits][2r][rows], stored at out[row * rs + j * cs].
-cudaError_t launch_sum_hi_lo(const float* partial, int splits, int rows, int r, float alpha, float* out, int64_t rs,
-                             int64_t cs, cudaStream_t st);
+// scale * in [M][r] as three bf16 terms [M][3r] (their sum is exact in fp32).
+cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st);
+// out[row * rs + j * cs] = sum of the 3 terms' columns j, r + j, 2r + j over
+// the splits; partial fp32 [splits][3r][rows].
+cudaError_t launch_sum3(const float* partial, int splits, int rows, int r, float* out, int64_t rs, int64_t cs,
+                        cudaStream_t st);
 
 }  // namespace qnf4

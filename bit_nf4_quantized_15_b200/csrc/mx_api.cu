@@ -51,10 +51,10 @@ int drop_args(const qlora_dropout_config* c, DropArgs* d) {
 
 // The tensor cores' fp32 accumulation truncates, an error that grows with
 // the length of the sum (measured on normal data: 3.8e-7 of the result after
-// 410 terms, 1.65e-6 after 1638).  The adapter sums are fp32 results, so
-// they run in pieces of at most kAdapterSum terms that are added with
-// rounding.
-constexpr int kAdapterSum = 1024;
+// 410 terms, 1.1e-6 after 1024, 1.65e-6 after 1638; fp32 arithmetic with
+// rounding has 0.2 to 1e-6).  The adapter sums are fp32 results, so they run
+// in pieces of at most kAdapterSum terms that are added with rounding.
+constexpr int kAdapterSum = 512;
 
 GemmPlan plan_adapter(int64_t rows, int cols, int64_t red, int sms) {
   const int kb = (int)((red + 63) / 64);
@@ -166,8 +166,8 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
 // the same regions for their own data:
 //   q      MXFP4 of X (forward) or dY (backward): codes, then scales
 //   t      fp32 [M][r]: dT (backward)
-//   u, v   bf16 [M][2r]: hi | lo of the scaled dT (u) and of s T (v); the
-//          forward keeps RNbf16(s T) in u
+//   u, v   bf16 [M][3r]: the scaled dT (u) and s T (v) in three terms, the
+//          first RNbf16; the forward keeps RNbf16(s T) in u
 //   xm     bf16 [M][K]: X with the dropped elements zeroed
 //   part   fp32 partial sums of the adapter products
 struct MxWs {
@@ -185,16 +185,16 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, bool drop, int sms) {
     w.t = o;
     o += up256((size_t)M * r * 4);
     w.u = o;
-    o += up256((size_t)M * r * 4);
+    o += up256((size_t)M * r * 6);
     w.v = o;
-    o += up256((size_t)M * r * 4);
+    o += up256((size_t)M * r * 6);
     w.xm = o;
     if (drop) o += up256((size_t)M * K * 2);
     w.part = o;
     w.t_fwd = plan_adapter(M, r, K, sms);
     w.dt = plan_adapter(M, r, N, sms);
-    w.dl1 = plan_adapter(K, 2 * r, M, sms);
-    w.dl2 = plan_adapter(N, 2 * r, M, sms);
+    w.dl1 = plan_adapter(K, 3 * r, M, sms);
+    w.dl2 = plan_adapter(N, 3 * r, M, sms);
     size_t part = 0;
     for (const GemmPlan* p : {&w.t_fwd, &w.dt, &w.dl1, &w.dl2})
       part = p->partial_bytes > part ? p->partial_bytes : part;
@@ -362,7 +362,7 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   uint16_t* sT = reinterpret_cast<uint16_t*>(wb + lay.v);
   float* part = reinterpret_cast<float*>(wb + lay.part);
 
-  // dT = dY.L2^T, then s dT / (1 - p) as two bf16 terms [hi | lo]
+  // dT = dY.L2^T, then s dT / (1 - p) as three bf16 terms
   if (r && (dX || dL1)) {
     EngineArgs a;
     engine_args(&a, status_dev, M, r, N);
@@ -374,12 +374,12 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
     if (int rc = run_adapter(a, p, part, st)) return rc;
     if (p.splits > 1 && launch_split_reduce(part, p.splits, a.rows, a.cols, a.epi, st) != cudaSuccess)
       return QLORA_ERR_CUDA;
-    if (launch_split_hi_lo(dT, M, r, s * d.inv, sdT, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (launch_split3(dT, M, r, s * d.inv, sdT, st) != cudaSuccess) return QLORA_ERR_CUDA;
   }
   if (dX) {
     if (launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess)
       return QLORA_ERR_CUDA;
-    const LoraTerm lora{sdT, (uint64_t)r * 4, L1, 0, r};
+    const LoraTerm lora{sdT, (uint64_t)r * 6, L1, 0, r};
     if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d, dX, 0,
                          status_dev, di.sms, st))
       return rc;
@@ -394,28 +394,28 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
       Xa = xm;
     }
     EngineArgs a;
-    engine_args(&a, status_dev, K, 2 * r, M);
+    engine_args(&a, status_dev, K, 3 * r, M);
     const GemmPlan& p = lay.dl1;
-    if (map_operand(&a.tmA, Xa, 1, K, M, 128) || map_operand(&a.tmB, sdT, 1, 2 * r, M, p.BN)) return QLORA_ERR_CUDA;
+    if (map_operand(&a.tmA, Xa, 1, K, M, 128) || map_operand(&a.tmB, sdT, 1, 3 * r, M, p.BN)) return QLORA_ERR_CUDA;
     a.a_mn_main = a.b_mn_main = 1;
-    a.epi.out = part;  // one split: the same [2r][rows] layout
+    a.epi.out = part;  // one split: the same [3r][rows] layout
     a.epi.rs = 1;
     a.epi.cs = K;
     if (int rc = run_adapter(a, p, part, st)) return rc;
-    if (launch_sum_hi_lo(part, p.splits, (int)K, r, 1.0f, dL1, r, 1, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (launch_sum3(part, p.splits, (int)K, r, dL1, r, 1, st) != cudaSuccess) return QLORA_ERR_CUDA;
   }
   if (dL2) {
-    if (launch_split_hi_lo(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (launch_split3(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
     EngineArgs a;
-    engine_args(&a, status_dev, N, 2 * r, M);
+    engine_args(&a, status_dev, N, 3 * r, M);
     const GemmPlan& p = lay.dl2;
-    if (map_operand(&a.tmA, dY, 1, N, M, 128) || map_operand(&a.tmB, sT, 1, 2 * r, M, p.BN)) return QLORA_ERR_CUDA;
+    if (map_operand(&a.tmA, dY, 1, N, M, 128) || map_operand(&a.tmB, sT, 1, 3 * r, M, p.BN)) return QLORA_ERR_CUDA;
     a.a_mn_main = a.b_mn_main = 1;
     a.epi.out = part;
     a.epi.rs = 1;
     a.epi.cs = N;
     if (int rc = run_adapter(a, p, part, st)) return rc;
-    if (launch_sum_hi_lo(part, p.splits, (int)N, r, 1.0f, dL2, 1, N, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (launch_sum3(part, p.splits, (int)N, r, dL2, 1, N, st) != cudaSuccess) return QLORA_ERR_CUDA;
   }
   return QLORA_OK;
 }

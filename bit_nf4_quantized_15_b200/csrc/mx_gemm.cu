@@ -335,28 +335,31 @@ cudaError_t launch_bn(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st)
 }
 
 // ------------------------------------------------ adapter-side small kernels
-__global__ void split_hi_lo_kernel(const float* __restrict__ in, int64_t n, int r, float scale,
-                                   __nv_bfloat16* __restrict__ out) {
+// fp32 as three bf16 terms: 8 + 8 + 8 significant bits hold all 24.
+__global__ void split3_kernel(const float* __restrict__ in, int64_t n, int r, float scale,
+                              __nv_bfloat16* __restrict__ out) {
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t m = i / r;
-    const float v = __fmul_rn(in[i], scale);
-    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-    out[i + m * r] = hi;
-    out[i + m * r + r] = __float2bfloat16_rn(__fsub_rn(v, __bfloat162float(hi)));
+    __nv_bfloat16* o = out + i + i / r * 2 * r;
+    float v = __fmul_rn(in[i], scale);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      o[t * r] = h;
+      v = __fsub_rn(v, __bfloat162float(h));
+    }
   }
 }
 
-__global__ void sum_hi_lo_kernel(const float* __restrict__ p, int splits, int rows, int r, float alpha,
-                                 float* __restrict__ out, int64_t rs, int64_t cs) {
+__global__ void sum3_kernel(const float* __restrict__ p, int splits, int rows, int r, float* __restrict__ out,
+                            int64_t rs, int64_t cs) {
   const int64_t n = (int64_t)rows * r;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = i % rows, j = i / rows;
-    float hi = 0.0f, lo = 0.0f;
-    for (int z = 0; z < splits; ++z) {
-      hi += p[((int64_t)z * 2 * r + j) * rows + row];
-      lo += p[((int64_t)z * 2 * r + r + j) * rows + row];
-    }
-    out[row * rs + j * cs] = __fmul_rn(alpha, hi + lo);
+    float t[3] = {0.0f, 0.0f, 0.0f};
+    for (int z = 0; z < splits; ++z)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) t[k] += p[((int64_t)(3 * z + k) * r + j) * rows + row];
+    out[row * rs + j * cs] = t[0] + (t[1] + t[2]);
   }
 }
 
@@ -396,15 +399,15 @@ static int small_grid(int64_t n) {
   return (int)(want < 2368 ? (want > 0 ? want : 1) : 2368);
 }
 
-cudaError_t launch_split_hi_lo(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {
-  split_hi_lo_kernel<<<small_grid(M * r), 256, 0, st>>>(in, M * r, r, scale, reinterpret_cast<__nv_bfloat16*>(out));
+cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {
+  split3_kernel<<<small_grid(M * r), 256, 0, st>>>(in, M * r, r, scale, reinterpret_cast<__nv_bfloat16*>(out));
   count_launches(1);
   return cudaGetLastError();
 }
 
-cudaError_t launch_sum_hi_lo(const float* partial, int splits, int rows, int r, float alpha, float* out, int64_t rs,
-                             int64_t cs, cudaStream_t st) {
-  sum_hi_lo_kernel<<<small_grid((int64_t)rows * r), 256, 0, st>>>(partial, splits, rows, r, alpha, out, rs, cs);
+cudaError_t launch_sum3(const float* partial, int splits, int rows, int r, float* out, int64_t rs, int64_t cs,
+                        cudaStream_t st) {
+  sum3_kernel<<<small_grid((int64_t)rows * r), 256, 0, st>>>(partial, splits, rows, r, out, rs, cs);
   count_launches(1);
   return cudaGetLastError();
 }

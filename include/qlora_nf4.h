@@ -411,8 +411,8 @@ QLORA_API int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_t
  *   dX  = RNbf16( Q(dY) . Wt^T + drop(RNbf16(dT) . L1^T) )
  *   dL1 = drop(X)^T . dT        (fp32)
  *   dL2 = s T^T . dY            (fp32)
- * dT and s T enter the products of dL1 and dL2 as two bf16 terms each (2^-17
- * relative).  drop names the forward's mask.  dX, dL1 or dL2 may be NULL to
+ * dT and s T enter the products of dL1 and dL2 unrounded (three bf16 terms
+ * each, whose sum is the fp32 value).  drop names the forward's mask.  dX, dL1 or dL2 may be NULL to
  * skip that output (wt may then be NULL with dX, L1 and L2 must not).  Requires
  * K % 32 == 0, N % 32 == 0; r as in the forward; r = 0: dX alone.
  */
