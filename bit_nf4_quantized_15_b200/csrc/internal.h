@@ -309,6 +309,40 @@ struct MxPairArgs {
 size_t mx_pair_smem_bytes();
 cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, cudaStream_t st);
 
+// Quantise X and form D = drop(X).L in one pass (mx_prep.cu).
+struct MxPrepPlan {
+  int units_per_tile;  // units (128 rows x 256 columns) of a row tile
+  int64_t units;
+  int grid, maxc;      // CTAs; most CTAs that share a row tile
+  size_t part_bytes;   // fp32 [row tiles][maxc][128][r]
+};
+struct MxPrepArgs {
+  CUtensorMap tmX;      // bf16 [M][C], box 64 x 128, 128-byte swizzle
+  CUtensorMap tmL;      // L1 [C][r] (l_mn: box 64 x 64) or L2 [r][C] (box 64 x r16)
+  CUtensorMap tmCodes;  // codes [M][C / 2], box 128 x 128, 128-byte swizzle
+  uint8_t* scales;
+  int kt;               // scale tiles along C
+  int64_t cols;
+  int r, r16, l_mn;     // r16: r rounded up to 16
+  int64_t units;
+  int units_per_tile, maxc;
+  float* part;
+  DropArgs drop;
+  int* status;
+};
+struct MxPrepFinish {
+  const float* part;
+  int64_t M, units;
+  int r, units_per_tile, grid, maxc, terms;
+  float* T;
+  float alpha, beta;
+  uint16_t* out;
+};
+MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms);
+cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st);
+cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, const float* part, int64_t M, int r, float* T, float alpha,
+                                  uint16_t* out, int terms, float beta, cudaStream_t st);
+
 // ------------------------------------------- adapter side of the MX linear
 // scale * in [M][r] as three bf16 terms [M][3r] (their sum is exact in fp32).
 cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st);

@@ -162,17 +162,39 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
   return launch_mx_gemm(g, p, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
+// Q(X) and the partial sums of D = drop(X).L (L MN-major [C][r] or K-major [r][C]).
+int prep(const uint16_t* X, int64_t M, int64_t C, const uint16_t* L, int l_mn, int r, const DropArgs& d,
+         uint8_t* codes, uint8_t* scales, float* part, const MxPrepPlan& p, int* status, cudaStream_t st) {
+  MxPrepArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const int r16 = (r + 15) / 16 * 16;
+  if (map_operand(&a.tmX, X, 0, M, C, 128) ||
+      (l_mn ? map_operand(&a.tmL, L, 1, r, C, 64) : map_operand(&a.tmL, L, 0, r, C, r16)) ||
+      make_map(&a.tmCodes, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)C / 2, (uint64_t)M, 128, 128,
+               CU_TENSOR_MAP_SWIZZLE_128B))
+    return QLORA_ERR_CUDA;
+  a.scales = scales;
+  a.kt = (int)((C + 127) / 128);
+  a.cols = C;
+  a.r = r;
+  a.l_mn = l_mn;
+  a.part = part;
+  a.drop = d;
+  a.status = status;
+  return launch_mx_prep(a, p, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
 // Workspace of the linear layer (offsets in bytes).  Forward and backward use
 // the same regions for their own data:
 //   q      MXFP4 of X (forward) or dY (backward): codes, then scales
-//   t      fp32 [M][r]: dT (backward)
 //   u, v   bf16 [M][3r]: the scaled dT (u) and s T (v) in three terms, the
 //          first RNbf16; the forward keeps RNbf16(s T) in u
 //   xm     bf16 [M][K]: X with the dropped elements zeroed
 //   part   fp32 partial sums of the adapter products
 struct MxWs {
-  size_t q_scales, t, u, v, xm, part, total;
-  GemmPlan t_fwd, dt, dl1, dl2;
+  size_t q_scales, u, v, xm, part, total;
+  MxPrepPlan prep_x, prep_dy;
+  GemmPlan dl1, dl2;
 };
 
 MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, bool drop, int sms) {
@@ -182,8 +204,6 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, bool drop, int sms) {
   const size_t sk = up256(scales_bytes(M, K)), sn = up256(scales_bytes(M, N));
   size_t o = w.q_scales + (sk > sn ? sk : sn);
   if (r) {
-    w.t = o;
-    o += up256((size_t)M * r * 4);
     w.u = o;
     o += up256((size_t)M * r * 6);
     w.v = o;
@@ -191,13 +211,13 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, bool drop, int sms) {
     w.xm = o;
     if (drop) o += up256((size_t)M * K * 2);
     w.part = o;
-    w.t_fwd = plan_adapter(M, r, K, sms);
-    w.dt = plan_adapter(M, r, N, sms);
+    w.prep_x = plan_mx_prep(M, K, r, sms);
+    w.prep_dy = plan_mx_prep(M, N, r, sms);
     w.dl1 = plan_adapter(K, 3 * r, M, sms);
     w.dl2 = plan_adapter(N, 3 * r, M, sms);
     size_t part = 0;
-    for (const GemmPlan* p : {&w.t_fwd, &w.dt, &w.dl1, &w.dl2})
-      part = p->partial_bytes > part ? p->partial_bytes : part;
+    for (size_t b : {w.prep_x.part_bytes, w.prep_dy.part_bytes, w.dl1.partial_bytes, w.dl2.partial_bytes})
+      part = b > part ? b : part;
     o += up256(part);
   }
   w.total = o;
@@ -301,34 +321,13 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
   uint8_t* wb = static_cast<uint8_t*>(ws);
   uint16_t* sT = reinterpret_cast<uint16_t*>(wb + lay.u);
 
-  if (launch_mx_quantize(X, QLORA_DTYPE_BF16, M, K, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess)
-    return QLORA_ERR_CUDA;
   if (r) {
-    const uint16_t* Xa = X;  // the adapter's input, its dropped elements zero (the scale goes on T)
-    if (masked) {
-      DropArgs d1 = d;
-      d1.inv = 1.0f;
-      uint16_t* xm = reinterpret_cast<uint16_t*>(wb + lay.xm);
-      if (launch_dropout(X, QLORA_DTYPE_BF16, M * K, d1, xm, st) != cudaSuccess) return QLORA_ERR_CUDA;
-      Xa = xm;
-    }
-    EngineArgs a;
-    engine_args(&a, status_dev, M, r, K);
-    const GemmPlan& pt = lay.t_fwd;
-    if (map_operand(&a.tmA, Xa, 0, M, K, 128) || map_operand(&a.tmB, L1, 1, r, K, pt.BN)) return QLORA_ERR_CUDA;
-    a.b_mn_main = 1;
-    a.epi.out = T_save;
-    a.epi.alpha = d.inv;
-    a.epi.rs = r;
-    a.epi.cs = 1;
-    a.epi.out2 = sT;
-    a.epi.alpha2 = s * d.inv;
-    a.epi.rs2 = r;
-    a.epi.cs2 = 1;
     float* part = reinterpret_cast<float*>(wb + lay.part);
-    if (int rc = run_adapter(a, pt, part, st)) return rc;
-    if (pt.splits > 1 && launch_split_reduce(part, pt.splits, a.rows, a.cols, a.epi, st) != cudaSuccess)
+    if (int rc = prep(X, M, K, L1, 1, r, d, wb, wb + lay.q_scales, part, lay.prep_x, status_dev, st)) return rc;
+    if (launch_mx_prep_finish(lay.prep_x, part, M, r, T_save, d.inv, sT, 1, s * d.inv, st) != cudaSuccess)
       return QLORA_ERR_CUDA;
+  } else if (launch_mx_quantize(X, QLORA_DTYPE_BF16, M, K, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
+    return QLORA_ERR_CUDA;
   }
   const LoraTerm lora{sT, 0, L2, 1, r};
   return product(wb, wb + lay.q_scales, M, w->codes, w->scales, N, K, r ? &lora : nullptr, DropArgs{}, Y, 0,
@@ -357,28 +356,21 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* wb = static_cast<uint8_t*>(ws);
-  float* dT = reinterpret_cast<float*>(wb + lay.t);
   uint16_t* sdT = reinterpret_cast<uint16_t*>(wb + lay.u);
   uint16_t* sT = reinterpret_cast<uint16_t*>(wb + lay.v);
   float* part = reinterpret_cast<float*>(wb + lay.part);
 
-  // dT = dY.L2^T, then s dT / (1 - p) as three bf16 terms
+  // Q(dY) and dT = dY.L2^T, kept as three bf16 terms of s dT / (1 - p)
   if (r && (dX || dL1)) {
-    EngineArgs a;
-    engine_args(&a, status_dev, M, r, N);
-    const GemmPlan& p = lay.dt;
-    if (map_operand(&a.tmA, dY, 0, M, N, 128) || map_operand(&a.tmB, L2, 0, r, N, p.BN)) return QLORA_ERR_CUDA;
-    a.epi.out = dT;
-    a.epi.rs = r;
-    a.epi.cs = 1;
-    if (int rc = run_adapter(a, p, part, st)) return rc;
-    if (p.splits > 1 && launch_split_reduce(part, p.splits, a.rows, a.cols, a.epi, st) != cudaSuccess)
+    if (int rc = prep(dY, M, N, L2, 0, r, DropArgs{}, wb, wb + lay.q_scales, part, lay.prep_dy, status_dev, st))
+      return rc;
+    if (launch_mx_prep_finish(lay.prep_dy, part, M, r, nullptr, 0.0f, sdT, 3, s * d.inv, st) != cudaSuccess)
       return QLORA_ERR_CUDA;
-    if (launch_split3(dT, M, r, s * d.inv, sdT, st) != cudaSuccess) return QLORA_ERR_CUDA;
+  } else if (dX &&
+             launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
+    return QLORA_ERR_CUDA;
   }
   if (dX) {
-    if (launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess)
-      return QLORA_ERR_CUDA;
     const LoraTerm lora{sdT, (uint64_t)r * 6, L1, 0, r};
     if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d, dX, 0,
                          status_dev, di.sms, st))

@@ -1,0 +1,420 @@
+// One pass over the activations (forward) or the upstream gradient
+// (backward) of the MXFP4 linear layer:
+//
+//   Q(X): codes and scales of X [M][C], and
+//   D = drop(X) . L  [M][r]  (fp32), L = L1 [C][r] or L2^T with L2 [r][C].
+//
+// Both read all of X and little else, so the bound is X's bytes (2 a value
+// in, 0.53 out); two passes would read it twice, and a dropped copy of X
+// would be a third and fourth.  The tile of X comes to shared memory by TMA;
+// there the quantise warps read it once, write the codes and scales, and
+// zero the dropped elements in place, and the tensor cores take the same
+// tile as the A operand of D.
+//
+// Work is cut into units of 128 rows x 256 columns, taken in order by one CTA
+// per SM in equal runs (the last units of a row tile and the first of the
+// next may share a CTA).  A run's rows of D go to a partial slot; a small
+// second kernel adds the slots of a row tile in order and forms T, RNbf16(s T)
+// or the three bf16 terms of the scaled D.
+//
+// The tensor cores truncate their fp32 sums, an error that grows with their
+// length, so D is accumulated in pieces of 512 columns that are added with
+// rounding: two work accumulators in tensor memory that take turns, and the
+// sum beside them.
+//
+// Roles: warp 0 TMA producer, 1 MMA issuer, 2 stores codes and scales, 4-7 sum
+// D, 8-23 quantise (two groups of 8 warps, alternate 64-column stages; a
+// thread has one 32-block of one row).
+#include "engine_util.cuh"
+#include "mx_codec.cuh"
+#include "mx_util.cuh"
+#include "pair_util.cuh"
+#include "philox.cuh"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kPieces = 8;  // 64-column stages of a piece of D
+
+template <bool WIDE>  // r > 64
+struct PrepCfg {
+  static constexpr int S = WIDE ? 5 : 6;
+  static constexpr int L = WIDE ? 16384 : 8192;  // tile of L: 64 columns x up to 128 / 64 ranks
+  static constexpr int STAGE = 16384 + L;
+  static constexpr int OUT = S * STAGE;          // two staging buffers: 16 KB of codes, 1 KB of scales
+  static constexpr int OUTB = 16384 + 1024;
+  static constexpr int BAR = OUT + 2 * OUTB;
+  static constexpr int TOTAL = BAR + 512 + 1024;
+  static_assert(TOTAL <= 232448 && STAGE % 1024 == 0 && OUTB % 1024 == 0, "budget");
+};
+constexpr int kPrepThreads = 24 * 32;
+constexpr uint32_t kSumCol = 256;  // tensor memory: work accumulators at 0 and 128, the sum at 256
+
+QDEV void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"((uint64_t)m),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+QDEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+QDEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+QDEV void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+QDEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Units [lo, hi) of CTA c.
+__host__ __device__ inline int64_t prep_unit(int64_t units, int grid, int64_t c) { return c * units / grid; }
+// CTA that owns unit u.
+__host__ __device__ inline int prep_owner(int64_t units, int grid, int64_t u) {
+  return (int)(((u + 1) * grid - 1) / units);
+}
+
+template <bool WIDE>
+__global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_constant__ MxPrepArgs args) {
+  using C = PrepCfg<WIDE>;
+  constexpr int kS = C::S;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR);  // X and L tiles landed
+  uint64_t* ready = full + kS;    // 8 quantise warps have zeroed the dropped elements (dropout only)
+  uint64_t* empty = ready + kS;   // MMAs done (1) and 8 quantise warps have read the tile
+  uint64_t* ofull = empty + kS;   // staging buffer written: 8 warps x 4 stages
+  uint64_t* oempty = ofull + 2;   // ... and stored
+  uint64_t* wfull = oempty + 2;   // work accumulator holds a piece
+  uint64_t* wempty = wfull + 2;   // ... and has been added (4 warps)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+  const int64_t u_lo = prep_unit(args.units, (int)gridDim.x, blockIdx.x);
+  const int64_t u_hi = prep_unit(args.units, (int)gridDim.x, (int64_t)blockIdx.x + 1);
+  const int n_units = (int)(u_hi - u_lo);
+  const int upt = args.units_per_tile;
+  const bool drop = args.drop.threshold != 0;
+
+  if (tid == 0) {
+    for (int s = 0; s < kS; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(ready + s, 8);
+      mbar_init(empty + s, 9);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(ofull + b, 32);
+      mbar_init(oempty + b, 1);
+      mbar_init(wfull + b, 1);
+      mbar_init(wempty + b, 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&args.tmX);
+    tma_prefetch_desc(&args.tmL);
+    tma_prefetch_desc(&args.tmCodes);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const int lboxes = (args.r16 + 63) / 64;
+      const uint32_t lbytes = args.l_mn ? (uint32_t)lboxes * 8192u : (uint32_t)args.r16 * 128u;
+      int s = 0;
+      uint32_t ph = 0;
+      for (int u = 0; u < n_units; ++u) {
+        const int64_t uu = u_lo + u;
+        const int row0 = (int)(uu / upt) * 128, c0 = (int)(uu % upt) * 256;
+        bool ok = true;
+        for (int q = 0; q < 4; ++q) {
+          if (!(ok = mbar_wait(empty + s, ph ^ 1u, abort_flag, args.status))) break;
+          uint8_t* sx = smem + s * C::STAGE;
+          uint8_t* sl = sx + 16384;
+          const int c = c0 + 64 * q;
+          mbar_arrive_expect_tx(full + s, 16384u + lbytes);
+          tma_load_2d(sx, &args.tmX, full + s, c, row0);
+          if (args.l_mn) {
+            for (int j = 0; j < lboxes; ++j) tma_load_2d(sl + 8192 * j, &args.tmL, full + s, 64 * j, c);
+          } else {
+            tma_load_2d(sl, &args.tmL, full + s, c, 0);
+          }
+          if (++s == kS) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    const uint32_t idesc = idesc_bf16(128, 16, 0, args.l_mn) + ((uint32_t)((args.r16 - 16) >> 3) << 17);
+    const bool one = elect_one();
+    int s = 0, piece = 0, in_piece = 0;
+    uint32_t ph = 0;
+    for (int u = 0; u < n_units; ++u) {
+      const bool last = u + 1 == n_units || (int)((u_lo + u + 1) % upt) == 0;  // ends a row tile's run
+      bool ok = true;
+      for (int q = 0; q < 4; ++q) {
+        const int b = piece & 1;
+        if (in_piece == 0) {
+          if (!(ok = warp_poll(wempty + b, ((uint32_t)(piece >> 1) & 1u) ^ 1u, abort_flag, args.status, lane))) break;
+        }
+        if (!(ok = warp_poll((drop ? ready : full) + s, ph, abort_flag, args.status, lane))) break;
+        tc_fence_after();
+        if (one) {
+          const uint8_t* sx = smem + s * C::STAGE;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem + 128u * (uint32_t)b, operand_desc(sx, 0, kk), operand_desc(sx + 16384, args.l_mn, kk), idesc,
+                      (in_piece | kk) != 0);
+          umma_commit(empty + s);
+        }
+        __syncwarp();
+        ++in_piece;
+        if (in_piece == kPieces || (last && q == 3)) {
+          if (one) umma_commit(wfull + b);
+          __syncwarp();
+          in_piece = 0;
+          ++piece;
+        }
+        if (++s == kS) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+    }
+  } else if (warp == 2) {
+    // --------------------------------------------------- codes and scales out
+    if (lane == 0) {
+      for (int u = 0; u < n_units; ++u) {
+        const int b = u & 1;
+        if (!mbar_wait(ofull + b, (uint32_t)(u >> 1) & 1u, abort_flag, args.status)) break;
+        const int64_t uu = u_lo + u;
+        const int64_t rt = uu / upt;
+        const int kb = (int)(uu % upt);
+        const uint8_t* so = smem + C::OUT + b * C::OUTB;
+        tma_store_2d(&args.tmCodes, so, kb * 128, (int)(rt * 128));
+        bulk_store(args.scales + (rt * args.kt + 2 * kb) * 512, so + 16384, 512u * (uint32_t)min(2, args.kt - 2 * kb));
+        bulk_commit();
+        bulk_wait_read<0>();
+        mbar_arrive(oempty + b);
+      }
+      bulk_wait_all();
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------- sum of the pieces
+    const int q4 = warp & 3;
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    int piece = 0, in_piece = 0;
+    bool first = true;
+    for (int u = 0; u < n_units; ++u) {
+      const bool last = u + 1 == n_units || (int)((u_lo + u + 1) % upt) == 0;
+      in_piece += 4;
+      if (in_piece < kPieces && !last) continue;
+      const int b = piece & 1;
+      if (!warp_wait(wfull + b, (uint32_t)(piece >> 1) & 1u, abort_flag, args.status, lane)) break;
+      tc_fence_after();
+      float* dst = nullptr;
+      if (last) {  // this run's rows of D: the slot of (row tile, ordinal of this CTA in it)
+        const int64_t tile = (u_lo + u) / upt;
+        const int ord = (int)blockIdx.x - prep_owner(args.units, (int)gridDim.x, tile * upt);
+        dst = args.part + ((tile * args.maxc + ord) * 128 + q4 * 32 + lane) * args.r;
+      }
+      for (int c = 0; c < args.r16; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tl + 128u * (uint32_t)b + (uint32_t)c, v);
+        if (!first) {
+          uint32_t m[16];
+          tmem_ld16(tl + kSumCol + (uint32_t)c, m);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(m[j])));
+        } else {
+          tmem_wait_ld();
+        }
+        if (!last) {
+          tmem_st16(tl + kSumCol + (uint32_t)c, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            if (c + j < args.r)
+              *reinterpret_cast<uint4*>(dst + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wempty + b);
+      first = last;
+      in_piece = 0;
+      ++piece;
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ quantise
+    const int grp = (warp - 8) >> 3, t = tid & 255;
+    const int rl = t & 127, half = t >> 7;
+    const PhiloxKey key = drop ? philox_key(args.drop) : PhiloxKey{0, 0, 0, 0};
+    bool bad = false;
+    for (int u = 0; u < n_units; ++u) {
+      const int64_t uu = u_lo + u;
+      const int64_t row = (uu / upt) * 128 + rl;
+      const int ob = u & 1;
+      uint8_t* so = smem + C::OUT + ob * C::OUTB;
+      if (!warp_wait(oempty + ob, ((uint32_t)(u >> 1) & 1u) ^ 1u, abort_flag, args.status, lane)) break;
+      bool ok = true;
+#pragma unroll 1
+      for (int q = grp; q < 4; q += 2) {
+        const int it = 4 * u + q, s = it % kS;
+        if (!(ok = warp_wait(full + s, (uint32_t)(it / kS) & 1u, abort_flag, args.status, lane))) break;
+        uint8_t* sx = smem + s * C::STAGE + rl * 128;
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 v = *reinterpret_cast<const uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4));
+          w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+        }
+        if (drop) {
+          const int64_t e = row * args.cols + (uu % upt) * 256 + 64 * q + 32 * half;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t k = keep8((uint64_t)e / 8 + j, key, args.drop.threshold);
+            uint32_t z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              z[i] = w[4 * j + i] & (((k >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((k >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u));
+            *reinterpret_cast<uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+        }
+        fence_proxy_async_smem();  // these reads and writes before the MMAs and the TMA refill
+        __syncwarp();
+        if (lane == 0) {
+          if (drop) mbar_arrive(ready + s);
+          mbar_arrive(empty + s);
+        }
+        uint32_t m2 = 0;  // largest |x| bits, two 16-bit lanes
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m2 = __vmaxu2(m2, w[j] & 0x7FFF7FFFu);
+        const uint32_t b = mx_scale_byte(max(m2 & 0xFFFFu, m2 >> 16) << 16);
+        bad |= b == 255u;
+        const float f = mx_inv_scale(b);
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          c[j] = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[j] |= mx_codes2(w[4 * j + i], f) << (8 * i);
+        }
+        const int blk = 2 * q + half;  // 32-block of the unit
+        *reinterpret_cast<uint4*>(so + rl * 128 + ((blk ^ (rl & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
+        so[16384 + (blk >> 2) * 512 + (rl & 31) * 16 + (rl >> 5) * 4 + (blk & 3)] = (uint8_t)b;
+        fence_proxy_async_smem();  // before the TMA store reads the staging buffer
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ofull + ob);
+      }
+      if (!ok) break;
+    }
+    if (bad) report(args.status, QLORA_ERR_NONFINITE);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    if (tid == 0) {  // error path: let loads and MMAs still in flight finish
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 2000000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// D from the partial slots of its row tile, in order: T = alpha D (fp32, when
+// asked for) and `terms` bf16 terms of beta D, [M][terms * r].
+__global__ void __launch_bounds__(256) mx_prep_finish_kernel(MxPrepFinish a) {
+  const int64_t n = a.M * a.r;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / a.r, tile = m >> 7;
+    const int j = (int)(i - m * a.r);
+    const int c0 = prep_owner(a.units, a.grid, tile * a.units_per_tile);
+    const int c1 = prep_owner(a.units, a.grid, (tile + 1) * a.units_per_tile - 1);
+    const float* p = a.part + ((tile * a.maxc) * 128 + (m & 127)) * a.r + j;
+    float d = p[0];
+    for (int c = 1; c <= c1 - c0; ++c) d = __fadd_rn(d, p[(int64_t)c * 128 * a.r]);
+    if (a.T) a.T[i] = __fmul_rn(d, a.alpha);
+    float v = __fmul_rn(d, a.beta);
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + m * a.terms * a.r + j;
+    for (int t = 0; t < a.terms; ++t) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      o[(int64_t)t * a.r] = h;
+      v = __fsub_rn(v, __bfloat162float(h));
+    }
+  }
+}
+
+}  // namespace
+
+MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms) {
+  MxPrepPlan p{};
+  p.units_per_tile = (int)((C + 255) / 256);
+  const int64_t tiles = (M + 127) / 128;
+  p.units = tiles * p.units_per_tile;
+  p.grid = (int)(p.units < num_sms ? p.units : num_sms);
+  const int64_t per = p.units / p.grid;  // the least units of a CTA
+  p.maxc = (int)((p.units_per_tile + per - 1) / per) + 1;
+  if (p.maxc > p.grid) p.maxc = p.grid;
+  p.part_bytes = (size_t)tiles * p.maxc * 128 * r * sizeof(float);
+  return p;
+}
+
+cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) {
+  a.units = p.units;
+  a.units_per_tile = p.units_per_tile;
+  a.maxc = p.maxc;
+  a.r16 = (a.r + 15) / 16 * 16;
+  const bool wide = a.r > 64;
+  const int smem = wide ? PrepCfg<true>::TOTAL : PrepCfg<false>::TOTAL;
+  auto kern = wide ? mx_prep_kernel<true> : mx_prep_kernel<false>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  kern<<<p.grid, kPrepThreads, smem, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, const float* part, int64_t M, int r, float* T, float alpha,
+                                  uint16_t* out, int terms, float beta, cudaStream_t st) {
+  MxPrepFinish a{};
+  a.part = part;
+  a.M = M;
+  a.r = r;
+  a.units = p.units;
+  a.units_per_tile = p.units_per_tile;
+  a.grid = p.grid;
+  a.maxc = p.maxc;
+  a.T = T;
+  a.alpha = alpha;
+  a.out = out;
+  a.terms = terms;
+  a.beta = beta;
+  const int64_t want = (M * r + 255) / 256;
+  mx_prep_finish_kernel<<<(unsigned)(want < 2368 ? want : 2368), 256, 0, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace qnf4

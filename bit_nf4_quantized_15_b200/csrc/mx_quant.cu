@@ -13,10 +13,10 @@
 // in a tile the scale of row i, block j is byte (i % 32) * 16 + (i / 32) * 4
 // + j.  A tile goes from global to tensor memory without being rearranged.
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 
 #include "common.cuh"
 #include "internal.h"
+#include "mx_codec.cuh"
 #include "philox.cuh"
 
 namespace qnf4 {
@@ -55,23 +55,10 @@ QDEV float load1(const void* base, int64_t i) {
   else return __half2float(reinterpret_cast<const __half*>(base)[i]);
 }
 
-// Scale byte of a block from the largest |x| bits (Inf and NaN included: their
-// exponent field is 255 and their bits compare above every finite value's).
-QDEV uint32_t scale_byte(uint32_t maxbits) {
-  const uint32_t e = maxbits >> 23;
-  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
-}
-// 2^(127 - b): exact in fp32 for every b that a finite block has (b <= 252).
-QDEV float inv_scale(uint32_t b) { return __uint_as_float((254u - (b > 252u ? 127u : b)) << 23); }
-
-QDEV uint32_t codes2(float lo, float hi) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
-}
-
 QDEV uint32_t codes8(const float (&v)[8], float f) {
   uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w |= codes2(__fmul_rn(v[2 * j], f), __fmul_rn(v[2 * j + 1], f)) << (8 * j);
+  for (int j = 0; j < 4; ++j) w |= mx_codes(__fmul_rn(v[2 * j], f), __fmul_rn(v[2 * j + 1], f)) << (8 * j);
   return w;
 }
 
@@ -113,9 +100,9 @@ __global__ void __launch_bounds__(kQT) mx_quantize_kernel(const void* __restrict
     for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t b = scale_byte(m);
+    const uint32_t b = mx_scale_byte(m);
     bad |= b == 255u;
-    const uint32_t w = codes8(v[i], inv_scale(b));
+    const uint32_t w = codes8(v[i], mx_inv_scale(b));
     if (cok && row < rows) {
       reinterpret_cast<uint32_t*>(codes)[(row * cols + col) >> 3] = w;
       if ((t & 3) == 0) s_sc[(rl & 31) * 16 + (rl >> 5) * 4 + ((t & 15) >> 2)] = (uint8_t)b;
@@ -173,9 +160,9 @@ __global__ void __launch_bounds__(kQT) mx_quantize_t_kernel(const void* __restri
       v[j] = s_x[(blk * 32 + j) * kTP + cl];
       m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
-    const uint32_t b = scale_byte(m);
+    const uint32_t b = mx_scale_byte(m);
     bad |= b == 255u;
-    const float f = inv_scale(b);
+    const float f = mx_inv_scale(b);
     uint32_t w[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
