@@ -343,12 +343,35 @@ cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st);
 cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, const float* part, int64_t M, int r, float* T, float alpha,
                                   uint16_t* out, int terms, float beta, cudaStream_t st);
 
-// ------------------------------------------- adapter side of the MX linear
+// Adapter gradients (mx_grad.cu): problem 0 is dL1 = drop(X)^T.u, problem 1
+// dL2 = (dY^T.v)^T, either may be absent (cols 0).
+struct MxGradProblem {
+  CUtensorMap tmZ;  // X or dY, bf16 [M][cols], box 64 x 64, 128-byte swizzle
+  CUtensorMap tmV;  // bf16 [M][3r], the same box
+  int64_t cols;
+  int transposed;   // out is [r][cols], else [cols][r]
+  float* part;
+  float* out;
+};
+struct MxGradPlan {
+  int64_t units0, units;  // 128 columns x 512 tokens: of problem 0, of both
+  int pieces, grid, maxc, n16, nbuf, vboxes, stages;
+  size_t part0_bytes, part_bytes;
+};
+struct MxGradArgs {
+  MxGradProblem p[2];
+  int M, r;
+  int64_t units0, units;
+  int pieces, maxc;
+  int n16, nbuf;       // columns of an accumulator (3r up to 16), accumulators
+  int vboxes, stages;
+  DropArgs drop;       // mask of X
+  int* status;
+};
+MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, int num_sms);
+cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st);
+
 // scale * in [M][r] as three bf16 terms [M][3r] (their sum is exact in fp32).
 cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st);
-// out[row * rs + j * cs] = sum of the 3 terms' columns j, r + j, 2r + j over
-// the splits; partial fp32 [splits][3r][rows].
-cudaError_t launch_sum3(const float* partial, int splits, int rows, int r, float* out, int64_t rs, int64_t cs,
-                        cudaStream_t st);
 
 }  // namespace qnf4

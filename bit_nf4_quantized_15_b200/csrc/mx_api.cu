@@ -49,37 +49,6 @@ int drop_args(const qlora_dropout_config* c, DropArgs* d) {
   return QLORA_OK;
 }
 
-// The tensor cores' fp32 accumulation truncates, an error that grows with
-// the length of the sum (measured on normal data: 3.8e-7 of the result after
-// 410 terms, 1.1e-6 after 1024, 1.65e-6 after 1638; fp32 arithmetic with
-// rounding has 0.2 to 1e-6).  The adapter sums are fp32 results, so they run
-// in pieces of at most kAdapterSum terms that are added with rounding.
-constexpr int kAdapterSum = 512;
-
-GemmPlan plan_adapter(int64_t rows, int cols, int64_t red, int sms) {
-  const int kb = (int)((red + 63) / 64);
-  GemmPlan p = plan_gemm((int)rows, cols, kb, sms);
-  const int need = (int)((red + kAdapterSum - 1) / kAdapterSum);
-  if (p.splits < need) p.splits = need;
-  p.partial_bytes = (size_t)p.splits * (size_t)rows * cols * sizeof(float);
-  return p;
-}
-
-int run_adapter(EngineArgs& a, const GemmPlan& p, float* partial, cudaStream_t st) {
-  a.splits = p.splits;
-  a.partial = partial;
-  return launch_engine(a, A_TMA, p, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
-}
-
-void engine_args(EngineArgs* a, int* status, int64_t rows, int cols, int64_t red) {
-  std::memset(a, 0, sizeof(*a));
-  a->status = status;
-  a->rows = (int)rows;
-  a->cols = cols;
-  a->kb_main = (int)((red + 63) / 64);
-  a->epi.alpha = a->epi.alpha2 = 1.0f;
-}
-
 // The LoRA term of a product: u [M][r] bf16 (rows `u_pitch` bytes apart) times
 // the feature side v, MN-major ([r][features]) or K-major ([features][r]).
 struct LoraTerm {
@@ -189,15 +158,13 @@ int prep(const uint16_t* X, int64_t M, int64_t C, const uint16_t* L, int l_mn, i
 //   q      MXFP4 of X (forward) or dY (backward): codes, then scales
 //   u, v   bf16 [M][3r]: the scaled dT (u) and s T (v) in three terms, the
 //          first RNbf16; the forward keeps RNbf16(s T) in u
-//   xm     bf16 [M][K]: X with the dropped elements zeroed
 //   part   fp32 partial sums of the adapter products
 struct MxWs {
-  size_t q_scales, u, v, xm, part, total;
+  size_t q_scales, u, v, part, total;
   MxPrepPlan prep_x, prep_dy;
-  GemmPlan dl1, dl2;
 };
 
-MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, bool drop, int sms) {
+MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms) {
   MxWs w{};
   const size_t qk = up256(codes_bytes(M, K)), qn = up256(codes_bytes(M, N));
   w.q_scales = qk > qn ? qk : qn;
@@ -208,15 +175,12 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, bool drop, int sms) {
     o += up256((size_t)M * r * 6);
     w.v = o;
     o += up256((size_t)M * r * 6);
-    w.xm = o;
-    if (drop) o += up256((size_t)M * K * 2);
     w.part = o;
     w.prep_x = plan_mx_prep(M, K, r, sms);
     w.prep_dy = plan_mx_prep(M, N, r, sms);
-    w.dl1 = plan_adapter(K, 3 * r, M, sms);
-    w.dl2 = plan_adapter(N, 3 * r, M, sms);
     size_t part = 0;
-    for (size_t b : {w.prep_x.part_bytes, w.prep_dy.part_bytes, w.dl1.partial_bytes, w.dl2.partial_bytes})
+    for (size_t b : {w.prep_x.part_bytes, w.prep_dy.part_bytes, plan_mx_grad(M, K, N, r, sms).part_bytes,
+                     plan_mx_grad(M, K, 0, r, sms).part_bytes, plan_mx_grad(M, 0, N, r, sms).part_bytes})
       part = b > part ? b : part;
     o += up256(part);
   }
@@ -294,11 +258,11 @@ int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_confi
                                                                                                     : QLORA_ERR_CUDA;
 }
 
-size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int dropout) {
+size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
   if (!linear_shape_ok(M, N, K, 8) || !rank_ok(r)) return 0;
   DevInfo di;
   if (current_device_info(&di)) di.sms = 148;
-  return mx_ws(M, N, K, r, dropout != 0, di.sms).total;
+  return mx_ws(M, N, K, r, di.sms).total;
 }
 
 int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, const uint16_t* L1,
@@ -314,8 +278,7 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
   if (!all16({X, w->codes, w->scales, L1, L2, Y, T_save, ws})) return QLORA_ERR_ALIGN;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  const bool masked = r && d.threshold;
-  const MxWs lay = mx_ws(M, N, K, r, masked, di.sms);
+  const MxWs lay = mx_ws(M, N, K, r, di.sms);
   if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* wb = static_cast<uint8_t*>(ws);
@@ -351,8 +314,7 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   if (dX && !all16({wt->codes, wt->scales})) return QLORA_ERR_ALIGN;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  const bool masked = r && d.threshold;
-  const MxWs lay = mx_ws(M, N, K, r, masked, di.sms);
+  const MxWs lay = mx_ws(M, N, K, r, di.sms);
   if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* wb = static_cast<uint8_t*>(ws);
@@ -376,38 +338,27 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
                          status_dev, di.sms, st))
       return rc;
   }
-  if (dL1) {
-    const uint16_t* Xa = X;
-    if (masked) {
-      DropArgs d1 = d;
-      d1.inv = 1.0f;
-      uint16_t* xm = reinterpret_cast<uint16_t*>(wb + lay.xm);
-      if (launch_dropout(X, QLORA_DTYPE_BF16, M * K, d1, xm, st) != cudaSuccess) return QLORA_ERR_CUDA;
-      Xa = xm;
-    }
-    EngineArgs a;
-    engine_args(&a, status_dev, K, 3 * r, M);
-    const GemmPlan& p = lay.dl1;
-    if (map_operand(&a.tmA, Xa, 1, K, M, 128) || map_operand(&a.tmB, sdT, 1, 3 * r, M, p.BN)) return QLORA_ERR_CUDA;
-    a.a_mn_main = a.b_mn_main = 1;
-    a.epi.out = part;  // one split: the same [3r][rows] layout
-    a.epi.rs = 1;
-    a.epi.cs = K;
-    if (int rc = run_adapter(a, p, part, st)) return rc;
-    if (launch_sum3(part, p.splits, (int)K, r, dL1, r, 1, st) != cudaSuccess) return QLORA_ERR_CUDA;
-  }
-  if (dL2) {
-    if (launch_split3(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
-    EngineArgs a;
-    engine_args(&a, status_dev, N, 3 * r, M);
-    const GemmPlan& p = lay.dl2;
-    if (map_operand(&a.tmA, dY, 1, N, M, 128) || map_operand(&a.tmB, sT, 1, 3 * r, M, p.BN)) return QLORA_ERR_CUDA;
-    a.a_mn_main = a.b_mn_main = 1;
-    a.epi.out = part;
-    a.epi.rs = 1;
-    a.epi.cs = N;
-    if (int rc = run_adapter(a, p, part, st)) return rc;
-    if (launch_sum3(part, p.splits, (int)N, r, dL2, 1, N, st) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (dL1 || dL2) {
+    if (dL2 && launch_split3(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    const MxGradPlan p = plan_mx_grad(M, dL1 ? K : 0, dL2 ? N : 0, r, di.sms);
+    MxGradArgs a;
+    std::memset(&a, 0, sizeof(a));
+    if (dL1 && (map_operand(&a.p[0].tmZ, X, 1, K, M, 64) || map_operand(&a.p[0].tmV, sdT, 1, 3 * r, M, 64)))
+      return QLORA_ERR_CUDA;
+    if (dL2 && (map_operand(&a.p[1].tmZ, dY, 1, N, M, 64) || map_operand(&a.p[1].tmV, sT, 1, 3 * r, M, 64)))
+      return QLORA_ERR_CUDA;
+    a.p[0].cols = K;
+    a.p[0].part = part;
+    a.p[0].out = dL1;
+    a.p[1].cols = N;
+    a.p[1].transposed = 1;
+    a.p[1].part = part + p.part0_bytes / sizeof(float);
+    a.p[1].out = dL2;
+    a.M = (int)M;
+    a.r = r;
+    a.drop = d;
+    a.status = status_dev;
+    if (launch_mx_grad(a, p, st) != cudaSuccess) return QLORA_ERR_CUDA;
   }
   return QLORA_OK;
 }

@@ -350,19 +350,6 @@ __global__ void split3_kernel(const float* __restrict__ in, int64_t n, int r, fl
   }
 }
 
-__global__ void sum3_kernel(const float* __restrict__ p, int splits, int rows, int r, float* __restrict__ out,
-                            int64_t rs, int64_t cs) {
-  const int64_t n = (int64_t)rows * r;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i % rows, j = i / rows;
-    float t[3] = {0.0f, 0.0f, 0.0f};
-    for (int z = 0; z < splits; ++z)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) t[k] += p[((int64_t)(3 * z + k) * r + j) * rows + row];
-    out[row * rs + j * cs] = t[0] + (t[1] + t[2]);
-  }
-}
-
 }  // namespace
 
 MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms) {
@@ -401,13 +388,6 @@ static int small_grid(int64_t n) {
 
 cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {
   split3_kernel<<<small_grid(M * r), 256, 0, st>>>(in, M * r, r, scale, reinterpret_cast<__nv_bfloat16*>(out));
-  count_launches(1);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_sum3(const float* partial, int splits, int rows, int r, float* out, int64_t rs, int64_t cs,
-                        cudaStream_t st) {
-  sum3_kernel<<<small_grid((int64_t)rows * r), 256, 0, st>>>(partial, splits, rows, r, out, rs, cs);
   count_launches(1);
   return cudaGetLastError();
 }

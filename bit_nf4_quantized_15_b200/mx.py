@@ -46,7 +46,7 @@ SIGS = {
     "qlora_mx_dequant": (_INT, [_T, _P, _INT, _P]),
     "qlora_mx_matmul": (_INT, [_T, _T, _P, _INT, _P, _P]),
     "qlora_dropout": (_INT, [_P, _INT, _I64, _D, _P, _P]),
-    "qlora_mx_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT, _INT]),
+    "qlora_mx_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT]),
     "qlora_mx_linear_fwd": (_INT, [_P, _I64, _T, _P, _P, _INT, ctypes.c_float, _D, _P, _P, _P, _SZ, _P, _P]),
     "qlora_mx_linear_bwd": (_INT, [_P, _P, _I64, _P, _T, _I64, _I64, _P, _P, _INT, ctypes.c_float, _D, _P, _P, _P, _P,
                                    _SZ, _P, _P]),
@@ -213,9 +213,9 @@ def mx_weight(W, backward: bool = True, status=None) -> MXWeight:
     return MXWeight(mx_quantize(W, status=status), mx_quantize(W, transpose=True, status=status) if backward else None)
 
 
-def mx_linear_workspace_bytes(M: int, N: int, K: int, r: int = 0, dropout: bool = False) -> int:
+def mx_linear_workspace_bytes(M: int, N: int, K: int, r: int = 0) -> int:
     """Workspace of mx_linear_fwd and mx_linear_bwd (the larger of the two)."""
-    n = _q.lib().qlora_mx_linear_workspace_bytes(M, N, K, r, int(dropout))
+    n = _q.lib().qlora_mx_linear_workspace_bytes(M, N, K, r)
     _need(n, "invalid shape or rank for mx_linear_workspace_bytes")
     return n
 
@@ -229,7 +229,7 @@ def _linear_args(M, N, K, L1, L2, dropout, ws, device):
         _tensor(L1, "L1", (K, r), torch.bfloat16, device)
         _tensor(L2, "L2", (r, N), torch.bfloat16, device)
     cfg = dropout.config(device) if dropout is not None else None
-    need = mx_linear_workspace_bytes(M, N, K, r, cfg is not None and cfg.p > 0)
+    need = mx_linear_workspace_bytes(M, N, K, r)
     if ws is None:
         ws = torch.empty(need, dtype=torch.uint8, device=device)
     _need(ws.is_cuda and ws.device == device and ws.is_contiguous() and ws.numel() * ws.element_size() >= need,

@@ -385,9 +385,9 @@ QLORA_API int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dro
                             qlora_stream_t stream);
 
 /* Workspace bytes of qlora_mx_linear_fwd and qlora_mx_linear_bwd (the maximum
- * of both) for M tokens, an N x K weight, rank r (0: no adapter) and dropout
- * on the adapter's input or not.  0 for an invalid shape. */
-QLORA_API size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int dropout);
+ * of both) for M tokens, an N x K weight and rank r (0: no adapter).  0 for
+ * an invalid shape. */
+QLORA_API size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
 
 /*
  * Forward of the LoRA linear layer on an MXFP4 weight W^ [N][K]:

@@ -268,7 +268,7 @@ def test_linear_optional_outputs_and_workspace(lib):
     M, N, K, r = 100, 96, 160, 16
     X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=4)
     drop = lib.Dropout(0.1, 1, 2)
-    ws = torch.full((lib.mx_linear_workspace_bytes(M, N, K, r, True),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((lib.mx_linear_workspace_bytes(M, N, K, r),), 255, dtype=torch.uint8, device="cuda")
     Y, T = lib.mx_linear_fwd(X, w, L1, L2, 0.5, dropout=drop)
     Y2, T2 = lib.mx_linear_fwd(X, w, L1, L2, 0.5, dropout=drop, ws=ws)
     assert torch.equal(Y, Y2) and torch.equal(T, T2)
