@@ -51,5 +51,16 @@ QDEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, in
   return ok != 0;
 }
 
+// The same for a warp off the critical path: it sleeps between polls, so that
+// its spinning takes no issue slots from the warps that work.
+QDEV bool warp_wait_backoff(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status, int lane,
+                            uint32_t sleep_ns) {
+  int ok = 1;
+  if (lane == 0) ok = mbar_wait_backoff(bar, parity, abort_flag, status, sleep_ns) ? 1 : 0;
+  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  if (ok) mbar_test_wait(smem_u32(bar), parity);
+  return ok != 0;
+}
+
 }  // namespace
 }  // namespace qnf4

@@ -332,16 +332,22 @@ struct MxPrepArgs {
 };
 struct MxPrepFinish {
   const float* part;
-  int64_t M, units;
-  int r, units_per_tile, grid, maxc, terms;
-  float* T;
-  float alpha, beta;
-  uint16_t* out;
+  int64_t M;
+  int r;
+  float* T;            // alpha D (may be null)
+  float alpha;
+  uint16_t* out;       // `terms` bf16 terms of beta D
+  int terms;
+  float beta;
+  const float* T_in;   // when not null: out2 = three bf16 terms of gamma T_in
+  uint16_t* out2;
+  float gamma;
+  int64_t units;       // filled by the launch
+  int units_per_tile, grid, maxc;
 };
 MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms);
 cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st);
-cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, const float* part, int64_t M, int r, float* T, float alpha,
-                                  uint16_t* out, int terms, float beta, cudaStream_t st);
+cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, MxPrepFinish a, cudaStream_t st);
 
 // Adapter gradients (mx_grad.cu): problem 0 is dL1 = drop(X)^T.u, problem 1
 // dL2 = (dY^T.v)^T, either may be absent (cols 0).
@@ -353,22 +359,26 @@ struct MxGradProblem {
   float* part;
   float* out;
 };
-struct MxGradPlan {
+struct MxGradShare {  // how the units are shared out
   int64_t units0, units;  // 128 columns x 512 tokens: of problem 0, of both
-  int pieces, grid, maxc, n16, nbuf, vboxes, stages;
+  int w0, grid;           // cost of a unit of problem 0 (the other's: 2), CTAs
+};
+struct MxGradPlan {
+  MxGradShare sh;
+  int pieces, maxc, n16, nbuf, vboxes, stages;
   size_t part0_bytes, part_bytes;
 };
 struct MxGradArgs {
   MxGradProblem p[2];
   int M, r;
-  int64_t units0, units;
+  MxGradShare sh;
   int pieces, maxc;
   int n16, nbuf;       // columns of an accumulator (3r up to 16), accumulators
   int vboxes, stages;
   DropArgs drop;       // mask of X
   int* status;
 };
-MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, int num_sms);
+MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool drop, int num_sms);
 cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st);
 
 // scale * in [M][r] as three bf16 terms [M][3r] (their sum is exact in fp32).

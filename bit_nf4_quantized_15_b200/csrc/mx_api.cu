@@ -68,15 +68,15 @@ int map_scales(CUtensorMap* m, const uint8_t* scales, int64_t rows, int64_t K, i
 // out [M][N] = x w^T (+ the LoRA term), x = (xc, xs) the tokens, w = (wc, ws)
 // the features.
 //
-// CTA pairs when their 256 x 256 tiles fill the machine, else tiles of 128
-// features split over clusters.
+// CTA pairs when their 256 x 256 tiles fill the machine and are mostly tokens,
+// else tiles of 128 features split over clusters.
 int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, const uint8_t* ws, int64_t N,
             int64_t K, const LoraTerm* lora, const DropArgs& drop, void* out, int out_f32, int* status, int sms,
             cudaStream_t st) {
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t stall_ns = take_stall_request();
-  if (((M + 255) / 256) * ((N + 255) / 256) >= sms / 2 && !stall_ns) {
+  if (M > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= sms / 2 && !stall_ns) {
     MxPairArgs g;
     std::memset(&g, 0, sizeof(g));
     if (make_map(&g.tmA, xc, u8, 1, (uint64_t)K / 2, (uint64_t)M, 128, 128, sw) ||
@@ -179,9 +179,12 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms) {
     w.prep_x = plan_mx_prep(M, K, r, sms);
     w.prep_dy = plan_mx_prep(M, N, r, sms);
     size_t part = 0;
-    for (size_t b : {w.prep_x.part_bytes, w.prep_dy.part_bytes, plan_mx_grad(M, K, N, r, sms).part_bytes,
-                     plan_mx_grad(M, K, 0, r, sms).part_bytes, plan_mx_grad(M, 0, N, r, sms).part_bytes})
+    for (size_t b : {w.prep_x.part_bytes, w.prep_dy.part_bytes})
       part = b > part ? b : part;
+    for (int i = 0; i < 6; ++i) {  // dL1 and dL2 or one of them, with dropout or without
+      const size_t b = plan_mx_grad(M, i % 3 == 2 ? 0 : K, i % 3 == 1 ? 0 : N, r, i >= 3, sms).part_bytes;
+      part = b > part ? b : part;
+    }
     o += up256(part);
   }
   w.total = o;
@@ -287,8 +290,17 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
   if (r) {
     float* part = reinterpret_cast<float*>(wb + lay.part);
     if (int rc = prep(X, M, K, L1, 1, r, d, wb, wb + lay.q_scales, part, lay.prep_x, status_dev, st)) return rc;
-    if (launch_mx_prep_finish(lay.prep_x, part, M, r, T_save, d.inv, sT, 1, s * d.inv, st) != cudaSuccess)
-      return QLORA_ERR_CUDA;
+    MxPrepFinish f;
+    std::memset(&f, 0, sizeof(f));
+    f.part = part;
+    f.M = M;
+    f.r = r;
+    f.T = T_save;
+    f.alpha = d.inv;
+    f.out = sT;
+    f.terms = 1;
+    f.beta = s * d.inv;
+    if (launch_mx_prep_finish(lay.prep_x, f, st) != cudaSuccess) return QLORA_ERR_CUDA;
   } else if (launch_mx_quantize(X, QLORA_DTYPE_BF16, M, K, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
     return QLORA_ERR_CUDA;
   }
@@ -322,12 +334,23 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   uint16_t* sT = reinterpret_cast<uint16_t*>(wb + lay.v);
   float* part = reinterpret_cast<float*>(wb + lay.part);
 
-  // Q(dY) and dT = dY.L2^T, kept as three bf16 terms of s dT / (1 - p)
+  // Q(dY) and dT = dY.L2^T, kept as three bf16 terms of s dT / (1 - p); with
+  // them s T in three terms
   if (r && (dX || dL1)) {
     if (int rc = prep(dY, M, N, L2, 0, r, DropArgs{}, wb, wb + lay.q_scales, part, lay.prep_dy, status_dev, st))
       return rc;
-    if (launch_mx_prep_finish(lay.prep_dy, part, M, r, nullptr, 0.0f, sdT, 3, s * d.inv, st) != cudaSuccess)
-      return QLORA_ERR_CUDA;
+    MxPrepFinish f;
+    std::memset(&f, 0, sizeof(f));
+    f.part = part;
+    f.M = M;
+    f.r = r;
+    f.out = sdT;
+    f.terms = 3;
+    f.beta = s * d.inv;
+    f.T_in = dL2 ? T_saved : nullptr;
+    f.out2 = sT;
+    f.gamma = s;
+    if (launch_mx_prep_finish(lay.prep_dy, f, st) != cudaSuccess) return QLORA_ERR_CUDA;
   } else if (dX &&
              launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
     return QLORA_ERR_CUDA;
@@ -339,8 +362,8 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
       return rc;
   }
   if (dL1 || dL2) {
-    if (dL2 && launch_split3(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
-    const MxGradPlan p = plan_mx_grad(M, dL1 ? K : 0, dL2 ? N : 0, r, di.sms);
+    if (dL2 && !dX && !dL1 && launch_split3(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    const MxGradPlan p = plan_mx_grad(M, dL1 ? K : 0, dL2 ? N : 0, r, d.threshold != 0, di.sms);
     MxGradArgs a;
     std::memset(&a, 0, sizeof(a));
     if (dL1 && (map_operand(&a.p[0].tmZ, X, 1, K, M, 64) || map_operand(&a.p[0].tmV, sdT, 1, 3 * r, M, 64)))

@@ -334,22 +334,6 @@ cudaError_t launch_bn(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st)
   return cudaGetLastError();
 }
 
-// ------------------------------------------------ adapter-side small kernels
-// fp32 as three bf16 terms: 8 + 8 + 8 significant bits hold all 24.
-__global__ void split3_kernel(const float* __restrict__ in, int64_t n, int r, float scale,
-                              __nv_bfloat16* __restrict__ out) {
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    __nv_bfloat16* o = out + i + i / r * 2 * r;
-    float v = __fmul_rn(in[i], scale);
-#pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      const __nv_bfloat16 h = __float2bfloat16_rn(v);
-      o[t * r] = h;
-      v = __fsub_rn(v, __bfloat162float(h));
-    }
-  }
-}
-
 }  // namespace
 
 MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms) {
@@ -379,17 +363,6 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_
     case 256: return launch_bn<256>(a, p, st);
   }
   return cudaErrorInvalidValue;
-}
-
-static int small_grid(int64_t n) {
-  const int64_t want = (n + 255) / 256;
-  return (int)(want < 2368 ? (want > 0 ? want : 1) : 2368);
-}
-
-cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {
-  split3_kernel<<<small_grid(M * r), 256, 0, st>>>(in, M * r, r, scale, reinterpret_cast<__nv_bfloat16*>(out));
-  count_launches(1);
-  return cudaGetLastError();
 }
 
 }  // namespace qnf4

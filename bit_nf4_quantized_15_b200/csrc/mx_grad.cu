@@ -16,7 +16,7 @@
 //
 // With dropout the X tile is masked in shared memory before the MMAs read it.
 //
-// Roles: warp 0 TMA producer, 1 MMA issuer, 4-7 sum, 8-15 mask.
+// Roles: warp 0 TMA producer, 1 MMA issuer, 4-7 sum, 8-23 mask.
 #include "engine_util.cuh"
 #include "mx_util.cuh"
 #include "pair_util.cuh"
@@ -25,12 +25,24 @@
 namespace qnf4 {
 namespace {
 
-constexpr int kGThreads = 16 * 32;
+constexpr int kGThreads = 24 * 32;
 constexpr int kGMaxS = 6;
 constexpr int kGBudget = 220 * 1024;  // bytes of the stages
 constexpr int kGPiece = 8;            // 64-token stages of a unit
 
-QDEV int grad_owner(int64_t units, int grid, int64_t u) { return (int)(((u + 1) * grid - 1) / units); }
+// Runs are equal in cost: a unit of dL1 with dropout counts 3, others 2 (the
+// mask takes about as long as half a unit's loads).  CTA of a unit, and the
+// first unit of a CTA.
+__host__ __device__ inline int64_t grad_cost(const MxGradShare& a, int64_t u) {
+  return u < a.units0 ? u * a.w0 : a.units0 * a.w0 + (u - a.units0) * 2;
+}
+__host__ __device__ inline int grad_owner(const MxGradShare& a, int64_t u) {
+  return (int)(grad_cost(a, u) * a.grid / grad_cost(a, a.units));
+}
+__host__ __device__ inline int64_t grad_first(const MxGradShare& a, int64_t c) {
+  const int64_t x = (c * grad_cost(a, a.units) + a.grid - 1) / a.grid, x0 = a.units0 * a.w0;
+  return x <= x0 ? (x + a.w0 - 1) / a.w0 : a.units0 + (x - x0 + 1) / 2;
+}
 
 struct UnitAt {
   int prob;      // 0: dL1, 1: dL2
@@ -40,8 +52,8 @@ struct UnitAt {
 };
 QDEV UnitAt unit_at(const MxGradArgs& a, int64_t u, int64_t u_hi) {
   UnitAt x;
-  x.prob = u >= a.units0;
-  const int64_t v = x.prob ? u - a.units0 : u;
+  x.prob = u >= a.sh.units0;
+  const int64_t v = x.prob ? u - a.sh.units0 : u;
   x.tile = (int)(v / a.pieces);
   x.piece = (int)(v % a.pieces);
   x.last = x.piece + 1 == a.pieces || u + 1 == u_hi;
@@ -61,8 +73,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
-  const int grid = (int)gridDim.x;
-  const int64_t u_lo = blockIdx.x * args.units / grid, u_hi = ((int64_t)blockIdx.x + 1) * args.units / grid;
+  const int64_t u_lo = grad_first(args.sh, blockIdx.x), u_hi = grad_first(args.sh, (int64_t)blockIdx.x + 1);
   const int nbuf = args.nbuf;
   const uint32_t sum_col = (uint32_t)(nbuf * args.n16);
 
@@ -99,7 +110,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
         const MxGradProblem& p = args.p[x.prob];
         const int t0 = x.piece * 64 * kGPiece, n = min(kGPiece, (args.M - t0 + 63) / 64);
         for (int i = 0; i < n; ++i) {
-          if (!(ok = mbar_wait(empty + s, ph ^ 1u, abort_flag, args.status))) break;
+          if (!(ok = mbar_wait_backoff(empty + s, ph ^ 1u, abort_flag, args.status, 20))) break;
           uint8_t* sa = smem + s * stage;
           mbar_arrive_expect_tx(full + s, (uint32_t)stage);
           for (int j = 0; j < 2; ++j) tma_load_2d(sa + 8192 * j, &p.tmZ, full + s, x.tile * 128 + 64 * j, t0 + 64 * i);
@@ -124,10 +135,10 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
       const UnitAt x = unit_at(args, u, u_hi);
       const bool masked = x.prob == 0 && args.drop.threshold;
       const int t0 = x.piece * 64 * kGPiece, n = min(kGPiece, (args.M - t0 + 63) / 64);
-      if (!(ok = warp_poll(wempty + b, wph ^ 1u, abort_flag, args.status, lane))) break;
+      if (!(ok = warp_poll<40>(wempty + b, wph ^ 1u, abort_flag, args.status, lane))) break;
       const uint32_t d = tmem + (uint32_t)(b * args.n16);
       for (int i = 0; i < n; ++i) {
-        if (!(ok = warp_poll((masked ? ready : full) + s, ph, abort_flag, args.status, lane))) break;
+        if (!(ok = warp_poll<20>((masked ? ready : full) + s, ph, abort_flag, args.status, lane))) break;
         tc_fence_after();
         if (one) {
           const uint8_t* sa = smem + s * stage;
@@ -163,12 +174,12 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
     bool first = true;
     for (int64_t u = u_lo; u < u_hi; ++u) {
       const UnitAt x = unit_at(args, u, u_hi);
-      if (!warp_wait(wfull + b, wph, abort_flag, args.status, lane)) break;
+      if (!warp_wait_backoff(wfull + b, wph, abort_flag, args.status, lane, 100)) break;
       tc_fence_after();
       const MxGradProblem& p = args.p[x.prob];
       // this run's slot of the tile: its ordinal among the CTAs that share it
-      const int64_t tile_u = (x.prob ? args.units0 : 0) + (int64_t)x.tile * args.pieces;
-      const int ord = (int)blockIdx.x - grad_owner(args.units, grid, tile_u);
+      const int64_t tile_u = (x.prob ? args.sh.units0 : 0) + (int64_t)x.tile * args.pieces;
+      const int ord = (int)blockIdx.x - grad_owner(args.sh, tile_u);
       float* slot = p.part + ((int64_t)x.tile * args.maxc + ord) * 128 * r;
       const int row = q4 * 32 + lane;
       for (int c = 0; c < r16; c += 16) {
@@ -215,37 +226,37 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
     // Units of dL1 come first in a run, so every stage up to the last masked
     // one is masked and the ready barriers' phases follow the ring's.
     const PhiloxKey key = philox_key(args.drop);
-    const int t = tid & 255;
-    int s = 0;
+    const int grp = (warp - 8) >> 3, t = tid & 255;  // two groups of 8 warps, alternate stages
+    int s = 0, turn = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int64_t u = u_lo; u < u_hi && u < args.units0 && ok; ++u) {
+    for (int64_t u = u_lo; u < u_hi && u < args.sh.units0 && ok; ++u) {
       const UnitAt x = unit_at(args, u, u_hi);
       const int t0 = x.piece * 64 * kGPiece, n = min(kGPiece, (args.M - t0 + 63) / 64);
-      for (int i = 0; i < n; ++i) {
-        // 4 evaluations of this thread's chunks before the wait: they need no data
-        uint32_t keep[4];
+      for (int i = 0; i < n; ++i, turn ^= 1) {
+        if (turn == grp) {
+          // this thread's evaluations before the wait: they need no data
+          uint4 rnd[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int q = t + 256 * j, tok = (q >> 3) & 63, ch = q & 7, box = q >> 9;
-          const int64_t e = (int64_t)(t0 + 64 * i + tok) * args.p[0].cols + x.tile * 128 + 64 * box + 8 * ch;
-          keep[j] = keep8((uint64_t)e >> 3, key, args.drop.threshold);
+          for (int j = 0; j < 4; ++j) {
+            const int q = t + 256 * j, tok = (q >> 3) & 63, ch = q & 7, box = q >> 9;
+            const int64_t e = (int64_t)(t0 + 64 * i + tok) * args.p[0].cols + x.tile * 128 + 64 * box + 8 * ch;
+            rnd[j] = philox4x32_10((uint64_t)e >> 3, key);
+          }
+          if (!(ok = warp_poll<20>(full + s, ph, abort_flag, args.status, lane))) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int q = t + 256 * j, tok = (q >> 3) & 63, ch = q & 7, box = q >> 9;
+            uint4* at = reinterpret_cast<uint4*>(smem + s * stage + 8192 * box + tok * 128 + ((ch ^ (tok & 7)) << 4));
+            const uint4 v = *at;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            drop8_bf16(w, rnd[j], args.drop.threshold << 16);
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready + s);
         }
-        if (!(ok = warp_wait(full + s, ph, abort_flag, args.status, lane))) break;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int q = t + 256 * j, tok = (q >> 3) & 63, ch = q & 7, box = q >> 9;
-          uint4* at = reinterpret_cast<uint4*>(smem + s * stage + 8192 * box + tok * 128 + ((ch ^ (tok & 7)) << 4));
-          const uint4 v = *at;
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] &= ((keep[j] >> (2 * k)) & 1u ? 0xFFFFu : 0u) | ((keep[j] >> (2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
-          *at = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ready + s);
         if (++s == kS) {
           s = 0;
           ph ^= 1u;
@@ -271,39 +282,47 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
   }
 }
 
-// Both gradients from the slots of their tiles, in order.
-__global__ void __launch_bounds__(256) mx_grad_finish_kernel(const __grid_constant__ MxGradArgs a, int grid) {
-  const int64_t n0 = a.units0 ? a.p[0].cols * a.r : 0, n = n0 + (a.units > a.units0 ? a.p[1].cols * a.r : 0);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int prob = i >= n0;
-    const MxGradProblem& p = a.p[prob];
-    const int64_t k = prob ? i - n0 : i;
-    // the outputs' own order: [cols][r], transposed [r][cols]
-    const int64_t col = p.transposed ? k % p.cols : k / a.r;
-    const int j = (int)(p.transposed ? k / p.cols : k % a.r);
-    const int64_t tile = col >> 7, tile_u = (prob ? a.units0 : 0) + tile * a.pieces;
-    const int nc = grad_owner(a.units, grid, tile_u + a.pieces - 1) - grad_owner(a.units, grid, tile_u);
-    const float* s = p.part + tile * a.maxc * 128 * a.r + (p.transposed ? j * 128 + (col & 127) : (col & 127) * a.r + j);
-    float d = s[0];
-    for (int c = 1; c <= nc; ++c) d = __fadd_rn(d, s[(int64_t)c * 128 * a.r]);
-    p.out[k] = d;
+// Both gradients from the slots of their tiles, in order.  blockIdx.x is the
+// tile (those of dL1 first); a slot is contiguous in the output's order,
+// [128][r] of dL1 and, row by row, [r][128] of dL2.
+__global__ void __launch_bounds__(256) mx_grad_finish_kernel(const __grid_constant__ MxGradArgs a) {
+  const int64_t tiles0 = a.sh.units0 / a.pieces;
+  const int prob = blockIdx.x >= tiles0;
+  const MxGradProblem& p = a.p[prob];
+  const int64_t tile = blockIdx.x - (prob ? tiles0 : 0), tile_u = (int64_t)blockIdx.x * a.pieces;
+  const int nc = grad_owner(a.sh, tile_u + a.pieces - 1) - grad_owner(a.sh, tile_u);
+  const int64_t left = p.cols - tile * 128;
+  const int ncol = (int)(left < 128 ? left : 128), slot = 128 * a.r;
+  const float* s = p.part + tile * a.maxc * slot;
+  for (int i = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4; i < slot; i += (int)gridDim.y * 1024) {
+    if (p.transposed ? (i & 127) >= ncol : i >= ncol * a.r) continue;
+    float4 d = *reinterpret_cast<const float4*>(s + i);
+#pragma unroll 4
+    for (int c = 1; c <= nc; ++c) {
+      const float4 q = *reinterpret_cast<const float4*>(s + (int64_t)c * slot + i);
+      d = make_float4(__fadd_rn(d.x, q.x), __fadd_rn(d.y, q.y), __fadd_rn(d.z, q.z), __fadd_rn(d.w, q.w));
+    }
+    const int64_t o = p.transposed ? (int64_t)(i >> 7) * p.cols + tile * 128 + (i & 127) : tile * slot + i;
+    *reinterpret_cast<float4*>(p.out + o) = d;
   }
 }
 
 }  // namespace
 
-// Partial slots of one problem with `cols` columns in a launch of `units`.
-MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, int num_sms) {
+MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool drop, int num_sms) {
   MxGradPlan p{};
   p.pieces = (int)((M + 64 * kGPiece - 1) / (64 * kGPiece));
   const int64_t t0 = (cols0 + 127) / 128, t1 = (cols1 + 127) / 128;
-  p.units0 = t0 * p.pieces;
-  p.units = p.units0 + t1 * p.pieces;
-  if (!p.units) return p;
-  p.grid = (int)(p.units < num_sms ? p.units : num_sms);
-  const int64_t per = p.units / p.grid;
-  p.maxc = (int)((p.pieces + per - 1) / per) + 1;
-  if (p.maxc > p.grid) p.maxc = p.grid;
+  p.sh.units0 = t0 * p.pieces;
+  p.sh.units = p.sh.units0 + t1 * p.pieces;
+  p.sh.w0 = drop && t0 ? 3 : 2;
+  if (!p.sh.units) return p;
+  // no more CTAs than leave each the cost of a unit, so that none is empty
+  // (the slots of a tile's CTAs are then all written)
+  const int64_t cost = grad_cost(p.sh, p.sh.units), fit = cost / p.sh.w0;
+  p.sh.grid = (int)(fit < num_sms ? fit : num_sms);
+  // most CTAs that share a tile: its cost over a CTA's, and one at either end
+  p.maxc = (int)((int64_t)p.pieces * p.sh.w0 * p.sh.grid / cost) + 2;
   p.part0_bytes = (size_t)t0 * p.maxc * 128 * r * sizeof(float);
   p.part_bytes = p.part0_bytes + (size_t)t1 * p.maxc * 128 * r * sizeof(float);
   p.n16 = (3 * r + 15) / 16 * 16;
@@ -316,8 +335,7 @@ MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, int num_
 }
 
 cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st) {
-  a.units0 = p.units0;
-  a.units = p.units;
+  a.sh = p.sh;
   a.pieces = p.pieces;
   a.maxc = p.maxc;
   a.n16 = p.n16;
@@ -328,13 +346,12 @@ cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st) 
   cudaError_t err = cudaFuncSetAttribute(mx_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kGBudget + 512 + 1024);
   if (err != cudaSuccess) return err;
-  mx_grad_kernel<<<p.grid, kGThreads, smem, st>>>(a);
+  mx_grad_kernel<<<p.sh.grid, kGThreads, smem, st>>>(a);
   count_launches(1);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  const int64_t n = ((p.units0 ? a.p[0].cols : 0) + (p.units > p.units0 ? a.p[1].cols : 0)) * a.r;
-  const int64_t want = (n + 255) / 256;
-  mx_grad_finish_kernel<<<(unsigned)(want < 2368 ? want : 2368), 256, 0, st>>>(a, p.grid);
+  mx_grad_finish_kernel<<<dim3((unsigned)(p.sh.units / p.pieces), (unsigned)((128 * a.r + 1023) / 1024)), 256, 0,
+                          st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }

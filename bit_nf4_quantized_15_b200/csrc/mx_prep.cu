@@ -47,7 +47,8 @@ struct PrepCfg {
   static constexpr int TOTAL = BAR + 512 + 1024;
   static_assert(TOTAL <= 232448 && STAGE % 1024 == 0 && OUTB % 1024 == 0, "budget");
 };
-constexpr int kPrepThreads = 24 * 32;
+constexpr int kQGroups = 2;  // quantise groups of 8 warps (3 were a few percent slower)
+constexpr int kPrepThreads = (8 + 8 * kQGroups) * 32;
 constexpr uint32_t kSumCol = 256;  // tensor memory: work accumulators at 0 and 128, the sum at 256
 
 QDEV void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
@@ -71,6 +72,17 @@ __host__ __device__ inline int64_t prep_unit(int64_t units, int grid, int64_t c)
 // CTA that owns unit u.
 __host__ __device__ inline int prep_owner(int64_t units, int grid, int64_t u) {
   return (int)(((u + 1) * grid - 1) / units);
+}
+
+// beta v as `terms` bf16 terms, r elements apart; four neighbours at a time.
+QDEV void store_terms(uint16_t* out, float4 v, float beta, int terms, int r) {
+  v = make_float4(__fmul_rn(v.x, beta), __fmul_rn(v.y, beta), __fmul_rn(v.z, beta), __fmul_rn(v.w, beta));
+  for (int t = 0; t < terms; ++t) {
+    const uint2 w = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    *reinterpret_cast<uint2*>(out + (int64_t)t * r) = w;
+    v = make_float4(__fsub_rn(v.x, __uint_as_float(w.x << 16)), __fsub_rn(v.y, __uint_as_float(w.x & 0xFFFF0000u)),
+                    __fsub_rn(v.z, __uint_as_float(w.y << 16)), __fsub_rn(v.w, __uint_as_float(w.y & 0xFFFF0000u)));
+  }
 }
 
 template <bool WIDE>
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
         const int row0 = (int)(uu / upt) * 128, c0 = (int)(uu % upt) * 256;
         bool ok = true;
         for (int q = 0; q < 4; ++q) {
-          if (!(ok = mbar_wait(empty + s, ph ^ 1u, abort_flag, args.status))) break;
+          if (!(ok = mbar_wait_backoff(empty + s, ph ^ 1u, abort_flag, args.status, 20))) break;
           uint8_t* sx = smem + s * C::STAGE;
           uint8_t* sl = sx + 16384;
           const int c = c0 + 64 * q;
@@ -166,9 +178,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
       for (int q = 0; q < 4; ++q) {
         const int b = piece & 1;
         if (in_piece == 0) {
-          if (!(ok = warp_poll(wempty + b, ((uint32_t)(piece >> 1) & 1u) ^ 1u, abort_flag, args.status, lane))) break;
+          if (!(ok = warp_poll<40>(wempty + b, ((uint32_t)(piece >> 1) & 1u) ^ 1u, abort_flag, args.status, lane))) break;
         }
-        if (!(ok = warp_poll((drop ? ready : full) + s, ph, abort_flag, args.status, lane))) break;
+        if (!(ok = warp_poll<40>((drop ? ready : full) + s, ph, abort_flag, args.status, lane))) break;
         tc_fence_after();
         if (one) {
           const uint8_t* sx = smem + s * C::STAGE;
@@ -198,7 +210,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
     if (lane == 0) {
       for (int u = 0; u < n_units; ++u) {
         const int b = u & 1;
-        if (!mbar_wait(ofull + b, (uint32_t)(u >> 1) & 1u, abort_flag, args.status)) break;
+        if (!mbar_wait_backoff(ofull + b, (uint32_t)(u >> 1) & 1u, abort_flag, args.status, 40)) break;
         const int64_t uu = u_lo + u;
         const int64_t rt = uu / upt;
         const int kb = (int)(uu % upt);
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
       in_piece += 4;
       if (in_piece < kPieces && !last) continue;
       const int b = piece & 1;
-      if (!warp_wait(wfull + b, (uint32_t)(piece >> 1) & 1u, abort_flag, args.status, lane)) break;
+      if (!warp_wait_backoff(wfull + b, (uint32_t)(piece >> 1) & 1u, abort_flag, args.status, lane, 100)) break;
       tc_fence_after();
       float* dst = nullptr;
       if (last) {  // this run's rows of D: the slot of (row tile, ordinal of this CTA in it)
@@ -264,64 +276,69 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
     const int grp = (warp - 8) >> 3, t = tid & 255;
     const int rl = t & 127, half = t >> 7;
     const PhiloxKey key = drop ? philox_key(args.drop) : PhiloxKey{0, 0, 0, 0};
+    const uint32_t thr = args.drop.threshold << 16;
     bool bad = false;
-    for (int u = 0; u < n_units; ++u) {
-      const int64_t uu = u_lo + u;
-      const int64_t row = (uu / upt) * 128 + rl;
-      const int ob = u & 1;
+    int s = grp;  // ring stage of iteration `it` (grp < kS)
+    uint32_t ph = 0;
+    int64_t tile = u_lo / upt;  // of the unit
+    int kb = (int)(u_lo % upt);
+    for (int it = grp, u = 0; it < 4 * n_units; it += kQGroups) {
+      for (; u < it >> 2; ++u)  // the unit of this stage
+        if (++kb == upt) {
+          kb = 0;
+          ++tile;
+        }
+      const int q = it & 3, ob = u & 1;
       uint8_t* so = smem + C::OUT + ob * C::OUTB;
-      if (!warp_wait(oempty + ob, ((uint32_t)(u >> 1) & 1u) ^ 1u, abort_flag, args.status, lane)) break;
-      bool ok = true;
-#pragma unroll 1
-      for (int q = grp; q < 4; q += 2) {
-        const int it = 4 * u + q, s = it % kS;
-        if (!(ok = warp_wait(full + s, (uint32_t)(it / kS) & 1u, abort_flag, args.status, lane))) break;
-        uint8_t* sx = smem + s * C::STAGE + rl * 128;
-        uint32_t w[16];
+      uint4 rnd[4];
+      if (drop) {  // the generator needs no data: evaluated before the wait
+        const uint64_t e8 = (uint64_t)((tile * 128 + rl) * args.cols + kb * 256 + 64 * q + 32 * half) >> 3;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 v = *reinterpret_cast<const uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4));
-          w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-        }
-        if (drop) {
-          const int64_t e = row * args.cols + (uu % upt) * 256 + 64 * q + 32 * half;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t k = keep8((uint64_t)e / 8 + j, key, args.drop.threshold);
-            uint32_t z[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              z[i] = w[4 * j + i] & (((k >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((k >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u));
-            *reinterpret_cast<uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
-          }
-        }
-        fence_proxy_async_smem();  // these reads and writes before the MMAs and the TMA refill
-        __syncwarp();
-        if (lane == 0) {
-          if (drop) mbar_arrive(ready + s);
-          mbar_arrive(empty + s);
-        }
-        uint32_t m2 = 0;  // largest |x| bits, two 16-bit lanes
-#pragma unroll
-        for (int j = 0; j < 16; ++j) m2 = __vmaxu2(m2, w[j] & 0x7FFF7FFFu);
-        const uint32_t b = mx_scale_byte(max(m2 & 0xFFFFu, m2 >> 16) << 16);
-        bad |= b == 255u;
-        const float f = mx_inv_scale(b);
-        uint32_t c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          c[j] = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) c[j] |= mx_codes2(w[4 * j + i], f) << (8 * i);
-        }
-        const int blk = 2 * q + half;  // 32-block of the unit
-        *reinterpret_cast<uint4*>(so + rl * 128 + ((blk ^ (rl & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
-        so[16384 + (blk >> 2) * 512 + (rl & 31) * 16 + (rl >> 5) * 4 + (blk & 3)] = (uint8_t)b;
-        fence_proxy_async_smem();  // before the TMA store reads the staging buffer
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ofull + ob);
+        for (int j = 0; j < 4; ++j) rnd[j] = philox4x32_10(e8 | j, key);  // e8 is a multiple of 4
       }
-      if (!ok) break;
+      if (!warp_poll<20>(full + s, ph, abort_flag, args.status, lane)) break;
+      uint8_t* sx = smem + s * C::STAGE + rl * 128;
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 v = *reinterpret_cast<const uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4));
+        w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+      }
+      if (drop) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t z[4] = {w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
+          drop8_bf16(z, rnd[j], thr);
+          *reinterpret_cast<uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
+        }
+      }
+      fence_proxy_async_smem();  // these reads and writes before the MMAs and the TMA refill
+      __syncwarp();
+      if (lane == 0) {
+        if (drop) mbar_arrive(ready + s);
+        mbar_arrive(empty + s);
+      }
+      uint32_t m2 = 0;  // largest |x|, two lanes
+#pragma unroll
+      for (int j = 0; j < 16; ++j) m2 = mx_absmax2(m2, w[j]);
+      const uint32_t b = mx_scale_byte(max(m2 & 0xFFFFu, m2 >> 16) << 16);
+      bad |= b == 255u;
+      const float f = mx_inv_scale(b);
+      uint32_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = mx_codes8(w + 4 * j, f);
+      if (!warp_poll<20>(oempty + ob, ((uint32_t)(u >> 1) & 1u) ^ 1u, abort_flag, args.status, lane)) break;
+      const int blk = 2 * q + half;  // 32-block of the unit
+      *reinterpret_cast<uint4*>(so + rl * 128 + ((blk ^ (rl & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
+      so[16384 + (blk >> 2) * 512 + (rl & 31) * 16 + (rl >> 5) * 4 + (blk & 3)] = (uint8_t)b;
+      fence_proxy_async_smem();  // before the TMA store reads the staging buffer
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ofull + ob);
+      s += kQGroups;
+      if (s >= kS) {
+        s -= kS;
+        ph ^= 1u;
+      }
     }
     if (bad) report(args.status, QLORA_ERR_NONFINITE);
   }
@@ -344,25 +361,43 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
 }
 
 // D from the partial slots of its row tile, in order: T = alpha D (fp32, when
-// asked for) and `terms` bf16 terms of beta D, [M][terms * r].
+// asked for) and `terms` bf16 terms of beta D, [M][terms * r].  blockIdx.x is
+// the row tile; a slot [128][r] is contiguous in D's own order.
 __global__ void __launch_bounds__(256) mx_prep_finish_kernel(MxPrepFinish a) {
-  const int64_t n = a.M * a.r;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / a.r, tile = m >> 7;
-    const int j = (int)(i - m * a.r);
-    const int c0 = prep_owner(a.units, a.grid, tile * a.units_per_tile);
-    const int c1 = prep_owner(a.units, a.grid, (tile + 1) * a.units_per_tile - 1);
-    const float* p = a.part + ((tile * a.maxc) * 128 + (m & 127)) * a.r + j;
-    float d = p[0];
-    for (int c = 1; c <= c1 - c0; ++c) d = __fadd_rn(d, p[(int64_t)c * 128 * a.r]);
-    if (a.T) a.T[i] = __fmul_rn(d, a.alpha);
-    float v = __fmul_rn(d, a.beta);
-    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + m * a.terms * a.r + j;
-    for (int t = 0; t < a.terms; ++t) {
-      const __nv_bfloat16 h = __float2bfloat16_rn(v);
-      o[(int64_t)t * a.r] = h;
-      v = __fsub_rn(v, __bfloat162float(h));
+  const int64_t tile = blockIdx.x;
+  const int nc = prep_owner(a.units, a.grid, (tile + 1) * a.units_per_tile - 1) -
+                 prep_owner(a.units, a.grid, tile * a.units_per_tile);
+  const int64_t left = (a.M - tile * 128) * a.r;
+  const int n = (int)(left < 128 * a.r ? left : 128 * a.r);
+  const float* p = a.part + tile * a.maxc * 128 * a.r;
+  for (int i = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4; i < n; i += (int)gridDim.y * 1024) {
+    float4 d = *reinterpret_cast<const float4*>(p + i);
+#pragma unroll 4
+    for (int c = 1; c <= nc; ++c) {
+      const float4 q = *reinterpret_cast<const float4*>(p + (int64_t)c * 128 * a.r + i);
+      d = make_float4(__fadd_rn(d.x, q.x), __fadd_rn(d.y, q.y), __fadd_rn(d.z, q.z), __fadd_rn(d.w, q.w));
     }
+    if (a.T)
+      *reinterpret_cast<float4*>(a.T + tile * 128 * a.r + i) =
+          make_float4(__fmul_rn(d.x, a.alpha), __fmul_rn(d.y, a.alpha), __fmul_rn(d.z, a.alpha), __fmul_rn(d.w, a.alpha));
+    const int row = i / a.r, j = i - row * a.r;
+    store_terms(a.out + (tile * 128 + row) * a.terms * a.r + j, d, a.beta, a.terms, a.r);
+  }
+  // the other operand of the backward's adapter sums rides along: s T in three terms
+  if (a.T_in) {
+    const float* t = a.T_in + tile * 128 * a.r;
+    for (int i = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4; i < n; i += (int)gridDim.y * 1024) {
+      const int row = i / a.r, j = i - row * a.r;
+      store_terms(a.out2 + (tile * 128 + row) * 3 * a.r + j, *reinterpret_cast<const float4*>(t + i), a.gamma, 3, a.r);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) split3_kernel(const float* __restrict__ in, int64_t n4, int r, float scale,
+                                                      uint16_t* __restrict__ out) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i * 4 / r;
+    store_terms(out + i * 4 + 2 * r * m, reinterpret_cast<const float4*>(in)[i], scale, 3, r);
   }
 }
 
@@ -396,23 +431,21 @@ cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) 
   return cudaGetLastError();
 }
 
-cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, const float* part, int64_t M, int r, float* T, float alpha,
-                                  uint16_t* out, int terms, float beta, cudaStream_t st) {
-  MxPrepFinish a{};
-  a.part = part;
-  a.M = M;
-  a.r = r;
+cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, MxPrepFinish a, cudaStream_t st) {
   a.units = p.units;
   a.units_per_tile = p.units_per_tile;
   a.grid = p.grid;
   a.maxc = p.maxc;
-  a.T = T;
-  a.alpha = alpha;
-  a.out = out;
-  a.terms = terms;
-  a.beta = beta;
-  const int64_t want = (M * r + 255) / 256;
-  mx_prep_finish_kernel<<<(unsigned)(want < 2368 ? want : 2368), 256, 0, st>>>(a);
+  const int64_t tiles = (a.M + 127) / 128;
+  const int rows = (int)(a.M < 128 ? a.M : 128);
+  mx_prep_finish_kernel<<<dim3((unsigned)tiles, (unsigned)((rows * a.r + 1023) / 1024)), 256, 0, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {
+  const int64_t n4 = M * r / 4, want = (n4 + 255) / 256;
+  split3_kernel<<<(unsigned)(want < 1184 ? want : 1184), 256, 0, st>>>(in, n4, r, scale, out);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -13,6 +13,7 @@
 // in a tile the scale of row i, block j is byte (i % 32) * 16 + (i / 32) * 4
 // + j.  A tile goes from global to tensor memory without being rearranged.
 #include <cuda_fp16.h>
+#include <cuda_fp4.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -56,10 +57,11 @@ QDEV float load1(const void* base, int64_t i) {
 }
 
 QDEV uint32_t codes8(const float (&v)[8], float f) {
-  uint32_t w = 0;
+  const float2 ff = make_float2(f, f);
+  float2 u[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w |= mx_codes(__fmul_rn(v[2 * j], f), __fmul_rn(v[2 * j + 1], f)) << (8 * j);
-  return w;
+  for (int j = 0; j < 4; ++j) u[j] = __fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), ff);
+  return mx_codes8(u);
 }
 
 // One CTA per scale tile (128 rows x 128 columns).  16 threads share a row,

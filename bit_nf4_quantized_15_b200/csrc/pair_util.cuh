@@ -55,12 +55,17 @@ QDEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_
   }
 }
 // Warp-wide bounded wait of a warp that stays converged: every lane polls.
+// SLEEP > 0: that many ns between polls, so that the spinning takes no issue
+// slots from warps that work (a spinning warp was measured to issue a third of
+// its scheduler's instructions).
+template <int SLEEP = 0>
 QDEV bool warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status, int lane,
                     uint64_t limit_ns = QNF4_WAIT_NS) {
   const uint32_t a = smem_u32(bar);
   if (__all_sync(0xFFFFFFFFu, mbar_test_wait_cluster(a, parity))) return true;
   const uint64_t t0 = globaltimer();
   for (uint32_t i = 1;; ++i) {
+    if (SLEEP) __nanosleep(SLEEP);
     if (__all_sync(0xFFFFFFFFu, mbar_test_wait_cluster(a, parity))) return true;
     if ((i & 63) == 0) {
       const bool late = globaltimer() - t0 > limit_ns;

@@ -53,4 +53,16 @@ QDEV uint32_t keep8(uint64_t ctr, const PhiloxKey& key, uint32_t threshold) {
   return m;
 }
 
+// Zero the dropped of eight bf16 (four words): `w` their random words, `thr`
+// the threshold in the high half.  A 16-bit lane is kept where it is >= the
+// threshold; for the high lane the whole word compares alike.
+QDEV void drop8_bf16(uint32_t* x, const uint4& w, uint32_t thr) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (ws[j] < thr) x[j] &= 0x0000FFFFu;
+    if ((ws[j] << 16) < thr) x[j] &= 0xFFFF0000u;
+  }
+}
+
 }  // namespace qnf4
