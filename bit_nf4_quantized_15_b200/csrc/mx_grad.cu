@@ -243,6 +243,8 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
             const int64_t e = (int64_t)(t0 + 64 * i + tok) * args.p[0].cols + x.tile * 128 + 64 * box + 8 * ch;
             rnd[j] = philox4x32_10((uint64_t)e >> 3, key);
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) keep_here(rnd[j]);
           if (!(ok = warp_poll<20>(full + s, ph, abort_flag, args.status, lane))) break;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {

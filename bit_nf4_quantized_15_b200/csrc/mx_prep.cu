@@ -295,6 +295,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
         const uint64_t e8 = (uint64_t)((tile * 128 + rl) * args.cols + kb * 256 + 64 * q + 32 * half) >> 3;
 #pragma unroll
         for (int j = 0; j < 4; ++j) rnd[j] = philox4x32_10(e8 | j, key);  // e8 is a multiple of 4
+#pragma unroll
+        for (int j = 0; j < 4; ++j) keep_here(rnd[j]);
       }
       if (!warp_poll<20>(full + s, ph, abort_flag, args.status, lane)) break;
       uint8_t* sx = smem + s * C::STAGE + rl * 128;
