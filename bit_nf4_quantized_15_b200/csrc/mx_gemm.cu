@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const int rank = (int)cluster_ctarank(), csize = (int)mx_cluster_size();
   const int id = (int)(blockIdx.x / (unsigned)csize);
   const int n_tiles = (args.cols + BN - 1) / BN;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   bool committed = false;
 
   if (warp == 0) {
@@ -176,52 +176,64 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      const uint32_t id_ext = idesc_bf16(128, BN, args.a_mn_ext, 0);
-      for (int it = 0; it < n_iters; ++it) {
-        const int s = it % kS;
-        if (!mbar_wait(full + s, (uint32_t)(it / kS) & 1u, abort_flag, args.status, lim)) break;
-        tc_fence_after();
+    const uint32_t id_ext = idesc_bf16(128, BN, args.a_mn_ext, 0);
+    const int64_t tail = args.K - (int64_t)(args.kb - 1) * kMxKB;
+    const int tail_steps = (int)((tail + 63) / 64);
+    const uint32_t base = smem_u32(smem), a0 = kdesc_lo(base), f0 = (uint32_t)sdesc_scales(base + C::A + C::B);
+    const uint32_t fhi = (uint32_t)(sdesc_scales(0) >> 32);
+    const bool one = elect_one();
+    int s = 0;
+    uint32_t ph = 0;
+    for (int it = 0; it < n_iters; ++it) {
+      if (!warp_poll(full + s, ph, abort_flag, args.status, lane, lim)) break;
+      tc_fence_after();
+      if (it < n_ext) {
         const uint8_t* sa = smem + s * C::STAGE;
-        const uint8_t* sb = sa + C::A;
-        if (it < n_ext) {
+        if (one) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem, operand_desc(sa, args.a_mn_ext, kk), operand_desc(sb, 0, kk), id_ext, (it | kk) != 0);
+            umma_bf16(tmem, operand_desc(sa, args.a_mn_ext, kk), operand_desc(sa + C::A, 0, kk), id_ext, (it | kk) != 0);
           umma_commit(empty + s);
-          if (it == n_ext - 1) {
-            // MMAs of another kind follow: let these finish (and be masked)
-            umma_commit(ext_done);
-            if (!mbar_wait(masked ? ext_masked : ext_done, 0, abort_flag, args.status, lim)) break;
-            tc_fence_after();
-          }
-          continue;
+          if (it == n_ext - 1) umma_commit(ext_done);
         }
-        const int64_t left = args.K - (int64_t)(kb_lo + it - n_ext) * kMxKB;
-        const int steps = left >= kMxKB ? 4 : (int)((left + 63) / 64);
+        __syncwarp();
+        // MMAs of another kind follow: let these finish (and be masked)
+        if (it == n_ext - 1) {
+          if (!warp_poll(masked ? ext_masked : ext_done, 0, abort_flag, args.status, lane, lim)) break;
+          tc_fence_after();
+        }
+      } else if (one) {
+        const int steps = kb_lo + it - n_ext == args.kb - 1 ? tail_steps : 4;
+        const uint32_t so = (uint32_t)s * (C::STAGE >> 4);
         const uint32_t sf = tmem + C::ACC + (uint32_t)s * C::SF;  // this stage's scale columns
-        const uint32_t ssf = smem_u32(sb + C::B);
         // A stage's scale columns are free again with the stage: its barrier
         // says that the MMAs that read them have finished.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (2 * h >= steps) break;
-          tmem_cp_scales(sf + 4 * h, sdesc_scales(ssf + 512 * h));
+          if (2 * h < steps) {
+            const uint64_t f = ((uint64_t)fhi << 32) | (f0 + so + 32 * h);
+            tmem_cp_scales(sf + 4 * h, f);
 #pragma unroll
-          for (int j = 0; j < C::FB; ++j)
-            tmem_cp_scales(sf + 8 + 4 * (C::FB * h + j), sdesc_scales(ssf + 1024 + 1024 * j + 512 * h));
+            for (int j = 0; j < C::FB; ++j) tmem_cp_scales(sf + 8 + 4 * (C::FB * h + j), f + 64 + 64 * j);
+          }
         }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          if (kk >= steps) break;
-          umma_mxf4(tmem, operand_desc(sa, 0, kk), operand_desc(sb, 0, kk), idesc_mxf4(128, BN, 2 * (kk & 1)),
-                    sf + 4 * (kk >> 1), sf + 8 + 4 * C::FB * (kk >> 1), (it | kk) != 0);
+          if (kk < steps)
+            umma_mxf4(tmem, kdesc(a0 + so + 2 * kk), kdesc(a0 + so + (C::A >> 4) + 2 * kk),
+                      idesc_mxf4(128, BN, 2 * (kk & 1)), sf + 4 * (kk >> 1), sf + 8 + 4 * C::FB * (kk >> 1),
+                      (it | kk) != 0);
         }
         umma_commit(empty + s);
       }
-      umma_commit(accum);
-      committed = true;
+      __syncwarp();
+      if (++s == kS) {
+        s = 0;
+        ph ^= 1u;
+      }
     }
+    if (one) umma_commit(accum);
+    committed = true;
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
