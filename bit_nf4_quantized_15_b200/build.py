@@ -20,7 +20,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libqlora_nf4.so")
 SOURCES = ["api.cu", "mx_api.cu", "mx_gemm.cu", "mx_gemm_pair.cu", "mx_prep.cu", "mx_grad.cu", "mx_quant.cu", "engine.cu", "engine_pair.cu", "gemv.cu", "gemv_bwd.cu", "quant.cu", "adapters.cu",
            "noalloc.cu", "nf4_tables.cpp"]
-HEADERS = ["common.cuh", "philox.cuh", "mx_codec.cuh", "mx_util.cuh", "pair_util.cuh", "engine_util.cuh", "internal.h"]
+HEADERS = ["common.cuh", "philox.cuh", "mx_codec.cuh", "launch.cuh", "mx_util.cuh", "pair_util.cuh", "engine_util.cuh", "internal.h"]
 
 
 def nvcc_path() -> str:

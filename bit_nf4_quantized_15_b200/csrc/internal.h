@@ -283,7 +283,9 @@ struct MxGemmPlan {
 };
 MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms);
 size_t mx_gemm_smem_bytes(int BN);
-cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st);
+// dependent: starts while the kernel before it on the stream (which writes
+// the tokens' side) still runs.
+cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, bool dependent, cudaStream_t st);
 
 
 // The same product on persistent CTA pairs, tokens on the lanes:
@@ -307,7 +309,7 @@ struct MxPairArgs {
   int* status;
 };
 size_t mx_pair_smem_bytes();
-cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, bool dependent, cudaStream_t st);
 
 // Quantise X and form D = drop(X).L in one pass (mx_prep.cu).
 struct MxPrepPlan {

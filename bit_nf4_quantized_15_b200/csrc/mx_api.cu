@@ -68,15 +68,18 @@ int map_scales(CUtensorMap* m, const uint8_t* scales, int64_t rows, int64_t K, i
 // out [M][N] = x w^T (+ the LoRA term), x = (xc, xs) the tokens, w = (wc, ws)
 // the features.
 //
-// CTA pairs when their 256 x 256 tiles fill the machine and are mostly tokens,
-// else tiles of 128 features split over clusters.
+// CTA pairs when more than a quarter of the SMs would have one of their 256 x
+// 256 tiles, else tiles of 128 features split over clusters.  Both measured:
+// 1024 x 4096 x 4096 (64 tiles) 14.0 us on pairs, 16.0 on clusters; 256 x
+// 11008 x 4096 (43) 15.6 and 16.2; 512 x 4096 x 4096 (32) 13.5 and 12.2; but
+// 128 x 22016 x 8192 (86, half of each empty) 36.8 and 34.3.
 int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, const uint8_t* ws, int64_t N,
             int64_t K, const LoraTerm* lora, const DropArgs& drop, void* out, int out_f32, int* status, int sms,
-            cudaStream_t st) {
+            bool dependent, cudaStream_t st) {
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t stall_ns = take_stall_request();
-  if (M > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= sms / 2 && !stall_ns) {
+  if (M > 128 && ((M + 255) / 256) * ((N + 255) / 256) > sms / 4 && !stall_ns) {
     MxPairArgs g;
     std::memset(&g, 0, sizeof(g));
     if (make_map(&g.tmA, xc, u8, 1, (uint64_t)K / 2, (uint64_t)M, 128, 128, sw) ||
@@ -99,7 +102,7 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
     g.ldo = N;
     g.out_f32 = out_f32;
     g.status = status;
-    return launch_mx_gemm_pair(g, sms, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+    return launch_mx_gemm_pair(g, sms, dependent, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
   }
   const MxGemmPlan p = plan_mx_gemm(N, M, K, sms);
   MxGemmArgs g;
@@ -128,7 +131,7 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
   g.status = status;
   g.stall = stall_ns != 0;
   g.wait_ns = stall_ns;
-  return launch_mx_gemm(g, p, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  return launch_mx_gemm(g, p, dependent, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 // Q(X) and the partial sums of D = drop(X).L (L MN-major [C][r] or K-major [r][C]).
@@ -243,7 +246,7 @@ int qlora_mx_matmul(const qlora_mx_tensor* a, const qlora_mx_tensor* b, void* ou
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
   return product(a->codes, a->scales, a->rows, b->codes, b->scales, b->rows, a->cols, nullptr, DropArgs{}, out,
-                 dtype == QLORA_DTYPE_F32, status_dev, di.sms, reinterpret_cast<cudaStream_t>(stream));
+                 dtype == QLORA_DTYPE_F32, status_dev, di.sms, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_config* cfg, void* out,
@@ -306,7 +309,7 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
   }
   const LoraTerm lora{sT, 0, L2, 1, r};
   return product(wb, wb + lay.q_scales, M, w->codes, w->scales, N, K, r ? &lora : nullptr, DropArgs{}, Y, 0,
-                 status_dev, di.sms, st);
+                 status_dev, di.sms, true, st);
 }
 
 int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const float* T_saved,
@@ -358,7 +361,7 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   if (dX) {
     const LoraTerm lora{sdT, (uint64_t)r * 6, L1, 0, r};
     if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d, dX, 0,
-                         status_dev, di.sms, st))
+                         status_dev, di.sms, true, st))
       return rc;
   }
   if (dL1 || dL2) {

@@ -21,6 +21,7 @@
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, then 4 epilogue warps (8 for
 // BN >= 128).
 #include "engine_util.cuh"
+#include "launch.cuh"
 #include "mx_util.cuh"
 #include "pair_util.cuh"
 #include "philox.cuh"
@@ -143,37 +144,53 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  pdl_trigger();  // not before this CTA has its tensor memory: a dependent CTA must not take it first
   bool committed = false;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    // The weight side (A) is not written by the kernel before this one, so its
+    // first stages are loaded before that has finished; the tokens' side waits.
     if (lane == 0 && !args.stall) {
-      for (int it = 0; it < n_iters; ++it) {
-        const int s = it % kS;
-        if (!mbar_wait(empty + s, ((uint32_t)(it / kS) & 1u) ^ 1u, abort_flag, args.status, lim)) break;
+      const int nb = C::FB == 2 && col0 + 128 < args.cols ? 2 : 1;  // token scale tiles
+      auto load_a = [&](int it, int s) {
         uint8_t* sa = smem + s * C::STAGE;
-        uint8_t* sb = sa + C::A;
         if (it < n_ext) {
           mbar_arrive_expect_tx(full + s, tx_bytes(args.a_mn_ext, 128) + tx_bytes(0, BN));
           load_operand(sa, &args.tmAx, full + s, args.a_mn_ext, row0, it * 64, 128);
+        } else {
+          const int kb = kb_lo + it - n_ext;
+          const uint32_t sbytes = 512u * (uint32_t)min(2, args.kt - 2 * kb);  // scale tiles along K
+          mbar_arrive_expect_tx(full + s, (uint32_t)C::A + (uint32_t)C::B + sbytes * (1u + (uint32_t)nb));
+          tma_load_2d(sa, &args.tmA, full + s, kb * 128, row0);
+          bulk_load(sa + C::A + C::B, args.sfA + ((int64_t)(row0 >> 7) * args.kt + 2 * kb) * 512, sbytes, full + s);
+        }
+      };
+      auto load_b = [&](int it, int s) {
+        uint8_t* sb = smem + s * C::STAGE + C::A;
+        if (it < n_ext) {
           load_operand(sb, &args.tmBx, full + s, 0, col0, it * 64, BN);
         } else {
           const int kb = kb_lo + it - n_ext;
-          const int nt = min(2, args.kt - 2 * kb);  // scale tiles along K of this stage
-          uint8_t* sfa = sb + C::B;
-          uint8_t* sfb = sfa + 1024;
-          const int nb = C::FB == 2 && col0 + 128 < args.cols ? 2 : 1;
-          const uint32_t sbytes = 512u * (uint32_t)nt;
-          mbar_arrive_expect_tx(full + s, (uint32_t)C::A + (uint32_t)C::B + sbytes * (1u + (uint32_t)nb));
-          tma_load_2d(sa, &args.tmA, full + s, kb * 128, row0);
+          const uint32_t sbytes = 512u * (uint32_t)min(2, args.kt - 2 * kb);
           tma_load_2d(sb, &args.tmB, full + s, kb * 128, col0);
-          bulk_load(sfa, args.sfA + ((int64_t)(row0 >> 7) * args.kt + 2 * kb) * 512, sbytes, full + s);
           for (int j = 0; j < nb; ++j)
-            bulk_load(sfb + 1024 * j, args.sfB + ((int64_t)((col0 >> 7) + j) * args.kt + 2 * kb) * 512, sbytes,
-                      full + s);
+            bulk_load(sb + C::B + 1024 + 1024 * j, args.sfB + ((int64_t)((col0 >> 7) + j) * args.kt + 2 * kb) * 512,
+                      sbytes, full + s);
         }
+      };
+      const int ahead = min(kS, n_iters);
+      for (int it = 0; it < ahead; ++it) load_a(it, it);
+      pdl_wait();
+      for (int it = 0; it < ahead; ++it) load_b(it, it);
+      for (int it = ahead; it < n_iters; ++it) {
+        const int s = it % kS;
+        if (!mbar_wait(empty + s, ((uint32_t)(it / kS) & 1u) ^ 1u, abort_flag, args.status, lim)) break;
+        load_a(it, s);
+        load_b(it, s);
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
     const uint32_t id_ext = idesc_bf16(128, BN, args.a_mn_ext, 0);
@@ -181,6 +198,8 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
     const int tail_steps = (int)((tail + 63) / 64);
     const uint32_t base = smem_u32(smem), a0 = kdesc_lo(base), f0 = (uint32_t)sdesc_scales(base + C::A + C::B);
     const uint32_t fhi = (uint32_t)(sdesc_scales(0) >> 32);
+    // a tile of 64 tokens may begin inside a scale tile: 32 rows a column
+    const uint32_t sfb0 = (uint32_t)(col0 & 127) >> 5;
     const bool one = elect_one();
     int s = 0;
     uint32_t ph = 0;
@@ -221,7 +240,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
         for (int kk = 0; kk < 4; ++kk) {
           if (kk < steps)
             umma_mxf4(tmem, kdesc(a0 + so + 2 * kk), kdesc(a0 + so + (C::A >> 4) + 2 * kk),
-                      idesc_mxf4(128, BN, 2 * (kk & 1)), sf + 4 * (kk >> 1), sf + 8 + 4 * C::FB * (kk >> 1),
+                      idesc_mxf4(128, BN, 2 * (kk & 1)), sf + 4 * (kk >> 1), sfb0 + sf + 8 + 4 * C::FB * (kk >> 1),
                       (it | kk) != 0);
         }
         umma_commit(empty + s);
@@ -323,41 +342,38 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
 }
 
 template <int BN>
-cudaError_t launch_bn(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st) {
+cudaError_t launch_bn(const MxGemmArgs& a, const MxGemmPlan& p, bool dependent, cudaStream_t st) {
   using C = MxCfg<BN>;
-  auto kern = mx_gemm_kernel<BN>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
-  if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.m_tiles * p.n_tiles * p.cluster));
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::TOTAL;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, kern, a);
-  if (err != cudaSuccess) return err;
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_kernel(mx_gemm_kernel<BN>,
+                       {dim3((unsigned)(p.m_tiles * p.n_tiles * p.cluster)), C::THREADS, C::TOTAL, (unsigned)p.cluster,
+                        dependent},
+                       st, a);
 }
 
 }  // namespace
 
+// Tile width and reduction split: the most CTAs that still run at once (one
+// an SM), the smaller split among equals; a rank keeps two reduction blocks
+// at least.  A second wave costs more than any split gains: 1000 x 2056 x 1568
+// took 9.0 us on 136 CTAs of 128 columns, 10.6 on 272 of 64 and 15.2 on 136
+// of 256 columns in two ranks; one token through 4096 x 4096 5.9 us on 32 x 4
+// CTAs, 7.0 on 32 x 2 and 7.3 on 32 x 8.
 MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms) {
   MxGemmPlan p{};
-  p.BN = bn_for_cols((int)(cols < 256 ? cols : 256));
-  p.m_tiles = (int)((rows + 127) / 128);
-  p.n_tiles = (int)((cols + p.BN - 1) / p.BN);
   const int kb = (int)((K + kMxKB - 1) / kMxKB);
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-  const int64_t slots = (int64_t)num_sms * (p.BN <= 64 ? 2 : 1);
-  p.cluster = 1;
-  while (p.cluster < 8 && tiles * p.cluster * 2 <= slots && 2 * p.cluster <= kb) p.cluster *= 2;
+  const int64_t m_tiles = (rows + 127) / 128;
+  const int widest = bn_for_cols((int)(cols < 256 ? cols : 256));
+  int64_t best = 0;
+  for (int cl = 1; cl <= 8 && (cl == 1 || kb >= 2 * cl); cl *= 2)
+    for (int bn = widest; bn >= (widest < 64 ? widest : 64); bn /= 2) {
+      const int64_t n = m_tiles * ((cols + bn - 1) / bn) * cl;
+      if (p.BN && (n <= best || n > num_sms)) continue;
+      best = n;
+      p.BN = bn;
+      p.cluster = cl;
+    }
+  p.m_tiles = (int)m_tiles;
+  p.n_tiles = (int)((cols + p.BN - 1) / p.BN);
   return p;
 }
 
@@ -366,13 +382,13 @@ size_t mx_gemm_smem_bytes(int BN) {
          : BN >= 32 ? MxCfg<32>::TOTAL : MxCfg<16>::TOTAL;
 }
 
-cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, cudaStream_t st) {
+cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, bool dependent, cudaStream_t st) {
   switch (p.BN) {
-    case 16: return launch_bn<16>(a, p, st);
-    case 32: return launch_bn<32>(a, p, st);
-    case 64: return launch_bn<64>(a, p, st);
-    case 128: return launch_bn<128>(a, p, st);
-    case 256: return launch_bn<256>(a, p, st);
+    case 16: return launch_bn<16>(a, p, dependent, st);
+    case 32: return launch_bn<32>(a, p, dependent, st);
+    case 64: return launch_bn<64>(a, p, dependent, st);
+    case 128: return launch_bn<128>(a, p, dependent, st);
+    case 256: return launch_bn<256>(a, p, dependent, st);
   }
   return cudaErrorInvalidValue;
 }

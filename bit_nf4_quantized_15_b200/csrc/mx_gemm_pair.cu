@@ -30,6 +30,7 @@
 // Every wait is bounded; the pair meets at a cluster barrier before tensor
 // memory is freed.
 #include "engine_util.cuh"
+#include "launch.cuh"
 #include "mx_util.cuh"
 #include "pair_util.cuh"
 #include "philox.cuh"
@@ -130,6 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
   cluster_sync_all();  // both CTAs' barriers and tensor memory exist from here on
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  pdl_trigger();  // not before this CTA has its tensor memory: a dependent CTA must not take it first
   const uint32_t full0 = mapa_shared(smem_u32(full), 0);
   const uint32_t masked0 = mapa_shared(smem_u32(masked), 0);
   const uint32_t drained0 = mapa_shared(smem_u32(drained), 0);
@@ -138,34 +140,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    // The weight side (B) is not written by the kernel before this one, so its
+    // first stages are loaded before that has finished; the tokens' side waits.
     if (lane == 0) {
-      int it = 0;
+      auto load_b = [&](int i, int s, const TileXY& xy) {
+        const int col0 = xy.n * 256, bcol0 = col0 + (int)rank * 128;
+        uint8_t* sb = smem + s * kXStage + kXA;
+        const uint32_t bar = full0 + 8u * (uint32_t)s;
+        if (i < n_ext) {
+          if (leader) mbar_arrive_expect_tx(full + s, 2u * (kXA + kXB));
+          if (args.b_mn_ext) {
+            tma_load_2d_pair(sb, &args.tmBx, bar, bcol0, i * 64);
+            tma_load_2d_pair(sb + 8192, &args.tmBx, bar, bcol0 + 64, i * 64);
+          } else {
+            tma_load_2d_pair(sb, &args.tmBx, bar, i * 64, bcol0);
+          }
+        } else {
+          if (leader) mbar_arrive_expect_tx(full + s, 2u * kXStage);
+          tma_load_2d_pair(sb, &args.tmB, bar, (i - n_ext) * 128, bcol0);
+          tma_load_2d_pair(sb + kXB + 1024, &args.tmSB, bar, (i - n_ext) * 256, col0 >> 7);
+        }
+      };
+      auto load_a = [&](int i, int s, const TileXY& xy) {
+        const int row0 = xy.m * 256 + (int)rank * 128;
+        uint8_t* sa = smem + s * kXStage;
+        const uint32_t bar = full0 + 8u * (uint32_t)s;
+        if (i < n_ext) {
+          tma_load_2d_pair(sa, &args.tmAx, bar, i * 64, row0);
+        } else {
+          tma_load_2d_pair(sa, &args.tmA, bar, (i - n_ext) * 128, row0);
+          tma_load_2d_pair(sa + kXA + kXB, &args.tmSA, bar, (i - n_ext) * 256, row0 >> 7);
+        }
+      };
+      const int ahead = min(kXS, n_ext + n_main);  // of the first tile (every pair has one)
+      const TileXY first = tile_of(pair, m_tiles, n_tiles);
+      for (int i = 0; i < ahead; ++i) load_b(i, i, first);
+      pdl_wait();
+      for (int i = 0; i < ahead; ++i) load_a(i, i, first);
+      int s = 0;
+      uint32_t ph = 0;
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += n_pairs) {
         const TileXY xy = tile_of(t, m_tiles, n_tiles);
-        const int row0 = xy.m * 256 + (int)rank * 128, col0 = xy.n * 256, bcol0 = col0 + (int)rank * 128;
-        for (int i = 0; i < n_ext + n_main; ++i, ++it) {
-          const int s = it % kXS;
-          if (!(ok = mbar_wait(empty + s, ((uint32_t)(it / kXS) & 1u) ^ 1u, abort_flag, args.status))) break;
-          uint8_t* sa = smem + s * kXStage;
-          uint8_t* sb = sa + kXA;
-          const uint32_t bar = full0 + 8u * (uint32_t)s;
-          if (i < n_ext) {
-            if (leader) mbar_arrive_expect_tx(full + s, 2u * (kXA + kXB));
-            tma_load_2d_pair(sa, &args.tmAx, bar, i * 64, row0);
-            if (args.b_mn_ext) {
-              tma_load_2d_pair(sb, &args.tmBx, bar, bcol0, i * 64);
-              tma_load_2d_pair(sb + 8192, &args.tmBx, bar, bcol0 + 64, i * 64);
-            } else {
-              tma_load_2d_pair(sb, &args.tmBx, bar, i * 64, bcol0);
-            }
-          } else {
-            const int kb = i - n_ext;
-            if (leader) mbar_arrive_expect_tx(full + s, 2u * kXStage);
-            tma_load_2d_pair(sa, &args.tmA, bar, kb * 128, row0);
-            tma_load_2d_pair(sb, &args.tmB, bar, kb * 128, bcol0);
-            tma_load_2d_pair(sb + kXB, &args.tmSA, bar, kb * 256, row0 >> 7);
-            tma_load_2d_pair(sb + kXB + 1024, &args.tmSB, bar, kb * 256, col0 >> 7);
+        for (int i = 0; i < n_ext + n_main; ++i) {
+          if (t != pair || i >= ahead) {
+            if (!(ok = mbar_wait(empty + s, ph ^ 1u, abort_flag, args.status))) break;
+            load_b(i, s, xy);
+            load_a(i, s, xy);
+          }
+          if (++s == kXS) {
+            s = 0;
+            ph ^= 1u;
           }
         }
       }
@@ -348,16 +373,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
 
 size_t mx_pair_smem_bytes() { return kXTotal; }
 
-cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, cudaStream_t st) {
-  auto kern = a.out_f32 ? mx_gemm_pair_kernel<true> : mx_gemm_pair_kernel<false>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kXTotal);
-  if (err != cudaSuccess) return err;
+cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, bool dependent, cudaStream_t st) {
   const int64_t tiles = (int64_t)((a.rows + 255) / 256) * ((a.cols + 255) / 256);
   const int pairs = num_sms / 2;
-  const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-  kern<<<grid, kXThreads, kXTotal, st>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  const LaunchShape shape{dim3(2u * (unsigned)(tiles < pairs ? tiles : pairs)), kXThreads, kXTotal, 1, dependent};
+  return a.out_f32 ? launch_kernel(mx_gemm_pair_kernel<true>, shape, st, a)
+                   : launch_kernel(mx_gemm_pair_kernel<false>, shape, st, a);
 }
 
 }  // namespace qnf4

@@ -18,6 +18,7 @@
 //
 // Roles: warp 0 TMA producer, 1 MMA issuer, 4-7 sum, 8-23 mask.
 #include "engine_util.cuh"
+#include "launch.cuh"
 #include "mx_util.cuh"
 #include "pair_util.cuh"
 #include "philox.cuh"
@@ -98,10 +99,12 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  pdl_trigger();  // not before this CTA has its tensor memory: a dependent CTA must not take it first
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
+      pdl_wait();
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -288,6 +291,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
 // tile (those of dL1 first); a slot is contiguous in the output's order,
 // [128][r] of dL1 and, row by row, [r][128] of dL2.
 __global__ void __launch_bounds__(256) mx_grad_finish_kernel(const __grid_constant__ MxGradArgs a) {
+  pdl_wait();
   const int64_t tiles0 = a.sh.units0 / a.pieces;
   const int prob = blockIdx.x >= tiles0;
   const MxGradProblem& p = a.p[prob];
@@ -345,17 +349,11 @@ cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st) 
   a.vboxes = p.vboxes;
   a.stages = p.stages;
   const int smem = p.stages * (16384 + p.vboxes * 8192) + 512 + 1024;
-  cudaError_t err = cudaFuncSetAttribute(mx_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kGBudget + 512 + 1024);
+  const cudaError_t err = launch_kernel(mx_grad_kernel, {dim3((unsigned)p.sh.grid), kGThreads, (size_t)smem, 1, true}, st, a);
   if (err != cudaSuccess) return err;
-  mx_grad_kernel<<<p.sh.grid, kGThreads, smem, st>>>(a);
-  count_launches(1);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  mx_grad_finish_kernel<<<dim3((unsigned)(p.sh.units / p.pieces), (unsigned)((128 * a.r + 1023) / 1024)), 256, 0,
-                          st>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_kernel(mx_grad_finish_kernel,
+                       {dim3((unsigned)(p.sh.units / p.pieces), (unsigned)((128 * a.r + 1023) / 1024)), 256, 0, 1, true},
+                       st, a);
 }
 
 }  // namespace qnf4

@@ -26,6 +26,7 @@
 // D, 8-23 quantise (two groups of 8 warps, alternate 64-column stages; a
 // thread has one 32-block of one row).
 #include "engine_util.cuh"
+#include "launch.cuh"
 #include "mx_codec.cuh"
 #include "mx_util.cuh"
 #include "pair_util.cuh"
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  pdl_trigger();  // not before this CTA has its tensor memory: a dependent CTA must not take it first
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -365,7 +367,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
 // D from the partial slots of its row tile, in order: T = alpha D (fp32, when
 // asked for) and `terms` bf16 terms of beta D, [M][terms * r].  blockIdx.x is
 // the row tile; a slot [128][r] is contiguous in D's own order.
-__global__ void __launch_bounds__(256) mx_prep_finish_kernel(MxPrepFinish a) {
+__global__ void __launch_bounds__(256) mx_prep_finish_kernel(const __grid_constant__ MxPrepFinish a) {
+  pdl_trigger();
+  pdl_wait();
   const int64_t tile = blockIdx.x;
   const int nc = prep_owner(a.units, a.grid, (tile + 1) * a.units_per_tile - 1) -
                  prep_owner(a.units, a.grid, tile * a.units_per_tile);
@@ -423,14 +427,8 @@ cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) 
   a.units_per_tile = p.units_per_tile;
   a.maxc = p.maxc;
   a.r16 = (a.r + 15) / 16 * 16;
-  const bool wide = a.r > 64;
-  const int smem = wide ? PrepCfg<true>::TOTAL : PrepCfg<false>::TOTAL;
-  auto kern = wide ? mx_prep_kernel<true> : mx_prep_kernel<false>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err != cudaSuccess) return err;
-  kern<<<p.grid, kPrepThreads, smem, st>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  return a.r > 64 ? launch_kernel(mx_prep_kernel<true>, {dim3((unsigned)p.grid), kPrepThreads, PrepCfg<true>::TOTAL, 1, false}, st, a)
+                  : launch_kernel(mx_prep_kernel<false>, {dim3((unsigned)p.grid), kPrepThreads, PrepCfg<false>::TOTAL, 1, false}, st, a);
 }
 
 cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, MxPrepFinish a, cudaStream_t st) {
@@ -440,9 +438,8 @@ cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, MxPrepFinish a, cudaStrea
   a.maxc = p.maxc;
   const int64_t tiles = (a.M + 127) / 128;
   const int rows = (int)(a.M < 128 ? a.M : 128);
-  mx_prep_finish_kernel<<<dim3((unsigned)tiles, (unsigned)((rows * a.r + 1023) / 1024)), 256, 0, st>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_kernel(mx_prep_finish_kernel, {dim3((unsigned)tiles, (unsigned)((rows * a.r + 1023) / 1024)), 256, 0, 1, true},
+                       st, a);
 }
 
 cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {

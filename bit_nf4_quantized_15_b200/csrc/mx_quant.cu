@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "mx_codec.cuh"
 #include "philox.cuh"
 
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(kQT) mx_quantize_kernel(const void* __restrict
                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                                                           int kt, int* status) {
   __shared__ __align__(16) uint8_t s_sc[512];
+  pdl_trigger();
   const int t = threadIdx.x;
   const int64_t rt = blockIdx.x / kt;
   const int ct = (int)(blockIdx.x % kt);
