@@ -2,6 +2,8 @@
 // dependent launch.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -22,10 +24,27 @@ struct LaunchShape {
   bool dependent;    // starts while the kernel before it on the stream still runs
 };
 
-template <class K, class... A>
-cudaError_t launch_kernel(K* kern, const LaunchShape& s, cudaStream_t st, const A&... args) {
-  if (s.smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+// The shared-memory attribute is set once per kernel and device, to all that a
+// block may have; a launch that fails for want of it (the device was reset in
+// between) sets it again.
+template <auto* Kern>
+cudaError_t allow_smem(bool again) {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!again && (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <auto* Kern, class... A>
+cudaError_t launch_kernel(const LaunchShape& s, cudaStream_t st, const A&... args) {
+  const bool big = s.smem > 48 * 1024;
+  if (big) {
+    const cudaError_t e = allow_smem<Kern>(false);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -47,7 +66,11 @@ cudaError_t launch_kernel(K* kern, const LaunchShape& s, cudaStream_t st, const 
   }
   cfg.attrs = at;
   cfg.numAttrs = n;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, Kern, args...);
+  if (e == cudaErrorInvalidValue && big && allow_smem<Kern>(true) == cudaSuccess) {
+    (void)cudaGetLastError();
+    e = cudaLaunchKernelEx(&cfg, Kern, args...);
+  }
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();

@@ -344,8 +344,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
 template <int BN>
 cudaError_t launch_bn(const MxGemmArgs& a, const MxGemmPlan& p, bool dependent, cudaStream_t st) {
   using C = MxCfg<BN>;
-  return launch_kernel(mx_gemm_kernel<BN>,
-                       {dim3((unsigned)(p.m_tiles * p.n_tiles * p.cluster)), C::THREADS, C::TOTAL, (unsigned)p.cluster,
+  return launch_kernel<mx_gemm_kernel<BN>>({dim3((unsigned)(p.m_tiles * p.n_tiles * p.cluster)), C::THREADS, C::TOTAL, (unsigned)p.cluster,
                         dependent},
                        st, a);
 }

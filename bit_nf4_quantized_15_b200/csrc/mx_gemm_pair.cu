@@ -377,8 +377,8 @@ cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, bool dependent
   const int64_t tiles = (int64_t)((a.rows + 255) / 256) * ((a.cols + 255) / 256);
   const int pairs = num_sms / 2;
   const LaunchShape shape{dim3(2u * (unsigned)(tiles < pairs ? tiles : pairs)), kXThreads, kXTotal, 1, dependent};
-  return a.out_f32 ? launch_kernel(mx_gemm_pair_kernel<true>, shape, st, a)
-                   : launch_kernel(mx_gemm_pair_kernel<false>, shape, st, a);
+  return a.out_f32 ? launch_kernel<mx_gemm_pair_kernel<true>>(shape, st, a)
+                   : launch_kernel<mx_gemm_pair_kernel<false>>(shape, st, a);
 }
 
 }  // namespace qnf4

@@ -349,10 +349,9 @@ cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st) 
   a.vboxes = p.vboxes;
   a.stages = p.stages;
   const int smem = p.stages * (16384 + p.vboxes * 8192) + 512 + 1024;
-  const cudaError_t err = launch_kernel(mx_grad_kernel, {dim3((unsigned)p.sh.grid), kGThreads, (size_t)smem, 1, true}, st, a);
+  const cudaError_t err = launch_kernel<mx_grad_kernel>({dim3((unsigned)p.sh.grid), kGThreads, (size_t)smem, 1, true}, st, a);
   if (err != cudaSuccess) return err;
-  return launch_kernel(mx_grad_finish_kernel,
-                       {dim3((unsigned)(p.sh.units / p.pieces), (unsigned)((128 * a.r + 1023) / 1024)), 256, 0, 1, true},
+  return launch_kernel<mx_grad_finish_kernel>({dim3((unsigned)(p.sh.units / p.pieces), (unsigned)((128 * a.r + 1023) / 1024)), 256, 0, 1, true},
                        st, a);
 }
 

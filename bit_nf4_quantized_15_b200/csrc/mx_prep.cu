@@ -427,8 +427,8 @@ cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) 
   a.units_per_tile = p.units_per_tile;
   a.maxc = p.maxc;
   a.r16 = (a.r + 15) / 16 * 16;
-  return a.r > 64 ? launch_kernel(mx_prep_kernel<true>, {dim3((unsigned)p.grid), kPrepThreads, PrepCfg<true>::TOTAL, 1, false}, st, a)
-                  : launch_kernel(mx_prep_kernel<false>, {dim3((unsigned)p.grid), kPrepThreads, PrepCfg<false>::TOTAL, 1, false}, st, a);
+  return a.r > 64 ? launch_kernel<mx_prep_kernel<true>>({dim3((unsigned)p.grid), kPrepThreads, PrepCfg<true>::TOTAL, 1, false}, st, a)
+                  : launch_kernel<mx_prep_kernel<false>>({dim3((unsigned)p.grid), kPrepThreads, PrepCfg<false>::TOTAL, 1, false}, st, a);
 }
 
 cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, MxPrepFinish a, cudaStream_t st) {
@@ -438,7 +438,7 @@ cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, MxPrepFinish a, cudaStrea
   a.maxc = p.maxc;
   const int64_t tiles = (a.M + 127) / 128;
   const int rows = (int)(a.M < 128 ? a.M : 128);
-  return launch_kernel(mx_prep_finish_kernel, {dim3((unsigned)tiles, (unsigned)((rows * a.r + 1023) / 1024)), 256, 0, 1, true},
+  return launch_kernel<mx_prep_finish_kernel>({dim3((unsigned)tiles, (unsigned)((rows * a.r + 1023) / 1024)), 256, 0, 1, true},
                        st, a);
 }
 

@@ -15,6 +15,7 @@ not depend on which device is current.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -53,49 +54,45 @@ SIGS = {
 }
 
 
-def _need(ok, what):
-    if not ok:
-        raise _q.QLoRAError(what)
+def _bad(what):
+    raise _q.QLoRAError(what)
+
+
+def _name(dtype):
+    return str(dtype).removeprefix("torch.")
 
 
 def _tensor(t, name, shape, dtype, device):
     """`t` is a contiguous tensor of this shape, type and device."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dtype == dtype
-          and tuple(t.shape) == tuple(shape) and t.device == device,
-          f"{name} must be a contiguous {str(dtype).removeprefix('torch.')} tensor of shape {tuple(shape)} on {device}")
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda
+            and t.is_contiguous()):
+        _bad(f"{name} must be a contiguous {_name(dtype)} CUDA tensor of shape {tuple(shape)} on {device}")
     return t
 
 
 def _matrix(t, name, dtypes):
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.is_contiguous() and t.dtype in dtypes,
-          f"{name} must be a contiguous CUDA matrix of "
-          + " or ".join(str(d).removeprefix("torch.") for d in dtypes))
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.dtype in dtypes and t.is_contiguous()):
+        _bad(f"{name} must be a contiguous CUDA matrix of " + " or ".join(map(_name, dtypes)))
     return t
 
 
-class _on:
-    """Makes a device current for a call that launches on it."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(device, f, *args):
+    """f(*args, stream) with the device of its tensors current."""
+    if device.index == torch.cuda.current_device():
+        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc:
+        _q._check(rc)
 
 
 def _status_ptr(status, device):
-    return (status if status is not None else _q._status(device)).data_ptr()
-
-
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    if status is None:
+        status = _q._status_bufs.get(device.index)
+        if status is None:
+            status = _q._status(device)
+    return status.data_ptr()
 
 
 def mx_storage_bytes(rows: int, cols: int):
@@ -126,12 +123,12 @@ class MXTensor:
         return self.codes.device
 
     def descriptor(self) -> qlora_mx_tensor:
-        c, s, dev = self.codes, self.scales, self.codes.device
+        c, s = self.codes, self.scales
         tiles = ((self.rows + 127) // 128) * ((self.cols + 127) // 128)
-        _need(c.is_cuda and c.dtype == torch.uint8 and s.dtype == torch.uint8 and s.device == dev
-              and c.is_contiguous() and s.is_contiguous() and 2 * c.numel() >= self.rows * self.cols
-              and s.numel() >= 512 * tiles,
-              f"codes and scales must be contiguous uint8 tensors on one device that hold {self.rows} x {self.cols}")
+        if not (c.is_cuda and c.dtype == torch.uint8 and s.dtype == torch.uint8 and s.device == c.device
+                and c.is_contiguous() and s.is_contiguous() and 2 * c.numel() >= self.rows * self.cols
+                and s.numel() >= 512 * tiles):
+            _bad(f"codes and scales must be contiguous uint8 CUDA tensors on one device that hold {self.rows} x {self.cols}")
         return qlora_mx_tensor(c.data_ptr(), s.data_ptr(), self.rows, self.cols)
 
 
@@ -158,7 +155,8 @@ class Dropout:
         if isinstance(off, torch.Tensor):
             _tensor(off.reshape(-1), "offset", (1,), torch.int64, device)
             off, dev_ptr = 0, off.data_ptr()
-        _need(0 <= self.seed <= _U64 and 0 <= off <= _U64, "seed and offset must be 64-bit unsigned integers")
+        if not (0 <= self.seed <= _U64 and 0 <= off <= _U64):
+            _bad("seed and offset must be 64-bit unsigned integers")
         return qlora_dropout_config(float(self.p), int(self.seed), int(off), dev_ptr)
 
 
@@ -171,38 +169,44 @@ def mx_quantize(X, transpose: bool = False, out: MXTensor | None = None, status=
     shape = (C, R) if transpose else (R, C)
     if out is None:
         out = MXTensor.empty(*shape, device=X.device)
-    _need((out.rows, out.cols) == shape and out.device == X.device, f"out must be {shape[0]} x {shape[1]} on {X.device}")
+    if (out.rows, out.cols) != shape or out.device != X.device:
+        _bad(f"out must be {shape[0]} x {shape[1]} on {X.device}")
     d = out.descriptor()
-    with _on(X.device):
-        _q._check(_q.lib().qlora_mx_quantize(X.data_ptr(), DTYPES[X.dtype], R, C, int(transpose), ctypes.byref(d),
-                                             _status_ptr(status, X.device), _stream(X.device)))
+    _call(X.device, _q.lib().qlora_mx_quantize, X.data_ptr(), DTYPES[X.dtype], R, C, int(transpose), ctypes.byref(d),
+          _status_ptr(status, X.device))
     return out
+
+
+def _values_dtype(dtype):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        _bad("dtype must be bfloat16 or float32")
+    return DTYPES[dtype]
 
 
 def mx_dequant(t: MXTensor, dtype=torch.bfloat16, out=None) -> torch.Tensor:
     """The values of an MXFP4 matrix, [rows, cols] in bf16 or fp32 (both exact)."""
-    _need(dtype in (torch.bfloat16, torch.float32), "dtype must be bfloat16 or float32")
-    d = t.descriptor()
+    kind, d, dev = _values_dtype(dtype), t.descriptor(), t.device
     if out is None:
-        out = torch.empty((t.rows, t.cols), dtype=dtype, device=t.device)
-    _tensor(out, "out", (t.rows, t.cols), dtype, t.device)
-    with _on(t.device):
-        _q._check(_q.lib().qlora_mx_dequant(ctypes.byref(d), out.data_ptr(), DTYPES[dtype], _stream(t.device)))
+        out = torch.empty((t.rows, t.cols), dtype=dtype, device=dev)
+    else:
+        _tensor(out, "out", (t.rows, t.cols), dtype, dev)
+    _call(dev, _q.lib().qlora_mx_dequant, ctypes.byref(d), out.data_ptr(), kind)
     return out
 
 
 def mx_matmul(a: MXTensor, b: MXTensor, dtype=torch.bfloat16, out=None, status=None) -> torch.Tensor:
     """A.B^T of two MXFP4 matrices with equal cols, [a.rows, b.rows] in bf16
     or fp32; accumulated in fp32 (b.rows % 8 == 0)."""
-    _need(dtype in (torch.bfloat16, torch.float32), "dtype must be bfloat16 or float32")
-    _need(a.device == b.device, "a and b must be on one device")
+    kind, dev = _values_dtype(dtype), a.device
+    if b.device != dev:
+        _bad("a and b must be on one device")
     da, db = a.descriptor(), b.descriptor()
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.device)
-    _tensor(out, "out", (a.rows, b.rows), dtype, a.device)
-    with _on(a.device):
-        _q._check(_q.lib().qlora_mx_matmul(ctypes.byref(da), ctypes.byref(db), out.data_ptr(), DTYPES[dtype],
-                                           _status_ptr(status, a.device), _stream(a.device)))
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=dev)
+    else:
+        _tensor(out, "out", (a.rows, b.rows), dtype, dev)
+    _call(dev, _q.lib().qlora_mx_matmul, ctypes.byref(da), ctypes.byref(db), out.data_ptr(), kind,
+          _status_ptr(status, dev))
     return out
 
 
@@ -216,29 +220,41 @@ def mx_weight(W, backward: bool = True, status=None) -> MXWeight:
 def mx_linear_workspace_bytes(M: int, N: int, K: int, r: int = 0) -> int:
     """Workspace of mx_linear_fwd and mx_linear_bwd (the larger of the two)."""
     n = _q.lib().qlora_mx_linear_workspace_bytes(M, N, K, r)
-    _need(n, "invalid shape or rank for mx_linear_workspace_bytes")
+    if not n:
+        _bad("invalid shape or rank for mx_linear_workspace_bytes")
     return n
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(M, N, K, r, index):
+    with torch.cuda.device(index):
+        return mx_linear_workspace_bytes(M, N, K, r)
 
 
 def _linear_args(M, N, K, L1, L2, dropout, ws, device):
     """(r, dropout config or None, workspace) after checking the adapter."""
-    _need((L1 is None) == (L2 is None), "L1 and L2 come together")
+    if (L1 is None) != (L2 is None):
+        _bad("L1 and L2 come together")
     r = 0
     if L1 is not None:
         r = _matrix(L1, "L1", (torch.bfloat16,)).shape[1]
         _tensor(L1, "L1", (K, r), torch.bfloat16, device)
         _tensor(L2, "L2", (r, N), torch.bfloat16, device)
-    cfg = dropout.config(device) if dropout is not None else None
-    need = mx_linear_workspace_bytes(M, N, K, r)
+    cfg = None if dropout is None else ctypes.byref(dropout.config(device))
+    need = _workspace_bytes(M, N, K, r, device.index)
     if ws is None:
         ws = torch.empty(need, dtype=torch.uint8, device=device)
-    _need(ws.is_cuda and ws.device == device and ws.is_contiguous() and ws.numel() * ws.element_size() >= need,
-          f"ws must be a contiguous tensor of {need} bytes on {device}")
+    elif not (ws.is_cuda and ws.device == device and ws.is_contiguous() and ws.numel() * ws.element_size() >= need):
+        _bad(f"ws must be a contiguous CUDA tensor of {need} bytes on {device}")
     return r, cfg, ws
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _output(t, name, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _tensor(t, name, shape, dtype, device)
 
 
 def mx_linear_fwd(X, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropout: Dropout | None = None, ws=None, Y=None,
@@ -247,30 +263,18 @@ def mx_linear_fwd(X, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropout: Dro
     without an adapter).  X bf16 [M, K], quantised to MXFP4 on the way."""
     _matrix(X, "X", (torch.bfloat16,))
     M, K = X.shape
-    dev = X.device
-    _need(w.fwd.cols == K and w.fwd.device == dev, f"the weight must have {K} columns and be on {dev}")
-    N = w.fwd.rows
+    dev, wf = X.device, w.fwd
+    if wf.cols != K or wf.device != dev:
+        _bad(f"the weight must have {K} columns and be on {dev}")
+    N = wf.rows
+    Y = _output(Y, "Y", (M, N), torch.bfloat16, dev)
+    T = None if L1 is None else _output(T, "T", (M, _matrix(L1, "L1", (torch.bfloat16,)).shape[1]), torch.float32, dev)
     if M == 0:
-        r = 0 if L1 is None else L1.shape[1]
-        return (torch.empty((0, N), dtype=torch.bfloat16, device=dev) if Y is None else Y,
-                None if L1 is None else torch.empty((0, r), dtype=torch.float32, device=dev) if T is None else T)
+        return Y, T
     r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, dev)
-    if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    else:
-        _tensor(Y, "Y", (M, N), torch.bfloat16, dev)
-    if not r:
-        T = None
-    elif T is None:
-        T = torch.empty((M, r), dtype=torch.float32, device=dev)
-    else:
-        _tensor(T, "T", (M, r), torch.float32, dev)
-    d = w.fwd.descriptor()
-    with _on(dev):
-        _q._check(_q.lib().qlora_mx_linear_fwd(X.data_ptr(), M, ctypes.byref(d), _ptr(L1), _ptr(L2), r, float(s),
-                                               None if cfg is None else ctypes.byref(cfg), Y.data_ptr(), _ptr(T),
-                                               ws.data_ptr(), ws.numel() * ws.element_size(),
-                                               _status_ptr(status, dev), _stream(dev)))
+    d = wf.descriptor()
+    _call(dev, _q.lib().qlora_mx_linear_fwd, X.data_ptr(), M, ctypes.byref(d), _ptr(L1), _ptr(L2), r, s, cfg,
+          Y.data_ptr(), _ptr(T), ws.data_ptr(), ws.numel() * ws.element_size(), _status_ptr(status, dev))
     return Y, T
 
 
@@ -281,40 +285,35 @@ def mx_linear_bwd(dY, X, T, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropo
     adapter: dX alone.  dX needs ``w.bwd``."""
     _matrix(dY, "dY", (torch.bfloat16,))
     M, N = dY.shape
-    dev = dY.device
-    K = w.fwd.cols
-    _need(w.fwd.rows == N and w.fwd.device == dev, f"the weight must have {N} rows and be on {dev}")
-    need_dX, adapter = need_dX or dX is not None, L1 is not None
-    need_dL1, need_dL2 = adapter and (need_dL1 or dL1 is not None), adapter and (need_dL2 or dL2 is not None)
-    _need(not need_dX or (w.bwd is not None and (w.bwd.rows, w.bwd.cols) == (K, N) and w.bwd.device == dev),
-          "dX needs the weight's backward form (mx_weight(W), w.bwd)")
-    r = L1.shape[1] if adapter else 0
-    if need_dL1:
+    dev, K = dY.device, w.fwd.cols
+    if w.fwd.rows != N or w.fwd.device != dev:
+        _bad(f"the weight must have {N} rows and be on {dev}")
+    adapter = L1 is not None
+    r = _matrix(L1, "L1", (torch.bfloat16,)).shape[1] if adapter else 0
+    d = None
+    if need_dX or dX is not None:
+        wb = w.bwd
+        if wb is None or (wb.rows, wb.cols) != (K, N) or wb.device != dev:
+            _bad("dX needs the weight's backward form (mx_weight(W), w.bwd)")
+        d = ctypes.byref(wb.descriptor())
+        dX = _output(dX, "dX", (M, K), torch.bfloat16, dev)
+    if adapter and (need_dL1 or dL1 is not None):
         _tensor(X, "X", (M, K), torch.bfloat16, dev)
-    if need_dL2:
+        dL1 = _output(dL1, "dL1", (K, r), torch.float32, dev)
+    if adapter and (need_dL2 or dL2 is not None):
         _tensor(T, "T", (M, r), torch.float32, dev)
-
-    def output(t, name, shape, dtype, wanted):
-        if not wanted:
-            return None
-        return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, name, shape, dtype, dev)
-
-    dX = output(dX, "dX", (M, K), torch.bfloat16, need_dX)
-    dL1 = output(dL1, "dL1", (K, r), torch.float32, need_dL1)
-    dL2 = output(dL2, "dL2", (r, N), torch.float32, need_dL2)
+        dL2 = _output(dL2, "dL2", (r, N), torch.float32, dev)
+    if not adapter:
+        dL1 = dL2 = None
     if M == 0:
         for g in (dL1, dL2):
             if g is not None:
                 g.zero_()
         return dX, dL1, dL2
     r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, dev)
-    d = w.bwd.descriptor() if need_dX else None
-    with _on(dev):
-        _q._check(_q.lib().qlora_mx_linear_bwd(dY.data_ptr(), _ptr(X), M, _ptr(T),
-                                               None if d is None else ctypes.byref(d), N, K, _ptr(L1), _ptr(L2), r,
-                                               float(s), None if cfg is None else ctypes.byref(cfg), _ptr(dX),
-                                               _ptr(dL1), _ptr(dL2), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                               _status_ptr(status, dev), _stream(dev)))
+    _call(dev, _q.lib().qlora_mx_linear_bwd, dY.data_ptr(), _ptr(X) if dL1 is not None else None, M,
+          _ptr(T) if dL2 is not None else None, d, N, K, _ptr(L1), _ptr(L2), r, s, cfg, _ptr(dX), _ptr(dL1), _ptr(dL2),
+          ws.data_ptr(), ws.numel() * ws.element_size(), _status_ptr(status, dev))
     return dX, dL1, dL2
 
 
@@ -323,15 +322,14 @@ def dropout(X, p: float, seed: int, offset=0, out=None) -> torch.Tensor:
     1 / (1 - p) (p in steps of 2^-16), the mask named by (seed, offset) and
     never stored; the gradient is the same call on the upstream gradient.
     X: contiguous bf16, fp16 or fp32 CUDA tensor of any shape; out may be X."""
-    _need(isinstance(X, torch.Tensor) and X.is_cuda and X.is_contiguous() and X.dtype in DTYPES,
-          "X must be a contiguous bfloat16, float16 or float32 CUDA tensor")
-    cfg = Dropout(p, seed, offset).config(X.device)
+    if not (isinstance(X, torch.Tensor) and X.is_cuda and X.dtype in DTYPES and X.is_contiguous()):
+        _bad("X must be a contiguous bfloat16, float16 or float32 CUDA tensor")
+    dev = X.device
+    cfg = Dropout(p, seed, offset).config(dev)
     if out is None:
         out = torch.empty_like(X)
-    _tensor(out, "out", X.shape, X.dtype, X.device)
-    if X.numel() == 0:
-        return out
-    with _on(X.device):
-        _q._check(_q.lib().qlora_dropout(X.data_ptr(), DTYPES[X.dtype], X.numel(), ctypes.byref(cfg), out.data_ptr(),
-                                         _stream(X.device)))
+    else:
+        _tensor(out, "out", X.shape, X.dtype, dev)
+    if X.numel():
+        _call(dev, _q.lib().qlora_dropout, X.data_ptr(), DTYPES[X.dtype], X.numel(), ctypes.byref(cfg), out.data_ptr())
     return out
