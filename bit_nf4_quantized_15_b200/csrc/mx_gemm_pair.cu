@@ -14,8 +14,8 @@
 //
 // Tensor memory: the accumulator (256 columns), then the scales of each ring
 // stage (8 columns of A, 16 of B).  It has no room for two accumulators of
-// this size, so the epilogue drains the tile into registers (bf16, 64 a
-// thread), releases the accumulator, and stores while the next tile's MMAs
+// this size, so the epilogue drains the tile into registers (128 a
+// thread), releases the accumulator, and rounds and stores while the next tile's MMAs
 // run.  The LoRA term comes first in a tile, see mx_gemm.cu; with dropout
 // the epilogue warps have the tile's mask ready (128 bits a thread, evaluated
 // during the previous tile's main loop).
@@ -322,28 +322,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(drained0);
       } else {
-        uint32_t o[64];
+        uint32_t v[8][16];  // the whole row half, loads all in flight; packed once the accumulator is released
 #pragma unroll
-        for (int c = 0; c < 128; c += 64) {  // four loads in flight
-          uint32_t v[4][16];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld16(tl + (uint32_t)(c + 16 * q), v[q]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              o[c / 2 + 8 * q + j] = pack_bf16x2(__uint_as_float(v[q][2 * j]), __uint_as_float(v[q][2 * j + 1]));
-        }
+        for (int q = 0; q < 8; ++q) tmem_ld16(tl + (uint32_t)(16 * q), v[q]);
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(drained0);
         if (row < args.rows) {
           __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(args.out) + row * args.ldo + col;
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t* w = v[c >> 1] + 8 * (c & 1);
+            const auto two = [&](int j) { return pack_bf16x2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])); };
             if (col + 8 * c < args.cols)
-              *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+              *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(two(0), two(2), two(4), two(6));
+          }
         }
       }
     }
