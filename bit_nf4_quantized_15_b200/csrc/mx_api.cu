@@ -22,7 +22,7 @@ constexpr int64_t kMaxDim = 1 << 24;
 
 bool mx_shape_ok(int64_t rows, int64_t cols) {
   return rows >= 1 && cols >= 32 && cols % 32 == 0 && rows <= kMaxDim && cols <= kMaxDim &&
-         ((rows + 127) / 128) * ((cols + 127) / 128) <= 0x7FFFFFFF;
+         ((rows + 127) / 128) * ((cols + 127) / 128) <= 0x3FFFFFFF;
 }
 bool rank_ok(int r) { return r == 0 || (r >= 8 && r <= 128 && r % 8 == 0); }
 bool dtype_ok(int d) { return d == QLORA_DTYPE_BF16 || d == QLORA_DTYPE_F16 || d == QLORA_DTYPE_F32; }

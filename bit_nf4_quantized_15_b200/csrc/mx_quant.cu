@@ -26,27 +26,51 @@ namespace {
 
 constexpr int kQT = 256;  // threads of the element kernels
 
-// Eight consecutive elements as fp32.
 template <int DT>
-QDEV void load8(const void* base, int64_t i, float (&v)[8]) {
-  if constexpr (DT == QLORA_DTYPE_F32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(base) + i / 4);
-    const float4 b = __ldg(reinterpret_cast<const float4*>(base) + i / 4 + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+constexpr int kWords = DT == QLORA_DTYPE_F32 ? 8 : 4;  // 32-bit words of eight elements
+
+// Eight consecutive elements as they are stored.
+template <int DT>
+QDEV void load8(const uint4* p, uint32_t* w) {
+#pragma unroll
+  for (int j = 0; j < kWords<DT>; j += 4) {
+    const uint4 r = __ldg(p + j / 4);
+    w[j] = r.x, w[j + 1] = r.y, w[j + 2] = r.z, w[j + 3] = r.w;
+  }
+}
+// ... and as fp32, in pairs.
+template <int DT>
+QDEV float2 pair_of(const uint32_t* w, int j) {
+  if constexpr (DT == QLORA_DTYPE_F32) return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+  else if constexpr (DT == QLORA_DTYPE_BF16)
+    return make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+}
+// Largest |x| as fp32 bits (an Inf or NaN has exponent 255 and compares above).
+template <int DT>
+QDEV uint32_t absmax8(const uint32_t* w) {
+  if constexpr (DT == QLORA_DTYPE_BF16) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = mx_absmax2(m, w[j]);
+    return max(m & 0x7FFFu, (m >> 16) & 0x7FFFu) << 16;
   } else {
-    const uint4 r = __ldg(reinterpret_cast<const uint4*>(base) + i / 8);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if constexpr (DT == QLORA_DTYPE_BF16) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[2 * j] = f.x, v[2 * j + 1] = f.y;
-      }
+      const float2 v = pair_of<DT>(w, j);
+      m = max(m, max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu));
     }
+    return m;
   }
+}
+template <int DT>
+QDEV uint32_t codes8(const uint32_t* w, float f) {
+  const float2 ff = make_float2(f, f);
+  float2 u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) u[j] = __fmul2_rn(pair_of<DT>(w, j), ff);
+  return mx_codes8(u);
 }
 
 template <int DT>
@@ -57,129 +81,125 @@ QDEV float load1(const void* base, int64_t i) {
   else return __half2float(reinterpret_cast<const __half*>(base)[i]);
 }
 
-QDEV uint32_t codes8(const float (&v)[8], float f) {
-  const float2 ff = make_float2(f, f);
-  float2 u[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) u[j] = __fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), ff);
-  return mx_codes8(u);
-}
-
-// One CTA per scale tile (128 rows x 128 columns).  16 threads share a row,
-// 8 elements (one 16-byte load) each, so a warp reads whole 256-byte row
-// pieces; every thread has its 8 rows' loads in flight at once.  The block
+// One CTA per scale tile (128 rows x 128 columns).  16 threads share a row, 8
+// elements each, so a warp reads whole row pieces; a thread has the loads of
+// kRows rows in flight, as stored (fp32 takes twice the registers).  The block
 // maximum is two shuffles over 4 lanes.  The 512 scale bytes meet in shared
 // memory and leave as 16-byte stores, zeros outside the matrix.
 template <int DT>
 __global__ void __launch_bounds__(kQT) mx_quantize_kernel(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                                                           int kt, int* status) {
+  constexpr int kRows = DT == QLORA_DTYPE_F32 ? 4 : 8, kW = kWords<DT>;
   __shared__ __align__(16) uint8_t s_sc[512];
   pdl_trigger();
-  const int t = threadIdx.x;
-  const int64_t rt = blockIdx.x / kt;
-  const int ct = (int)(blockIdx.x % kt);
-  const int64_t row0 = rt * 128;
-  const int64_t col = (int64_t)ct * 128 + (t & 15) * 8;
-  const bool cok = col < cols;
-  if (t < 32) reinterpret_cast<uint4*>(s_sc)[t] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
-  float v[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = row0 + (t >> 4) + 16 * i;
-    if (cok && row < rows) load8<DT>(X, row * cols + col, v[i]);
-    else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    }
-  }
+  const int t = threadIdx.x, rl0 = t >> 4, ch = t & 15;  // this thread's rows rl0 + 16 i, its 8 columns
+  const unsigned rt = blockIdx.x / (unsigned)kt, ct = blockIdx.x % (unsigned)kt;
+  const int64_t left = rows - (int64_t)rt * 128;
+  const int n = (int64_t)ct * 128 + ch * 8 < cols ? (int)(left < 128 ? left : 128) : 0;  // rows to do
+  const int64_t e8 = (((int64_t)rt * 128 + rl0) * cols + (int64_t)ct * 128) / 8 + ch;    // first row's 8 elements
+  const uint4* px = reinterpret_cast<const uint4*>(X) + e8 * (kW / 4);
+  uint32_t* pc = reinterpret_cast<uint32_t*>(codes) + e8;
+  const int64_t step = 2 * cols;  // 16 rows, in groups of 8 elements
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int rl = (t >> 4) + 16 * i;
-    const int64_t row = row0 + rl;
-    uint32_t m = 0;
+  for (int p = 0; p < 8; p += kRows) {
+    uint32_t w[kRows][kW];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t b = mx_scale_byte(m);
-    bad |= b == 255u;
-    const uint32_t w = codes8(v[i], mx_inv_scale(b));
-    if (cok && row < rows) {
-      reinterpret_cast<uint32_t*>(codes)[(row * cols + col) >> 3] = w;
-      if ((t & 3) == 0) s_sc[(rl & 31) * 16 + (rl >> 5) * 4 + ((t & 15) >> 2)] = (uint8_t)b;
+    for (int i = 0; i < kRows; ++i) {
+      if (rl0 + 16 * (p + i) < n) {
+        load8<DT>(px + (p + i) * step * (kW / 4), w[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kW; ++j) w[i][j] = 0u;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int rl = rl0 + 16 * (p + i);
+      uint32_t m = absmax8<DT>(w[i]);
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const uint32_t b = mx_scale_byte(m);
+      bad |= b == 255u;
+      const uint32_t c = codes8<DT>(w[i], mx_inv_scale(b));
+      if (rl < n) pc[(p + i) * step] = c;
+      if ((t & 3) == 0) s_sc[(rl & 31) * 16 + (rl >> 5) * 4 + (ch >> 2)] = (uint8_t)b;  // 0 outside
     }
   }
   if (bad) report(status, QLORA_ERR_NONFINITE);
   __syncthreads();
-  if (t < 32) reinterpret_cast<uint4*>(scales)[(rt * kt + ct) * 32 + t] = reinterpret_cast<const uint4*>(s_sc)[t];
+  if (t < 32) reinterpret_cast<uint4*>(scales)[(int64_t)blockIdx.x * 32 + t] = reinterpret_cast<const uint4*>(s_sc)[t];
 }
 
-// Transposed: X [R][C], output [C][R] with blocks along R.  One CTA per
-// output scale tile: a 128 (r) x 128 (c) piece goes through shared memory as
-// fp32 (row pitch 129 words: both the row writes and the column reads are
-// free of bank conflicts up to the vector loads' order); a thread then owns
-// one c and two blocks of 32 r.
-constexpr int kTP = 129;
+// Transposed: X [R][C], output [C][R] with blocks along R.  A CTA takes 128 r
+// x 64 c, half the rows of an output scale tile: the piece goes through
+// shared memory as stored, a lane 16 bytes of a row (rows padded by 16 bytes:
+// neither the row writes nor the column reads conflict); a thread then owns a
+// 32-block of one c.  The codes meet in shared memory too and leave as 64
+// bytes a row of the output.  (128 c a CTA left room for three CTAs an SM and
+// took half as long again.)
 template <int DT>
 __global__ void __launch_bounds__(kQT) mx_quantize_t_kernel(const void* __restrict__ X, int64_t R, int64_t C,
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales, int kt, int* status) {
-  extern __shared__ float s_x[];
-  __shared__ __align__(16) uint8_t s_sc[512];
+  constexpr int kE = DT == QLORA_DTYPE_F32 ? 4 : 2;      // bytes an element
+  constexpr int kPitch = 64 * kE + 16, kLanes = 4 * kE;  // bytes of a row; lanes that share one
+  constexpr int kStep = kQT / kLanes, kLoads = 128 / kStep;
+  __shared__ __align__(16) uint8_t s_x[128 * kPitch];
+  __shared__ __align__(16) uint4 s_c[64][5];             // codes, 64 bytes a row, padded
+  __shared__ __align__(8) uint8_t s_sc[256];             // scales: 32 x (2 groups of 32 rows) x 4 blocks
   const int t = threadIdx.x;
   // consecutive CTAs walk along C, so that their row pieces share DRAM pages
-  const int64_t n_ct = (C + 127) / 128;
-  const int64_t ct = blockIdx.x % n_ct;      // output row tile
-  const int rt = (int)(blockIdx.x / n_ct);   // output scale-tile column
-  if (t < 32) reinterpret_cast<uint4*>(s_sc)[t] = make_uint4(0, 0, 0, 0);
+  const unsigned n_ct = (unsigned)((C + 63) / 64);
+  const unsigned ct = blockIdx.x % n_ct, rt = blockIdx.x / n_ct;  // 64 output rows, output scale-tile column
+  const int64_t r0 = (int64_t)rt * 128, c0 = (int64_t)ct * 64;
+  const int nr = (int)(R - r0 < 128 ? R - r0 : 128), nc = (int)(C - c0 < 64 ? C - c0 : 64);
+  {
+    const int ch = t % kLanes, rl = t / kLanes;  // 16-byte piece of the row, first row
+    const uint4* p = reinterpret_cast<const uint4*>(X) + ((r0 + rl) * C + c0) / (16 / kE) + ch;
+    const int64_t step = kStep * (C / (16 / kE));
+    const int n = ch * (16 / kE) < nc ? nr : 0;
+    uint4 v[kLoads];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int rl = (t >> 4) + 16 * i;
-    const int64_t r = (int64_t)rt * 128 + rl, c = ct * 128 + (t & 15) * 8;
-    float v[8];
-    if (r < R && c < C) load8<DT>(X, r * C + c, v);
-    else {
+    for (int i = 0; i < kLoads; ++i) v[i] = rl + kStep * i < n ? __ldg(p + i * step) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s_x[rl * kTP + (t & 15) * 8 + j] = v[j];
+    for (int i = 0; i < kLoads; ++i) *reinterpret_cast<uint4*>(s_x + (rl + kStep * i) * kPitch + ch * 16) = v[i];
   }
   __syncthreads();
-  const int cl = t & 127, half = t >> 7;
-  const int64_t c = ct * 128 + cl;
-  bool bad = false;
+  const int cl = t & 63, blk = t >> 6;
+  float v[32];
+  uint32_t m = 0;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int blk = half * 2 + h;
-    const int64_t r0 = (int64_t)rt * 128 + blk * 32;
-    if (c >= C || r0 >= R) continue;
-    float v[32];
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      v[j] = s_x[(blk * 32 + j) * kTP + cl];
-      m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    }
-    const uint32_t b = mx_scale_byte(m);
-    bad |= b == 255u;
-    const float f = mx_inv_scale(b);
-    uint32_t w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float u[8] = {v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3], v[8 * q + 4], v[8 * q + 5], v[8 * q + 6],
-                          v[8 * q + 7]};
-      w[q] = codes8(u, f);
-    }
-    reinterpret_cast<uint4*>(codes)[(c * R + r0) >> 5] = make_uint4(w[0], w[1], w[2], w[3]);
-    s_sc[(cl & 31) * 16 + (cl >> 5) * 4 + blk] = (uint8_t)b;
+  for (int j = 0; j < 32; ++j) {
+    v[j] = load1<DT>(s_x + (blk * 32 + j) * kPitch, cl);
+    m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
   }
-  if (bad) report(status, QLORA_ERR_NONFINITE);
+  const uint32_t b = mx_scale_byte(m);  // 0 outside the matrix
+  const float f = mx_inv_scale(b);
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float2 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = __fmul2_rn(make_float2(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]), make_float2(f, f));
+    w[q] = mx_codes8(u);
+  }
+  s_c[cl][blk] = make_uint4(w[0], w[1], w[2], w[3]);
+  s_sc[(cl & 31) * 8 + (cl >> 5) * 4 + blk] = (uint8_t)b;
+  if (b == 255u) report(status, QLORA_ERR_NONFINITE);
   __syncthreads();
-  if (t < 32) reinterpret_cast<uint4*>(scales)[(ct * kt + rt) * 32 + t] = reinterpret_cast<const uint4*>(s_sc)[t];
+  {
+    const int row = t >> 2, q = t & 3;  // 4 lanes a row of codes
+    if (row < nc && q * 32 < nr) reinterpret_cast<uint4*>(codes)[((c0 + row) * R + r0) / 32 + q] = s_c[row][q];
+  }
+  // this CTA's half of the scale tile: 8 of every 16 bytes
+  if (t < 32)
+    *reinterpret_cast<uint2*>(scales + ((int64_t)(ct >> 1) * kt + rt) * 512 + t * 16 + (ct & 1) * 8) =
+        *reinterpret_cast<const uint2*>(s_sc + t * 8);
+  // the last half tile of rows has no CTA of its own: its padding is zero too
+  if (t < 32 && ct + 1 == n_ct && (ct & 1) == 0)
+    *reinterpret_cast<uint2*>(scales + ((int64_t)(ct >> 1) * kt + rt) * 512 + t * 16 + 8) = make_uint2(0u, 0u);
 }
 
 // Value of a code times 2^(b - 127).  The E2M1 value is exact in fp16 and the
@@ -191,31 +211,44 @@ QDEV float2 values2(uint32_t byte, float lo, float hi) {
   return make_float2(__fmul_rn(__fmul_rn(f.x, lo), hi), __fmul_rn(__fmul_rn(f.y, lo), hi));
 }
 
-// Eight elements a thread: a 4-byte code load and one (bf16) or two (fp32)
-// 16-byte stores, all coalesced; the four threads of a block read the same
-// scale byte.
+// One CTA per scale tile again, the quantiser's mapping: its 512 scale bytes
+// through shared memory, 8 rows' codes in flight a thread, 16-byte stores.
 template <int DT>
 __global__ void __launch_bounds__(kQT) mx_dequant_kernel(const uint32_t* __restrict__ codes,
-                                                         const uint8_t* __restrict__ scales, int64_t n8, int cols8,
-                                                         int kt, void* __restrict__ out) {
-  for (int64_t i = (int64_t)blockIdx.x * kQT + threadIdx.x; i < n8; i += (int64_t)gridDim.x * kQT) {
-    const int64_t row = i / cols8;
-    const int c8 = (int)(i - row * cols8);
-    const int blk = c8 >> 2, rl = (int)(row & 127);
-    const uint32_t b = __ldg(scales + ((row >> 7) * kt + (blk >> 2)) * 512 + (rl & 31) * 16 + (rl >> 5) * 4 + (blk & 3));
-    const uint32_t w = __ldg(codes + i);
+                                                         const uint8_t* __restrict__ scales, int64_t rows,
+                                                         int64_t cols, int kt, void* __restrict__ out) {
+  __shared__ __align__(16) uint8_t s_sc[512];
+  const int t = threadIdx.x, rl0 = t >> 4, ch = t & 15;
+  const unsigned rt = blockIdx.x / (unsigned)kt, ct = blockIdx.x % (unsigned)kt;
+  const int64_t left = rows - (int64_t)rt * 128;
+  const int n = (int64_t)ct * 128 + ch * 8 < cols ? (int)(left < 128 ? left : 128) : 0;
+  const int64_t e8 = (((int64_t)rt * 128 + rl0) * cols + (int64_t)ct * 128) / 8 + ch;
+  const int64_t step = 2 * cols;
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = rl0 + 16 * i < n ? __ldg(codes + e8 + i * step) : 0u;
+  if (t < 32)
+    reinterpret_cast<uint4*>(s_sc)[t] = __ldg(reinterpret_cast<const uint4*>(scales) + (int64_t)blockIdx.x * 32 + t);
+  __syncthreads();
+  uint4* po = reinterpret_cast<uint4*>(out) + e8 * (kWords<DT> / 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int rl = rl0 + 16 * i;
+    if (rl >= n) break;
+    const uint32_t b = s_sc[(rl & 31) * 16 + (rl >> 5) * 4 + (ch >> 2)];
     // 2^(b - 127) as a product of two normal powers of two
     const float lo = b == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float((64u + (b >> 1)) << 23);
     const float hi = __uint_as_float((63u + b - (b >> 1)) << 23);
     float2 v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = values2((w >> (8 * j)) & 255u, lo, hi);
+    for (int j = 0; j < 4; ++j) v[j] = values2((w[i] >> (8 * j)) & 255u, lo, hi);
+    uint4* o = po + i * step * (kWords<DT> / 4);
     if constexpr (DT == QLORA_DTYPE_F32) {
-      reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-      reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+      o[0] = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+      o[1] = make_uint4(__float_as_uint(v[2].x), __float_as_uint(v[2].y), __float_as_uint(v[3].x), __float_as_uint(v[3].y));
     } else {
-      reinterpret_cast<uint4*>(out)[i] = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                                                    pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+      *o = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                      pack_bf16x2(v[3].x, v[3].y));
     }
   }
 }
@@ -235,8 +268,14 @@ __global__ void __launch_bounds__(kQT) dropout_kernel(const void* __restrict__ X
   const PhiloxKey key = philox_key(d);
   const int64_t n8 = n / 8, stride = (int64_t)gridDim.x * kQT;
   for (int64_t i = (int64_t)blockIdx.x * kQT + threadIdx.x; i < n8; i += stride) {
+    uint32_t w[kWords<DT>];
+    load8<DT>(reinterpret_cast<const uint4*>(X) + i * (kWords<DT> / 4), w);
     float v[8];
-    load8<DT>(X, i * 8, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = pair_of<DT>(w, j);
+      v[2 * j] = f.x, v[2 * j + 1] = f.y;
+    }
     const uint32_t keep = keep8((uint64_t)i, key, d.threshold);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (keep >> j) & 1u ? __fmul_rn(v[j], d.inv) : 0.0f;
@@ -247,7 +286,6 @@ __global__ void __launch_bounds__(kQT) dropout_kernel(const void* __restrict__ X
       reinterpret_cast<uint4*>(out)[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                                     pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     } else {
-      uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
@@ -293,11 +331,8 @@ template <int DT>
 static cudaError_t quantize_t(const void* X, int64_t R, int64_t C, uint8_t* codes, uint8_t* scales, int* status,
                               cudaStream_t st) {
   const int kt = (int)((R + 127) / 128);
-  const unsigned grid = (unsigned)(((C + 127) / 128) * kt);
-  const int smem = 128 * kTP * 4;
-  cudaError_t err = cudaFuncSetAttribute(mx_quantize_t_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err != cudaSuccess) return err;
-  mx_quantize_t_kernel<DT><<<grid, kQT, smem, st>>>(X, R, C, codes, scales, kt, status);
+  const unsigned grid = (unsigned)(((C + 63) / 64) * kt);
+  mx_quantize_t_kernel<DT><<<grid, kQT, 0, st>>>(X, R, C, codes, scales, kt, status);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -313,13 +348,13 @@ cudaError_t launch_mx_quantize_t(const void* X, int dtype, int64_t R, int64_t C,
 
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int dtype,
                               void* out, cudaStream_t st) {
-  const int kt = (int)((cols + 127) / 128), cols8 = (int)(cols / 8);
-  const int64_t n8 = rows * cols8;
+  const int kt = (int)((cols + 127) / 128);
+  const unsigned grid = (unsigned)(((rows + 127) / 128) * kt);
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   if (dtype == QLORA_DTYPE_F32)
-    mx_dequant_kernel<QLORA_DTYPE_F32><<<elem_grid(n8), kQT, 0, st>>>(c, scales, n8, cols8, kt, out);
+    mx_dequant_kernel<QLORA_DTYPE_F32><<<grid, kQT, 0, st>>>(c, scales, rows, cols, kt, out);
   else
-    mx_dequant_kernel<QLORA_DTYPE_BF16><<<elem_grid(n8), kQT, 0, st>>>(c, scales, n8, cols8, kt, out);
+    mx_dequant_kernel<QLORA_DTYPE_BF16><<<grid, kQT, 0, st>>>(c, scales, rows, cols, kt, out);
   count_launches(1);
   return cudaGetLastError();
 }
