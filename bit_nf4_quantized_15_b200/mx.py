@@ -76,13 +76,20 @@ def _matrix(t, name, dtypes):
     return t
 
 
+# The current stream's handle; the binding's own accessor where torch has it
+# (the public one builds a Stream object, 2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(device, f, *args):
     """f(*args, stream) with the device of its tensors current."""
-    if device.index == torch.cuda.current_device():
-        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = f(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            rc = f(*args, _raw_stream(index))
     if rc:
         _q._check(rc)
 
@@ -187,7 +194,7 @@ def mx_dequant(t: MXTensor, dtype=torch.bfloat16, out=None) -> torch.Tensor:
     """The values of an MXFP4 matrix, [rows, cols] in bf16 or fp32 (both exact)."""
     kind, d, dev = _values_dtype(dtype), t.descriptor(), t.device
     if out is None:
-        out = torch.empty((t.rows, t.cols), dtype=dtype, device=dev)
+        out = t.codes.new_empty((t.rows, t.cols), dtype=dtype)
     else:
         _tensor(out, "out", (t.rows, t.cols), dtype, dev)
     _call(dev, _q.lib().qlora_mx_dequant, ctypes.byref(d), out.data_ptr(), kind)
@@ -202,7 +209,7 @@ def mx_matmul(a: MXTensor, b: MXTensor, dtype=torch.bfloat16, out=None, status=N
         _bad("a and b must be on one device")
     da, db = a.descriptor(), b.descriptor()
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=dev)
+        out = a.codes.new_empty((a.rows, b.rows), dtype=dtype)
     else:
         _tensor(out, "out", (a.rows, b.rows), dtype, dev)
     _call(dev, _q.lib().qlora_mx_matmul, ctypes.byref(da), ctypes.byref(db), out.data_ptr(), kind,
@@ -231,11 +238,11 @@ def _workspace_bytes(M, N, K, r, index):
         return mx_linear_workspace_bytes(M, N, K, r)
 
 
-def _linear_args(M, N, K, L1, L2, dropout, ws, device):
+def _linear_args(M, N, K, L1, L2, dropout, ws, like):
     """(r, dropout config or None, workspace) after checking the adapter."""
     if (L1 is None) != (L2 is None):
         _bad("L1 and L2 come together")
-    r = 0
+    r, device = 0, like.device
     if L1 is not None:
         r = _matrix(L1, "L1", (torch.bfloat16,)).shape[1]
         _tensor(L1, "L1", (K, r), torch.bfloat16, device)
@@ -243,7 +250,7 @@ def _linear_args(M, N, K, L1, L2, dropout, ws, device):
     cfg = None if dropout is None else ctypes.byref(dropout.config(device))
     need = _workspace_bytes(M, N, K, r, device.index)
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = like.new_empty(need, dtype=torch.uint8)
     elif not (ws.is_cuda and ws.device == device and ws.is_contiguous() and ws.numel() * ws.element_size() >= need):
         _bad(f"ws must be a contiguous CUDA tensor of {need} bytes on {device}")
     return r, cfg, ws
@@ -253,8 +260,8 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _output(t, name, shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else _tensor(t, name, shape, dtype, device)
+def _output(t, name, shape, dtype, like):
+    return like.new_empty(shape, dtype=dtype) if t is None else _tensor(t, name, shape, dtype, like.device)
 
 
 def mx_linear_fwd(X, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropout: Dropout | None = None, ws=None, Y=None,
@@ -267,11 +274,11 @@ def mx_linear_fwd(X, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropout: Dro
     if wf.cols != K or wf.device != dev:
         _bad(f"the weight must have {K} columns and be on {dev}")
     N = wf.rows
-    Y = _output(Y, "Y", (M, N), torch.bfloat16, dev)
-    T = None if L1 is None else _output(T, "T", (M, _matrix(L1, "L1", (torch.bfloat16,)).shape[1]), torch.float32, dev)
+    Y = _output(Y, "Y", (M, N), torch.bfloat16, X)
+    T = None if L1 is None else _output(T, "T", (M, _matrix(L1, "L1", (torch.bfloat16,)).shape[1]), torch.float32, X)
     if M == 0:
         return Y, T
-    r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, dev)
+    r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, X)
     d = wf.descriptor()
     _call(dev, _q.lib().qlora_mx_linear_fwd, X.data_ptr(), M, ctypes.byref(d), _ptr(L1), _ptr(L2), r, s, cfg,
           Y.data_ptr(), _ptr(T), ws.data_ptr(), ws.numel() * ws.element_size(), _status_ptr(status, dev))
@@ -296,13 +303,13 @@ def mx_linear_bwd(dY, X, T, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropo
         if wb is None or (wb.rows, wb.cols) != (K, N) or wb.device != dev:
             _bad("dX needs the weight's backward form (mx_weight(W), w.bwd)")
         d = ctypes.byref(wb.descriptor())
-        dX = _output(dX, "dX", (M, K), torch.bfloat16, dev)
+        dX = _output(dX, "dX", (M, K), torch.bfloat16, dY)
     if adapter and (need_dL1 or dL1 is not None):
         _tensor(X, "X", (M, K), torch.bfloat16, dev)
-        dL1 = _output(dL1, "dL1", (K, r), torch.float32, dev)
+        dL1 = _output(dL1, "dL1", (K, r), torch.float32, dY)
     if adapter and (need_dL2 or dL2 is not None):
         _tensor(T, "T", (M, r), torch.float32, dev)
-        dL2 = _output(dL2, "dL2", (r, N), torch.float32, dev)
+        dL2 = _output(dL2, "dL2", (r, N), torch.float32, dY)
     if not adapter:
         dL1 = dL2 = None
     if M == 0:
@@ -310,7 +317,7 @@ def mx_linear_bwd(dY, X, T, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropo
             if g is not None:
                 g.zero_()
         return dX, dL1, dL2
-    r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, dev)
+    r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, dY)
     _call(dev, _q.lib().qlora_mx_linear_bwd, dY.data_ptr(), _ptr(X) if dL1 is not None else None, M,
           _ptr(T) if dL2 is not None else None, d, N, K, _ptr(L1), _ptr(L2), r, s, cfg, _ptr(dX), _ptr(dL1), _ptr(dL2),
           ws.data_ptr(), ws.numel() * ws.element_size(), _status_ptr(status, dev))
