@@ -313,10 +313,28 @@ cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, bool dependent
 
 // Quantise X and form D = drop(X).L in one pass (mx_prep.cu).
 struct MxPrepPlan {
-  int units_per_tile;  // units (128 rows x 256 columns) of a row tile
+  int units_per_tile;   // units (128 rows x 256 columns) of a row tile
   int64_t units;
-  int grid, maxc;      // CTAs; most CTAs that share a row tile
-  size_t part_bytes;   // fp32 [row tiles][maxc][128][r]
+  bool direct;          // a cluster of `cluster` CTAs finishes a row tile
+  int cluster;
+  int grid, maxc;       // CTAs; most CTAs that share a row tile (not direct)
+  size_t part_bytes;    // fp32 [row tiles][maxc][128][r] (not direct)
+};
+// What becomes of D.
+struct MxPrepFinish {
+  int64_t M;
+  float* T;             // alpha D (may be null)
+  float alpha;
+  uint16_t* out;        // `terms` bf16 terms of beta D
+  int terms;
+  float beta;
+  const float* T_in;    // when not null: out2 = three bf16 terms of gamma T_in
+  uint16_t* out2;
+  float gamma;
+  const float* part;    // from here filled by the launch
+  int r;
+  int64_t units;
+  int units_per_tile, grid, maxc;
 };
 struct MxPrepArgs {
   CUtensorMap tmX;      // bf16 [M][C], box 64 x 128, 128-byte swizzle
@@ -328,28 +346,14 @@ struct MxPrepArgs {
   int r, r16, l_mn;     // r16: r rounded up to 16
   int64_t units;
   int units_per_tile, maxc;
+  int direct;
   float* part;
+  MxPrepFinish fin;
   DropArgs drop;
   int* status;
 };
-struct MxPrepFinish {
-  const float* part;
-  int64_t M;
-  int r;
-  float* T;            // alpha D (may be null)
-  float alpha;
-  uint16_t* out;       // `terms` bf16 terms of beta D
-  int terms;
-  float beta;
-  const float* T_in;   // when not null: out2 = three bf16 terms of gamma T_in
-  uint16_t* out2;
-  float gamma;
-  int64_t units;       // filled by the launch
-  int units_per_tile, grid, maxc;
-};
 MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms);
 cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st);
-cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, MxPrepFinish a, cudaStream_t st);
 
 // Adapter gradients (mx_grad.cu): problem 0 is dL1 = drop(X)^T.u, problem 1
 // dL2 = (dY^T.v)^T, either may be absent (cols 0).

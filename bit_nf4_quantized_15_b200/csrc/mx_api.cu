@@ -136,7 +136,8 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
 
 // Q(X) and the partial sums of D = drop(X).L (L MN-major [C][r] or K-major [r][C]).
 int prep(const uint16_t* X, int64_t M, int64_t C, const uint16_t* L, int l_mn, int r, const DropArgs& d,
-         uint8_t* codes, uint8_t* scales, float* part, const MxPrepPlan& p, int* status, cudaStream_t st) {
+         uint8_t* codes, uint8_t* scales, float* part, const MxPrepPlan& p, const MxPrepFinish& fin, int* status,
+         cudaStream_t st) {
   MxPrepArgs a;
   std::memset(&a, 0, sizeof(a));
   const int r16 = (r + 15) / 16 * 16;
@@ -151,6 +152,7 @@ int prep(const uint16_t* X, int64_t M, int64_t C, const uint16_t* L, int l_mn, i
   a.r = r;
   a.l_mn = l_mn;
   a.part = part;
+  a.fin = fin;
   a.drop = d;
   a.status = status;
   return launch_mx_prep(a, p, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
@@ -292,18 +294,15 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
 
   if (r) {
     float* part = reinterpret_cast<float*>(wb + lay.part);
-    if (int rc = prep(X, M, K, L1, 1, r, d, wb, wb + lay.q_scales, part, lay.prep_x, status_dev, st)) return rc;
     MxPrepFinish f;
     std::memset(&f, 0, sizeof(f));
-    f.part = part;
     f.M = M;
-    f.r = r;
     f.T = T_save;
     f.alpha = d.inv;
     f.out = sT;
     f.terms = 1;
     f.beta = s * d.inv;
-    if (launch_mx_prep_finish(lay.prep_x, f, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (int rc = prep(X, M, K, L1, 1, r, d, wb, wb + lay.q_scales, part, lay.prep_x, f, status_dev, st)) return rc;
   } else if (launch_mx_quantize(X, QLORA_DTYPE_BF16, M, K, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
     return QLORA_ERR_CUDA;
   }
@@ -340,20 +339,17 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   // Q(dY) and dT = dY.L2^T, kept as three bf16 terms of s dT / (1 - p); with
   // them s T in three terms
   if (r && (dX || dL1)) {
-    if (int rc = prep(dY, M, N, L2, 0, r, DropArgs{}, wb, wb + lay.q_scales, part, lay.prep_dy, status_dev, st))
-      return rc;
     MxPrepFinish f;
     std::memset(&f, 0, sizeof(f));
-    f.part = part;
     f.M = M;
-    f.r = r;
     f.out = sdT;
     f.terms = 3;
     f.beta = s * d.inv;
     f.T_in = dL2 ? T_saved : nullptr;
     f.out2 = sT;
     f.gamma = s;
-    if (launch_mx_prep_finish(lay.prep_dy, f, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (int rc = prep(dY, M, N, L2, 0, r, DropArgs{}, wb, wb + lay.q_scales, part, lay.prep_dy, f, status_dev, st))
+      return rc;
   } else if (dX &&
              launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
     return QLORA_ERR_CUDA;

@@ -66,20 +66,6 @@ QDEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
-QDEV uint32_t mx_cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-QDEV float2 ld_peer_f2(uint32_t addr, uint32_t rank) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-               : "=f"(v.x), "=f"(v.y)
-               : "r"(mapa_shared(addr, rank))
-               : "memory");
-  return v;
-}
-
 // Zero the dropped entries of this warp's 32 lanes x 16 columns of the LoRA
 // term.  Lanes are consecutive output rows (elements), so 8 lanes share one
 // generator evaluation per column: lane l evaluates column c + (l & 7) for
@@ -112,7 +98,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
-  const int rank = (int)cluster_ctarank(), csize = (int)mx_cluster_size();
+  const int rank = (int)cluster_ctarank(), csize = (int)cluster_nctarank();
   const int id = (int)(blockIdx.x / (unsigned)csize);
   const int n_tiles = (args.cols + BN - 1) / BN;
   const int row_tile = id / n_tiles, col_tile = id % n_tiles;

@@ -201,8 +201,21 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(w[j])));
         }
+        const int64_t col = (int64_t)x.tile * 128 + row;
         if (!x.last) {
           tmem_st16(tl + sum_col + (uint32_t)c, v);
+        } else if (args.pieces == 1) {  // this CTA has the whole sum
+          if (col >= p.cols) continue;
+          if (p.transposed) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < r) p.out[(c + j) * p.cols + col] = __uint_as_float(v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              if (c + j < r)
+                *reinterpret_cast<uint4*>(p.out + col * r + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          }
         } else if (p.transposed) {  // slot [r][128]
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -329,8 +342,10 @@ MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool dro
   p.sh.grid = (int)(fit < num_sms ? fit : num_sms);
   // most CTAs that share a tile: its cost over a CTA's, and one at either end
   p.maxc = (int)((int64_t)p.pieces * p.sh.w0 * p.sh.grid / cost) + 2;
-  p.part0_bytes = (size_t)t0 * p.maxc * 128 * r * sizeof(float);
-  p.part_bytes = p.part0_bytes + (size_t)t1 * p.maxc * 128 * r * sizeof(float);
+  if (p.pieces > 1) {
+    p.part0_bytes = (size_t)t0 * p.maxc * 128 * r * sizeof(float);
+    p.part_bytes = p.part0_bytes + (size_t)t1 * p.maxc * 128 * r * sizeof(float);
+  }
   p.n16 = (3 * r + 15) / 16 * 16;
   const int r16 = (r + 15) / 16 * 16;
   p.nbuf = 2 * p.n16 + r16 <= 512 ? 2 : 1;
@@ -350,7 +365,7 @@ cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st) 
   a.stages = p.stages;
   const int smem = p.stages * (16384 + p.vboxes * 8192) + 512 + 1024;
   const cudaError_t err = launch_kernel<mx_grad_kernel>({dim3((unsigned)p.sh.grid), kGThreads, (size_t)smem, 1, true}, st, a);
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess || p.pieces == 1) return err;
   return launch_kernel<mx_grad_finish_kernel>({dim3((unsigned)(p.sh.units / p.pieces), (unsigned)((128 * a.r + 1023) / 1024)), 256, 0, 1, true},
                        st, a);
 }

@@ -86,6 +86,18 @@ QDEV void store_terms(uint16_t* out, float4 v, float beta, int terms, int r) {
   }
 }
 
+// Four neighbours D[row][j ..] to T and the bf16 terms.
+QDEV void emit4(const MxPrepFinish& a, int64_t row, int j, float4 d) {
+  if (a.T)
+    *reinterpret_cast<float4*>(a.T + row * a.r + j) =
+        make_float4(__fmul_rn(d.x, a.alpha), __fmul_rn(d.y, a.alpha), __fmul_rn(d.z, a.alpha), __fmul_rn(d.w, a.alpha));
+  store_terms(a.out + row * a.terms * a.r + j, d, a.beta, a.terms, a.r);
+}
+// The other operand of the backward's adapter sums rides along: s T in three terms.
+QDEV void emit_t4(const MxPrepFinish& a, int64_t row, int j) {
+  store_terms(a.out2 + row * 3 * a.r + j, *reinterpret_cast<const float4*>(a.T_in + row * a.r + j), a.gamma, 3, a.r);
+}
+
 template <bool WIDE>
 __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_constant__ MxPrepArgs args) {
   using C = PrepCfg<WIDE>;
@@ -103,10 +115,14 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
-  const int64_t u_lo = prep_unit(args.units, (int)gridDim.x, blockIdx.x);
-  const int64_t u_hi = prep_unit(args.units, (int)gridDim.x, (int64_t)blockIdx.x + 1);
-  const int n_units = (int)(u_hi - u_lo);
   const int upt = args.units_per_tile;
+  const int csize = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
+  const int64_t tile0 = blockIdx.x / (unsigned)csize;  // direct: this cluster's row tile
+  const int64_t u_lo = args.direct ? tile0 * upt + (int64_t)rank * upt / csize
+                                   : prep_unit(args.units, (int)gridDim.x, blockIdx.x);
+  const int64_t u_hi = args.direct ? tile0 * upt + (int64_t)(rank + 1) * upt / csize
+                                   : prep_unit(args.units, (int)gridDim.x, (int64_t)blockIdx.x + 1);
+  const int n_units = (int)(u_hi - u_lo);
   const bool drop = args.drop.threshold != 0;
 
   if (tid == 0) {
@@ -239,7 +255,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
       if (!warp_wait_backoff(wfull + b, (uint32_t)(piece >> 1) & 1u, abort_flag, args.status, lane, 100)) break;
       tc_fence_after();
       float* dst = nullptr;
-      if (last) {  // this run's rows of D: the slot of (row tile, ordinal of this CTA in it)
+      if (last && !args.direct) {  // this run's rows of D: the slot of (row tile, ordinal of this CTA in it)
         const int64_t tile = (u_lo + u) / upt;
         const int ord = (int)blockIdx.x - prep_owner(args.units, (int)gridDim.x, tile * upt);
         dst = args.part + ((tile * args.maxc + ord) * 128 + q4 * 32 + lane) * args.r;
@@ -256,7 +272,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
         } else {
           tmem_wait_ld();
         }
-        if (!last) {
+        if (!last || args.direct) {
           tmem_st16(tl + kSumCol + (uint32_t)c, v);
         } else {
 #pragma unroll
@@ -358,6 +374,45 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
     }
     __syncthreads();
   }
+  if (args.direct) {
+    // The cluster holds its row tile's D: partial sums to shared memory (the
+    // ring is done with), added in rank order, 128 / csize rows a CTA.
+    const int r = args.r, pitch = r + 4;
+    float* red = reinterpret_cast<float*>(smem);
+    if (warp >= 4 && warp < 8) {
+      tc_fence_after();
+      const int row = (warp & 3) * 32 + lane;
+      for (int c = 0; c < args.r16; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kSumCol + (uint32_t)c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          if (c + j < r)
+            *reinterpret_cast<uint4*>(red + row * pitch + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync_all();
+    const MxPrepFinish& f = args.fin;
+    const int rows = 128 / csize, r4 = r / 4;
+    const bool good = !*abort_flag;
+    for (int i = tid; i < rows * r4; i += kPrepThreads) {
+      const int lr = rank * rows + i / r4, j = (i % r4) * 4;
+      const int64_t row = tile0 * 128 + lr;
+      if (!good || row >= f.M) continue;
+      const uint32_t at = smem_u32(red + lr * pitch + j);
+      float4 d = ld_peer_f4(at, 0);
+      for (int c = 1; c < csize; ++c) {
+        const float4 q = ld_peer_f4(at, (uint32_t)c);
+        d = make_float4(__fadd_rn(d.x, q.x), __fadd_rn(d.y, q.y), __fadd_rn(d.z, q.z), __fadd_rn(d.w, q.w));
+      }
+      emit4(f, row, j, d);
+      if (f.T_in) emit_t4(f, row, j);
+    }
+    cluster_sync_all();  // peers may still be reading this CTA's rows
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -383,19 +438,9 @@ __global__ void __launch_bounds__(256) mx_prep_finish_kernel(const __grid_consta
       const float4 q = *reinterpret_cast<const float4*>(p + (int64_t)c * 128 * a.r + i);
       d = make_float4(__fadd_rn(d.x, q.x), __fadd_rn(d.y, q.y), __fadd_rn(d.z, q.z), __fadd_rn(d.w, q.w));
     }
-    if (a.T)
-      *reinterpret_cast<float4*>(a.T + tile * 128 * a.r + i) =
-          make_float4(__fmul_rn(d.x, a.alpha), __fmul_rn(d.y, a.alpha), __fmul_rn(d.z, a.alpha), __fmul_rn(d.w, a.alpha));
     const int row = i / a.r, j = i - row * a.r;
-    store_terms(a.out + (tile * 128 + row) * a.terms * a.r + j, d, a.beta, a.terms, a.r);
-  }
-  // the other operand of the backward's adapter sums rides along: s T in three terms
-  if (a.T_in) {
-    const float* t = a.T_in + tile * 128 * a.r;
-    for (int i = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4; i < n; i += (int)gridDim.y * 1024) {
-      const int row = i / a.r, j = i - row * a.r;
-      store_terms(a.out2 + (tile * 128 + row) * 3 * a.r + j, *reinterpret_cast<const float4*>(t + i), a.gamma, 3, a.r);
-    }
+    emit4(a, tile * 128 + row, j, d);
+    if (a.T_in) emit_t4(a, tile * 128 + row, j);
   }
 }
 
@@ -409,11 +454,22 @@ __global__ void __launch_bounds__(256) split3_kernel(const float* __restrict__ i
 
 }  // namespace
 
+// A row tile's columns go to a cluster of up to 8 CTAs that finishes it alone
+// while the clusters of all tiles run at once; more tiles are cut into equal
+// runs of units, with a second kernel for what the runs share.
 MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms) {
   MxPrepPlan p{};
   p.units_per_tile = (int)((C + 255) / 256);
   const int64_t tiles = (M + 127) / 128;
   p.units = tiles * p.units_per_tile;
+  p.cluster = 1;
+  while (p.cluster < 8 && 2 * p.cluster <= p.units_per_tile) p.cluster *= 2;
+  p.direct = tiles * p.cluster <= num_sms || p.units_per_tile == 1;
+  if (p.direct) {
+    p.grid = (int)(tiles * p.cluster);
+    return p;
+  }
+  p.cluster = 1;
   p.grid = (int)(p.units < num_sms ? p.units : num_sms);
   const int64_t per = p.units / p.grid;  // the least units of a CTA
   p.maxc = (int)((p.units_per_tile + per - 1) / per) + 1;
@@ -426,20 +482,22 @@ cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) 
   a.units = p.units;
   a.units_per_tile = p.units_per_tile;
   a.maxc = p.maxc;
+  a.direct = p.direct;
   a.r16 = (a.r + 15) / 16 * 16;
-  return a.r > 64 ? launch_kernel<mx_prep_kernel<true>>({dim3((unsigned)p.grid), kPrepThreads, PrepCfg<true>::TOTAL, 1, false}, st, a)
-                  : launch_kernel<mx_prep_kernel<false>>({dim3((unsigned)p.grid), kPrepThreads, PrepCfg<false>::TOTAL, 1, false}, st, a);
-}
-
-cudaError_t launch_mx_prep_finish(const MxPrepPlan& p, MxPrepFinish a, cudaStream_t st) {
-  a.units = p.units;
-  a.units_per_tile = p.units_per_tile;
-  a.grid = p.grid;
-  a.maxc = p.maxc;
-  const int64_t tiles = (a.M + 127) / 128;
-  const int rows = (int)(a.M < 128 ? a.M : 128);
-  return launch_kernel<mx_prep_finish_kernel>({dim3((unsigned)tiles, (unsigned)((rows * a.r + 1023) / 1024)), 256, 0, 1, true},
-                       st, a);
+  a.fin.part = a.part;
+  a.fin.r = a.r;
+  a.fin.units = p.units;
+  a.fin.units_per_tile = p.units_per_tile;
+  a.fin.grid = p.grid;
+  a.fin.maxc = p.maxc;
+  const LaunchShape narrow{dim3((unsigned)p.grid), kPrepThreads, PrepCfg<false>::TOTAL, (unsigned)p.cluster, false};
+  const LaunchShape wide{dim3((unsigned)p.grid), kPrepThreads, PrepCfg<true>::TOTAL, (unsigned)p.cluster, false};
+  const cudaError_t e = a.r > 64 ? launch_kernel<mx_prep_kernel<true>>(wide, st, a)
+                                 : launch_kernel<mx_prep_kernel<false>>(narrow, st, a);
+  if (e != cudaSuccess || p.direct) return e;
+  const int64_t tiles = (a.fin.M + 127) / 128;
+  return launch_kernel<mx_prep_finish_kernel>(
+      {dim3((unsigned)tiles, (unsigned)((128 * a.r + 1023) / 1024)), 256, 0, 1, true}, st, a.fin);
 }
 
 cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {
