@@ -38,12 +38,14 @@ QDEV uint32_t mx_codes8(const uint32_t* w, float f) {
     v[j] = __fmul2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), ff);
   return mx_codes8(v);
 }
-// Running maximum of |x| of bf16 pairs, NaN kept.
+// Running maximum of |x| of bf16 pairs, NaN kept; the sign bits are noise.
 QDEV uint32_t mx_absmax2(uint32_t m, uint32_t w) {
-  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
-                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
-  return *reinterpret_cast<const uint32_t*>(&r);
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w));
+  return r;
 }
+// The larger of the two as fp32 bits.
+QDEV uint32_t mx_absmax_bits(uint32_t m) { return max(m & 0x7FFFu, (m >> 16) & 0x7FFFu) << 16; }
 
 }  // namespace
 }  // namespace qnf4

@@ -332,16 +332,18 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
           *reinterpret_cast<uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
         }
       }
-      fence_proxy_async_smem();  // these reads and writes before the MMAs and the TMA refill
-      __syncwarp();
-      if (lane == 0) {
-        if (drop) mbar_arrive(ready + s);
-        mbar_arrive(empty + s);
+      if (drop) {
+        fence_proxy_async_smem();  // before the MMAs read the tile
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready + s);
       }
-      uint32_t m2 = 0;  // largest |x|, two lanes
+      uint32_t m2 = 0, m3 = 0;  // largest |x|, two lanes each
 #pragma unroll
-      for (int j = 0; j < 16; ++j) m2 = mx_absmax2(m2, w[j]);
-      const uint32_t b = mx_scale_byte(max(m2 & 0xFFFFu, m2 >> 16) << 16);
+      for (int j = 0; j < 8; ++j) {
+        m2 = mx_absmax2(m2, w[j]);
+        m3 = mx_absmax2(m3, w[8 + j]);
+      }
+      const uint32_t b = mx_scale_byte(mx_absmax_bits(mx_absmax2(m2, m3)));
       bad |= b == 255u;
       const float f = mx_inv_scale(b);
       uint32_t c[4];
@@ -351,9 +353,13 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
       const int blk = 2 * q + half;  // 32-block of the unit
       *reinterpret_cast<uint4*>(so + rl * 128 + ((blk ^ (rl & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
       so[16384 + (blk >> 2) * 512 + (rl & 31) * 16 + (rl >> 5) * 4 + (blk & 3)] = (uint8_t)b;
-      fence_proxy_async_smem();  // before the TMA store reads the staging buffer
+      // the tile's reads before the TMA refills it, the codes before the TMA stores them
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ofull + ob);
+      if (lane == 0) {
+        mbar_arrive(empty + s);
+        mbar_arrive(ofull + ob);
+      }
       s += kQGroups;
       if (s >= kS) {
         s -= kS;

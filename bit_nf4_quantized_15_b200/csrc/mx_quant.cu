@@ -53,7 +53,7 @@ QDEV uint32_t absmax8(const uint32_t* w) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = mx_absmax2(m, w[j]);
-    return max(m & 0x7FFFu, (m >> 16) & 0x7FFFu) << 16;
+    return mx_absmax_bits(m);
   } else {
     uint32_t m = 0;
 #pragma unroll
