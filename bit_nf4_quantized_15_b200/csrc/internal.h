@@ -297,6 +297,7 @@ struct MxPairArgs {
   CUtensorMap tmSB;  // the same, box 256 x 2
   CUtensorMap tmAx;  // LoRA term: bf16 [rows][r], K-major
   CUtensorMap tmBx;  // LoRA term: B side (K- or MN-major per b_mn_ext)
+  CUtensorMap tmOut; // bf16 output [rows][ldo], box 64 x 32, 128-byte swizzle
   int rows, cols;
   int64_t K;
   int kb;            // 256-wide reduction blocks

@@ -84,7 +84,7 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
     std::memset(&g, 0, sizeof(g));
     if (make_map(&g.tmA, xc, u8, 1, (uint64_t)K / 2, (uint64_t)M, 128, 128, sw) ||
         make_map(&g.tmB, wc, u8, 1, (uint64_t)K / 2, (uint64_t)N, 128, 128, sw) || map_scales(&g.tmSA, xs, M, K, 1) ||
-        map_scales(&g.tmSB, ws, N, K, 2))
+        map_scales(&g.tmSB, ws, N, K, 2) || (!out_f32 && map_operand(&g.tmOut, out, 0, M, N, 32)))
       return QLORA_ERR_CUDA;
     if (lora) {
       if (map_operand(&g.tmAx, lora->u, 0, M, lora->r, 128, lora->u_pitch) ||

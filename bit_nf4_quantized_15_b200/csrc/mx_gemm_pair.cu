@@ -38,12 +38,13 @@
 namespace qnf4 {
 namespace {
 
-constexpr int kXS = 6;                                  // stages
+constexpr int kXS = 5;                                  // stages
 constexpr int kXA = 16384, kXB = 16384;                 // 128 rows x 128 bytes of codes each
 constexpr int kXStage = kXA + kXB + 1024 + 2048;        // + scales of 128 token rows, 256 weight rows
-constexpr int kXBar = kXS * kXStage;
-constexpr int kXTotal = kXBar + 256 + 1024;
 constexpr int kXEpi = 8;                                // epilogue warps: 2 (column halves) x 4 lane quarters
+constexpr int kXOut = kXS * kXStage;                    // output staging, 32 rows x 64 bf16 a warp
+constexpr int kXBar = kXOut + kXEpi * 4096;
+constexpr int kXTotal = kXBar + 256 + 1024;
 constexpr int kXThreads = 64 + 32 * kXEpi;
 constexpr uint32_t kXAcc = 256, kXSf = 24;              // accumulator columns, scale columns of a stage
 constexpr int kXGroup = 8;                              // row tiles of a raster group
@@ -303,9 +304,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
       }
       if (!warp_wait(accum, ph, abort_flag, args.status, lane)) break;
       tc_fence_after();
-      const int64_t row = (int64_t)xy.m * 256 + rl;
       const int col = xy.n * 256 + half * 128;
       if constexpr (F32) {
+        const int64_t row = (int64_t)xy.m * 256 + rl;
         float* dst = reinterpret_cast<float*>(args.out) + row * args.ldo + col;
 #pragma unroll
         for (int c = 0; c < 128; c += 16) {
@@ -329,18 +330,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(drained0);
-        if (row < args.rows) {
-          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(args.out) + row * args.ldo + col;
+        // Out by TMA in two halves of 64 columns, through this warp's buffer: a
+        // thread has one row, and its own 16-byte stores would each touch half
+        // a sector of another row.
+        uint8_t* buf = smem + kXOut + (warp - 2) * 4096;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t* w = v[c >> 1] + 8 * (c & 1);
+        for (int h = 0; h < 2; ++h) {
+          if (lane == 0) bulk_wait_read<0>();  // the buffer's last store has read it
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t* w = v[4 * h + (c >> 1)] + 8 * (c & 1);
             const auto two = [&](int j) { return pack_bf16x2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])); };
-            if (col + 8 * c < args.cols)
-              *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(two(0), two(2), two(4), two(6));
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(two(0), two(2), two(4), two(6));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int r0 = xy.m * 256 + (int)rank * 128 + q4 * 32, c0 = col + 64 * h;
+          if (lane == 0 && r0 < args.rows && c0 < args.cols) {
+            tma_store_2d(&args.tmOut, buf, c0, r0);
+            bulk_commit();
           }
         }
       }
     }
+    if (!F32 && lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();

@@ -52,22 +52,6 @@ constexpr int kQGroups = 2;  // quantise groups of 8 warps (3 were a few percent
 constexpr int kPrepThreads = (8 + 8 * kQGroups) * 32;
 constexpr uint32_t kSumCol = 256;  // tensor memory: work accumulators at 0 and 128, the sum at 256
 
-QDEV void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"((uint64_t)m),
-               "r"(smem_u32(src)), "r"(x), "r"(y)
-               : "memory");
-}
-QDEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-QDEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-QDEV void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-QDEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // Units [lo, hi) of CTA c.
 __host__ __device__ inline int64_t prep_unit(int64_t units, int grid, int64_t c) { return c * units / grid; }
 // CTA that owns unit u.
