@@ -340,3 +340,139 @@ def test_expired_wait_is_reported_and_the_next_call_is_right(lib):
     lib.mx_matmul(a, b)
     assert lib.read_status() == -8
     assert torch.equal(lib.mx_matmul(a, b), ref) and lib.read_status() == 0
+
+
+# ------------------------------------------------- calls that are easy to break
+def test_offsets_past_32_bits(lib):
+    """More than 2^32 elements: the last rows are those of a small call."""
+    R, C, tail = 131077, 32800, 300
+    X = torch.zeros((R, C), dtype=torch.bfloat16, device="cuda")
+    X[-tail:] = _rand((tail, C), 1.0, 5)
+    t = lib.mx_quantize(X)
+    small = lib.mx_quantize(X[-tail:].contiguous())
+    assert torch.equal(t.codes.view(R, -1)[-tail:], small.codes.view(tail, -1))
+    values = lib.mx_dequant(t)
+    assert torch.equal(values[-tail:], lib.mx_dequant(small)) and not values[:-tail].any()
+    del values, t, small
+    out = lib.dropout(X, 0.5, 3, 1)
+    kept = out[-tail:] != 0
+    assert not out[:-tail].any()
+    assert abs(kept.float().mean().item() - 0.5) < 5 * 0.5 / (tail * C) ** 0.5 + 1e-3
+    # element i of the tail is element i of the whole: counters of one call after another
+    q = np.arange((R * C - 8000) // 8, R * C // 8, dtype=np.uint64)
+    lo, one = np.uint64(0xFFFFFFFF), np.ones_like(q)
+    w = O.philox4x32([q & lo, q >> np.uint64(32), one, 0 * one], (3, 0))
+    keep = np.stack([h for x in w for h in (x & np.uint64(0xFFFF), x >> np.uint64(16))], 1).reshape(-1) >= 32768
+    last = out.view(-1)[-len(keep):].cpu().float().numpy() != 0
+    assert np.array_equal(last, keep & (X.view(-1)[-len(keep):].cpu().float().numpy() != 0))
+    del out, X
+    M, N, K = 70001, 65536, 32
+    a, b = lib.mx_quantize(_rand((M, K), 1.0, 6)), lib.mx_quantize(_rand((N, K), 1.0, 7))
+    big = lib.mx_matmul(a, b)
+    head = lib.mx_quantize(lib.mx_dequant(a)[-tail:].contiguous())
+    assert torch.equal(big[-tail:], lib.mx_matmul(head, b))
+
+
+def test_dropped_nan_reaches_no_adapter_sum(lib):
+    """A NaN that the mask drops leaves T and dL1 finite; its row of Y is NaN
+    through the quantised product.  A kept one makes its row of T NaN."""
+    M, N, K, r, p = 130, 64, 96, 16, 0.5
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=6)
+    keep = O.dropout_keep(M * K, p, 9, 9).reshape(M, K)
+    row = 77
+    dropped, kept = int(np.flatnonzero(~keep[row])[0]), int(np.flatnonzero(keep[row])[0])
+    X[row, dropped] = float("nan")
+    drop = lib.Dropout(p, 9, 9)
+    Y, T = lib.mx_linear_fwd(X, w, L1, L2, 1.0, dropout=drop)
+    assert torch.isfinite(T).all() and torch.isnan(Y[row]).all() and torch.isfinite(Y[:row]).all()
+    _, dL1, dL2 = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 1.0, dropout=drop)
+    assert torch.isfinite(dL1).all() and torch.isfinite(dL2).all()
+    X[row, kept] = float("nan")
+    _, T = lib.mx_linear_fwd(X, w, L1, L2, 1.0, dropout=drop)
+    assert torch.isnan(T[row]).all() and torch.isfinite(T[row + 1:]).all()
+    assert lib.read_status() == -7
+
+
+@pytest.mark.parametrize("M", [3, 300, 2500])
+def test_two_streams_and_two_graphs_at_once(lib, M):
+    """Independent calls on two streams, and two captured graphs replayed in
+    turn and together, give the bits of calls one after another."""
+    N, K, r = 1056, 544, 40
+    sets = [_problem(lib, M, N, K, r, seed=s) for s in (30, 40)]
+
+    def step(i):
+        X, w, L1, L2, dY, _ = sets[i]
+        drop = lib.Dropout(0.2, 5, i)
+        Y, T = lib.mx_linear_fwd(X, w, L1, L2, 0.5, dropout=drop)
+        return (Y, T) + lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop)
+
+    ref = [step(0), step(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i] = step(i)
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for a, b in zip(ref[i], got[i]))
+    graphs, outs = [], []
+    for i in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(i))
+        graphs.append(g)
+    for _ in range(3):
+        for i in (0, 1):
+            streams[i].wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert all(torch.equal(a, b) for a, b in zip(ref[i], outs[i]))
+
+
+@pytest.mark.parametrize("r", range(8, 136, 8))
+def test_every_rank(lib, r):
+    """All ranks against the fp64 adapter sums (their operands are exact: the
+    error is that of fp32 sums), with and without the pieces of 512 tokens."""
+    for M, N, K in ((70, 96, 320), (1100, 64, 128)):
+        X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=r)
+        Y, T = lib.mx_linear_fwd(X, w, L1, L2, 1.0)
+        Tr = to_f64(X) @ to_f64(L1)
+        assert np.linalg.norm(to_f64(T) - Tr) <= 2e-6 * np.linalg.norm(Tr)
+        _, dL1, dL2 = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 1.0)
+        g1 = to_f64(X).T @ (to_f64(dY) @ to_f64(L2).T)
+        g2 = to_f64(T).T @ to_f64(dY)
+        assert np.linalg.norm(to_f64(dL1) - g1) <= 2e-6 * np.linalg.norm(g1)
+        assert np.linalg.norm(to_f64(dL2) - g2) <= 2e-6 * np.linalg.norm(g2)
+
+
+def test_binding_refusals(lib):
+    """Shapes, types, layouts and devices that a call does not take."""
+    X, w, L1, L2, dY, _ = _problem(lib, 8, 64, 96, 16, seed=3)
+    Y, T = lib.mx_linear_fwd(X, w, L1, L2, 1.0)
+    E = lib.QLoRAError
+    bad = [lambda: lib.mx_quantize(X[:, :48].contiguous()), lambda: lib.mx_quantize(X.t()),
+           lambda: lib.mx_quantize(X.double()), lambda: lib.mx_quantize(X, transpose=True),
+           lambda: lib.mx_quantize(X, out=lib.MXTensor.empty(9, 96)),
+           lambda: lib.mx_dequant(w.fwd, dtype=torch.float16),
+           lambda: lib.mx_matmul(lib.mx_quantize(X), w.bwd), lambda: lib.mx_matmul(w.fwd, lib.mx_quantize(X[:7])),
+           lambda: lib.mx_linear_fwd(X.half(), w, L1, L2, 1.0), lambda: lib.mx_linear_fwd(X, w, L1, None, 1.0),
+           lambda: lib.mx_linear_fwd(X, w, L1.t().contiguous(), L2, 1.0),
+           lambda: lib.mx_linear_fwd(X, w, L1[:, :12].contiguous(), L2[:12].contiguous(), 1.0),
+           lambda: lib.mx_linear_fwd(X, w, L1, L2, 1.0, dropout=lib.Dropout(1.0, 1)),
+           lambda: lib.mx_linear_fwd(X, w, L1, L2, 1.0, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: lib.mx_linear_fwd(X, w, L1, L2, 1.0, Y=Y.float()),
+           lambda: lib.mx_linear_bwd(dY, X, T, lib.MXWeight(w.fwd), L1, L2, 1.0),
+           lambda: lib.mx_linear_bwd(dY, X[:4], T, w, L1, L2, 1.0),
+           lambda: lib.mx_linear_bwd(dY, X, T.bfloat16(), w, L1, L2, 1.0),
+           lambda: lib.dropout(X.view(-1)[1:], 0.1, 1), lambda: lib.dropout(X, -0.1, 1),
+           lambda: lib.dropout(X, 0.1, 1, torch.zeros(2, dtype=torch.int64, device="cuda")),
+           lambda: lib.MXTensor(w.fwd.codes[:-1], w.fwd.scales, 64, 96).descriptor()]
+    for i, call in enumerate(bad):
+        with pytest.raises(E):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    assert lib.read_status() == 0
