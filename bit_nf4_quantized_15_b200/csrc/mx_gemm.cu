@@ -18,6 +18,11 @@
 // (the weight), B the tokens: with few tokens BN shrinks to 16 and a call
 // streams the weight once through all SMs.
 //
+// Measured: one token through 4096 x 4096 5.7 us; 16 tokens through 22016 x
+// 8192 19 us, where its 96 MB take 14.6 at the measured copy bandwidth; 1000 x
+// 2056 x 1568 9 us.  The small ones are launch, tensor memory, one round trip
+// to HBM and the epilogue, one after another.
+//
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, then 4 epilogue warps (8 for
 // BN >= 128).
 #include "engine_util.cuh"
@@ -197,7 +202,8 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
         if (one) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem, operand_desc(sa, args.a_mn_ext, kk), operand_desc(sa + C::A, 0, kk), id_ext, (it | kk) != 0);
+            umma_bf16(tmem, operand_desc(sa, args.a_mn_ext, kk), operand_desc(sa + C::A, 0, kk), id_ext,
+                      (it | kk) != 0);
           umma_commit(empty + s);
           if (it == n_ext - 1) umma_commit(ext_done);
         }
@@ -330,9 +336,8 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
 template <int BN>
 cudaError_t launch_bn(const MxGemmArgs& a, const MxGemmPlan& p, bool dependent, cudaStream_t st) {
   using C = MxCfg<BN>;
-  return launch_kernel<mx_gemm_kernel<BN>>({dim3((unsigned)(p.m_tiles * p.n_tiles * p.cluster)), C::THREADS, C::TOTAL, (unsigned)p.cluster,
-                        dependent},
-                       st, a);
+  const dim3 grid((unsigned)(p.m_tiles * p.n_tiles * p.cluster));
+  return launch_kernel<mx_gemm_kernel<BN>>({grid, C::THREADS, C::TOTAL, (unsigned)p.cluster, dependent}, st, a);
 }
 
 }  // namespace

@@ -86,6 +86,9 @@ QDEV float load1(const void* base, int64_t i) {
 // kRows rows in flight, as stored (fp32 takes twice the registers).  The block
 // maximum is two shuffles over 4 lanes.  The 512 scale bytes meet in shared
 // memory and leave as 16-byte stores, zeros outside the matrix.
+//
+// Bound by HBM: 8192 x 8192 bf16, 170 MB, 29 us (5.9 TB/s; 6.7 TB/s by the slope
+// over larger ones).
 template <int DT>
 __global__ void __launch_bounds__(kQT) mx_quantize_kernel(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kQT) mx_quantize_kernel(const void* __restrict
 // neither the row writes nor the column reads conflict); a thread then owns a
 // 32-block of one c.  The codes meet in shared memory too and leave as 64
 // bytes a row of the output.  (128 c a CTA left room for three CTAs an SM and
-// took half as long again.)
+// took longer: 45 against 41 us for 11008 x 4096 fp32, 204 MB.)
 template <int DT>
 __global__ void __launch_bounds__(kQT) mx_quantize_t_kernel(const void* __restrict__ X, int64_t R, int64_t C,
                                                             uint8_t* __restrict__ codes,
@@ -182,7 +185,8 @@ __global__ void __launch_bounds__(kQT) mx_quantize_t_kernel(const void* __restri
   for (int q = 0; q < 4; ++q) {
     float2 u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = __fmul2_rn(make_float2(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]), make_float2(f, f));
+    for (int j = 0; j < 4; ++j)
+      u[j] = __fmul2_rn(make_float2(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]), make_float2(f, f));
     w[q] = mx_codes8(u);
   }
   s_c[cl][blk] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -213,6 +217,7 @@ QDEV float2 values2(uint32_t byte, float lo, float hi) {
 
 // One CTA per scale tile again, the quantiser's mapping: its 512 scale bytes
 // through shared memory, 8 rows' codes in flight a thread, 16-byte stores.
+// Bound by HBM: 8192 x 8192 to bf16, 170 MB, 28 us.
 template <int DT>
 __global__ void __launch_bounds__(kQT) mx_dequant_kernel(const uint32_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scales, int64_t rows,
@@ -244,8 +249,8 @@ __global__ void __launch_bounds__(kQT) mx_dequant_kernel(const uint32_t* __restr
     for (int j = 0; j < 4; ++j) v[j] = values2((w[i] >> (8 * j)) & 255u, lo, hi);
     uint4* o = po + i * step * (kWords<DT> / 4);
     if constexpr (DT == QLORA_DTYPE_F32) {
-      o[0] = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
-      o[1] = make_uint4(__float_as_uint(v[2].x), __float_as_uint(v[2].y), __float_as_uint(v[3].x), __float_as_uint(v[3].y));
+      reinterpret_cast<float4*>(o)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      reinterpret_cast<float4*>(o)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     } else {
       *o = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
                       pack_bf16x2(v[3].x, v[3].y));
@@ -261,7 +266,8 @@ QDEV void store1(void* out, int64_t i, float v) {
 }
 
 // out = x inv where kept, else 0 (a selection: a dropped Inf or NaN is 0).
-// Eight elements (one generator evaluation) a thread and step.
+// Eight elements (one generator evaluation) a thread and step.  Bound by HBM:
+// 8192 x 8192 bf16, 268 MB, 50 us (5.4 TB/s), with the integer pipes 60 % busy.
 template <int DT>
 __global__ void __launch_bounds__(kQT) dropout_kernel(const void* __restrict__ X, int64_t n, DropArgs d,
                                                       void* __restrict__ out) {

@@ -135,7 +135,8 @@ class MXTensor:
         if not (c.is_cuda and c.dtype == torch.uint8 and s.dtype == torch.uint8 and s.device == c.device
                 and c.is_contiguous() and s.is_contiguous() and 2 * c.numel() >= self.rows * self.cols
                 and s.numel() >= 512 * tiles):
-            _bad(f"codes and scales must be contiguous uint8 CUDA tensors on one device that hold {self.rows} x {self.cols}")
+            _bad("codes and scales must be contiguous uint8 CUDA tensors on one device that hold "
+                 f"{self.rows} x {self.cols}")
         return qlora_mx_tensor(c.data_ptr(), s.data_ptr(), self.rows, self.cols)
 
 

@@ -432,7 +432,8 @@ QLORA_API int qlora_set_gemm_events(void* ev_start, void* ev_end);
 /* Failure-detection test hook (diagnostic; the method has no counterpart).
  * The next fused dequant-GEMM launch of qlora_linear_fwd or qlora_linear_bwd
  * (the Y launch of a forward with more than 16 tokens, resp. the dX launch
- * of a backward; not the opt-in CTA-pair forward) runs with its TMA producer
+ * of a backward; not the opt-in CTA-pair forward), or the next MXFP4 product
+ * (on the cluster kernel whatever its size), runs with its TMA producer
  * issuing no loads and every internal wait bounded by wait_ns nanoseconds
  * instead of 4 s.  Its waits then expire: the kernel writes
  * QLORA_ERR_TIMEOUT to *status_dev, frees its tensor memory and returns

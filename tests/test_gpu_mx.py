@@ -109,7 +109,7 @@ def test_quantise_special_values(lib, transpose):
 MATMULS = [(1, 8, 32), (1, 128, 64), (3, 136, 4096), (16, 64, 96), (17, 136, 160), (32, 1032, 2048), (33, 200, 256),
            (64, 1000, 288), (65, 8, 512), (128, 264, 1056), (129, 128, 2080), (256, 256, 256), (257, 520, 320),
            (300, 2056, 1568), (1000, 264, 4128), (513, 3000, 416),
-           (2300, 2312, 416), (2433, 2184, 64), (4100, 1288, 2336), (2304, 4864, 32)]   # CTA pairs, ragged in each direction
+           (2300, 2312, 416), (2433, 2184, 64), (4100, 1288, 2336), (2304, 4864, 32)]   # CTA pairs, ragged
 
 
 @pytest.mark.parametrize("M,N,K", MATMULS)
