@@ -24,11 +24,11 @@ struct LaunchShape {
   bool dependent;    // starts while the kernel before it on the stream still runs
 };
 
-// The shared-memory attribute is set once per kernel and device, to all that a
-// block may have; a launch that fails for want of it (the device was reset in
-// between) sets it again.
+// The shared-memory attribute (all that a block may have) and that for clusters
+// of more than 8 are set once per kernel and device; a launch that fails for
+// want of them (the device was reset in between) sets them again.
 template <auto* Kern>
-cudaError_t allow_smem(bool again) {
+cudaError_t allow_big(bool again) {
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -36,6 +36,7 @@ cudaError_t allow_smem(bool again) {
   const uint64_t bit = 1ull << (dev & 63);
   if (!again && (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
   e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
@@ -44,7 +45,7 @@ template <auto* Kern, class... A>
 cudaError_t launch_kernel(const LaunchShape& s, cudaStream_t st, const A&... args) {
   const bool big = s.smem > 48 * 1024;
   if (big) {
-    const cudaError_t e = allow_smem<Kern>(false);
+    const cudaError_t e = allow_big<Kern>(false);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -67,7 +68,7 @@ cudaError_t launch_kernel(const LaunchShape& s, cudaStream_t st, const A&... arg
   cfg.attrs = at;
   cfg.numAttrs = n;
   cudaError_t e = cudaLaunchKernelEx(&cfg, Kern, args...);
-  if (e == cudaErrorInvalidValue && big && allow_smem<Kern>(true) == cudaSuccess) {
+  if (e == cudaErrorInvalidValue && big && allow_big<Kern>(true) == cudaSuccess) {
     (void)cudaGetLastError();
     e = cudaLaunchKernelEx(&cfg, Kern, args...);
   }

@@ -302,8 +302,10 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
         }
       const int q = it & 3, ob = u & 1;
       uint8_t* so = smem + C::OUT + ob * C::OUTB;
+      // a warp whose 32 rows are all past the last one only zeroes their scales
+      const bool live = tile * 128 + (rl & 96) < args.fin.M;
       uint4 rnd[4];
-      if (drop) {  // the generator needs no data: evaluated before the wait
+      if (drop && live) {  // the generator needs no data: evaluated before the wait
         const uint64_t e8 = (uint64_t)((tile * 128 + rl) * args.cols + kb * 256 + 64 * q + 32 * half) >> 3;
 #pragma unroll
         for (int j = 0; j < 4; ++j) rnd[j] = philox4x32_10(e8 | j, key);  // e8 is a multiple of 4
@@ -312,40 +314,43 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
       }
       if (!warp_poll<20>(full + s, ph, abort_flag, args.status, lane)) break;
       uint8_t* sx = smem + s * C::STAGE + rl * 128;
-      uint32_t w[16];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint4 v = *reinterpret_cast<const uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4));
-        w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-      }
-      if (drop) {
+      uint32_t c[4], b = 0;
+      if (live) {
+        uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t z[4] = {w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
-          drop8_bf16(z, rnd[j], thr);
-          *reinterpret_cast<uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
+          const uint4 v = *reinterpret_cast<const uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4));
+          w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
         }
-      }
-      if (drop) {
-        fence_proxy_async_smem();  // before the MMAs read the tile
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ready + s);
-      }
-      uint32_t m2 = 0, m3 = 0;  // largest |x|, two lanes each
+        if (drop) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m2 = mx_absmax2(m2, w[j]);
-        m3 = mx_absmax2(m3, w[8 + j]);
-      }
-      const uint32_t b = mx_scale_byte(mx_absmax_bits(mx_absmax2(m2, m3)));
-      bad |= b == 255u;
-      const float f = mx_inv_scale(b);
-      uint32_t c[4];
+          for (int j = 0; j < 4; ++j) {
+            uint32_t z[4] = {w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
+            drop8_bf16(z, rnd[j], thr);
+            *reinterpret_cast<uint4*>(sx + (((4 * half + j) ^ (rl & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+          fence_proxy_async_smem();  // before the MMAs read the tile
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready + s);
+        }
+        uint32_t m2 = 0, m3 = 0;  // largest |x|, two lanes each
 #pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = mx_codes8(w + 4 * j, f);
+        for (int j = 0; j < 8; ++j) {
+          m2 = mx_absmax2(m2, w[j]);
+          m3 = mx_absmax2(m3, w[8 + j]);
+        }
+        b = mx_scale_byte(mx_absmax_bits(mx_absmax2(m2, m3)));
+        bad |= b == 255u;
+        const float f = mx_inv_scale(b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = mx_codes8(w + 4 * j, f);
+      } else if (drop && lane == 0) {
+        mbar_arrive(ready + s);
+      }
       if (!warp_poll<20>(oempty + ob, ((uint32_t)(u >> 1) & 1u) ^ 1u, abort_flag, args.status, lane)) break;
       const int blk = 2 * q + half;  // 32-block of the unit
-      *reinterpret_cast<uint4*>(so + rl * 128 + ((blk ^ (rl & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
+      if (live)
+        *reinterpret_cast<uint4*>(so + rl * 128 + ((blk ^ (rl & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
       so[16384 + (blk >> 2) * 512 + (rl & 31) * 16 + (rl >> 5) * 4 + (blk & 3)] = (uint8_t)b;
       // the tile's reads before the TMA refills it, the codes before the TMA stores them
       fence_proxy_async_smem();
@@ -454,17 +459,20 @@ __global__ void __launch_bounds__(256) split3_kernel(const float* __restrict__ i
 
 }  // namespace
 
-// A row tile's columns go to a cluster of up to 8 CTAs that finishes it alone
-// while the clusters of all tiles run at once; more tiles are cut into equal
-// runs of units, with a second kernel for what the runs share.
+// Up to 8 row tiles of up to two units a CTA go to clusters of 8 (16 for up to
+// 4 tiles) that finish their tile alone; the rest is cut into equal runs of
+// units, with a second kernel for what the runs share.  Forward with 1024
+// features, both measured: 1 x 8192 13.6 us on a cluster, 15.1 in runs; 600 x
+// 4096 22.9 and 22.6 (and a launch less); 2000 x 4096 30.2 and 24.7 (16
+// clusters of 8 do not all fit at once).
 MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms) {
   MxPrepPlan p{};
   p.units_per_tile = (int)((C + 255) / 256);
   const int64_t tiles = (M + 127) / 128;
   p.units = tiles * p.units_per_tile;
   p.cluster = 1;
-  while (p.cluster < 8 && 2 * p.cluster <= p.units_per_tile) p.cluster *= 2;
-  p.direct = tiles * p.cluster <= num_sms || p.units_per_tile == 1;
+  while (p.cluster < (tiles <= 4 ? 16 : 8) && 2 * p.cluster <= p.units_per_tile) p.cluster *= 2;
+  p.direct = (tiles <= 8 && p.units_per_tile <= 2 * p.cluster) || p.units_per_tile == 1;
   if (p.direct) {
     p.grid = (int)(tiles * p.cluster);
     return p;
