@@ -372,14 +372,15 @@ struct MxGradShare {  // how the units are shared out
 };
 struct MxGradPlan {
   MxGradShare sh;
-  int pieces, maxc, n16, nbuf, vboxes, stages;
+  int piece, pieces;      // 64-token stages of a unit, units of a tile
+  int maxc, n16, nbuf, vboxes, stages;
   size_t part0_bytes, part_bytes;
 };
 struct MxGradArgs {
   MxGradProblem p[2];
   int M, r;
   MxGradShare sh;
-  int pieces, maxc;
+  int piece, pieces, maxc;
   int n16, nbuf;       // columns of an accumulator (3r up to 16), accumulators
   int vboxes, stages;
   DropArgs drop;       // mask of X

@@ -7,12 +7,14 @@
 // over the tokens and reads all of X or dY: the bound is those bytes, with
 // the terms' 6 r bytes a token read again (from L2) for every 128 columns.
 //
-// A unit is 128 columns of X or dY x 512 tokens: one accumulation in tensor
-// memory (the tensor cores' truncation grows with the length of a sum, see
-// mx_prep.cu), three groups of r columns wide; the sum warps add the groups,
-// and units of one run to one another, with rounding.  One CTA per SM takes an equal
-// run of units; both gradients are one launch, so that a small one fills the
-// other's tail.  Runs end in partial slots that a second kernel adds in order.
+// A unit is 128 columns of X or dY x 512 tokens (256 for small problems with
+// dropout): one accumulation in tensor memory (the tensor cores' truncation
+// grows with the length of a sum, see mx_prep.cu), three groups of r columns
+// wide; the sum warps add the groups, and units of one run to one another,
+// with rounding.  One CTA per SM takes a run of units of equal cost; both
+// gradients are one launch, so that a small one fills the other's tail.  A
+// tile that is one unit is written at once; other runs end in partial slots
+// that a second kernel adds in order.
 //
 // With dropout the X tile is masked in shared memory before the MMAs read it.
 //
@@ -36,7 +38,7 @@ namespace {
 constexpr int kGThreads = 24 * 32;
 constexpr int kGMaxS = 6;
 constexpr int kGBudget = 220 * 1024;  // bytes of the stages
-constexpr int kGPiece = 8;            // 64-token stages of a unit
+constexpr int kGPiece = 8;            // 64-token stages of a unit, at most
 
 // Runs are equal in cost: a unit of dL1 with dropout counts 3, others 2 (the
 // mask takes about as long as half a unit's loads).  CTA of a unit, and the
@@ -55,7 +57,7 @@ __host__ __device__ inline int64_t grad_first(const MxGradShare& a, int64_t c) {
 struct UnitAt {
   int prob;      // 0: dL1, 1: dL2
   int tile;      // 128-column tile
-  int piece;     // 512-token piece
+  int piece;     // piece of the tokens
   bool last;     // no further piece of this tile in the run
 };
 QDEV UnitAt unit_at(const MxGradArgs& a, int64_t u, int64_t u_hi) {
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
       for (int64_t u = u_lo; u < u_hi && ok; ++u) {
         const UnitAt x = unit_at(args, u, u_hi);
         const MxGradProblem& p = args.p[x.prob];
-        const int t0 = x.piece * 64 * kGPiece, n = min(kGPiece, (args.M - t0 + 63) / 64);
+        const int t0 = x.piece * 64 * args.piece, n = min(args.piece, (args.M - t0 + 63) / 64);
         for (int i = 0; i < n; ++i) {
           if (!(ok = mbar_wait_backoff(empty + s, ph ^ 1u, abort_flag, args.status, 20))) break;
           uint8_t* sa = smem + s * stage;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
     for (int64_t u = u_lo; u < u_hi && ok; ++u) {
       const UnitAt x = unit_at(args, u, u_hi);
       const bool masked = x.prob == 0 && args.drop.threshold;
-      const int t0 = x.piece * 64 * kGPiece, n = min(kGPiece, (args.M - t0 + 63) / 64);
+      const int t0 = x.piece * 64 * args.piece, n = min(args.piece, (args.M - t0 + 63) / 64);
       if (!(ok = warp_poll<40>(wempty + b, wph ^ 1u, abort_flag, args.status, lane))) break;
       const uint32_t d = tmem + (uint32_t)(b * args.n16);
       for (int i = 0; i < n; ++i) {
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
     bool ok = true;
     for (int64_t u = u_lo; u < u_hi && u < args.sh.units0 && ok; ++u) {
       const UnitAt x = unit_at(args, u, u_hi);
-      const int t0 = x.piece * 64 * kGPiece, n = min(kGPiece, (args.M - t0 + 63) / 64);
+      const int t0 = x.piece * 64 * args.piece, n = min(args.piece, (args.M - t0 + 63) / 64);
       for (int i = 0; i < n; ++i, turn ^= 1) {
         if (turn == grp) {
           // this thread's evaluations before the wait: they need no data
@@ -341,8 +343,13 @@ __global__ void __launch_bounds__(256) mx_grad_finish_kernel(const __grid_consta
 
 MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool drop, int num_sms) {
   MxGradPlan p{};
-  p.pieces = (int)((M + 64 * kGPiece - 1) / (64 * kGPiece));
   const int64_t t0 = (cols0 + 127) / 128, t1 = (cols1 + 127) / 128;
+  // The masked stages of a unit follow one another at 1.2 us; units of half the
+  // length are worth their second kernel while there is no unit for every SM
+  // (gradients of 512 x 512 x 512, r = 64: 21 us with dropout against 27, but
+  // without 16.3 and 17.8, and for 400 x 4096 x 4096 21.6 against 18.5).
+  p.piece = drop && (t0 + t1) * ((M + 64 * kGPiece - 1) / (64 * kGPiece)) < num_sms ? kGPiece / 2 : kGPiece;
+  p.pieces = (int)((M + 64 * p.piece - 1) / (64 * p.piece));
   p.sh.units0 = t0 * p.pieces;
   p.sh.units = p.sh.units0 + t1 * p.pieces;
   p.sh.w0 = drop && t0 ? 3 : 2;
@@ -369,6 +376,7 @@ MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool dro
 cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st) {
   a.sh = p.sh;
   a.pieces = p.pieces;
+  a.piece = p.piece;
   a.maxc = p.maxc;
   a.n16 = p.n16;
   a.nbuf = p.nbuf;
