@@ -281,7 +281,7 @@ def mx_linear_fwd(X, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropout: Dro
         return Y, T
     r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, X)
     d = wf.descriptor()
-    _call(dev, _q.lib().qlora_mx_linear_fwd, X.data_ptr(), M, ctypes.byref(d), _ptr(L1), _ptr(L2), r, s, cfg,
+    _call(dev, _q.lib().qlora_mx_linear_fwd, X.data_ptr(), M, ctypes.byref(d), _ptr(L1), _ptr(L2), r, float(s), cfg,
           Y.data_ptr(), _ptr(T), ws.data_ptr(), ws.numel() * ws.element_size(), _status_ptr(status, dev))
     return Y, T
 
@@ -320,8 +320,8 @@ def mx_linear_bwd(dY, X, T, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropo
         return dX, dL1, dL2
     r, cfg, ws = _linear_args(M, N, K, L1, L2, dropout, ws, dY)
     _call(dev, _q.lib().qlora_mx_linear_bwd, dY.data_ptr(), _ptr(X) if dL1 is not None else None, M,
-          _ptr(T) if dL2 is not None else None, d, N, K, _ptr(L1), _ptr(L2), r, s, cfg, _ptr(dX), _ptr(dL1), _ptr(dL2),
-          ws.data_ptr(), ws.numel() * ws.element_size(), _status_ptr(status, dev))
+          _ptr(T) if dL2 is not None else None, d, N, K, _ptr(L1), _ptr(L2), r, float(s), cfg, _ptr(dX), _ptr(dL1),
+          _ptr(dL2), ws.data_ptr(), ws.numel() * ws.element_size(), _status_ptr(status, dev))
     return dX, dL1, dL2
 
 

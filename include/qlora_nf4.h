@@ -414,7 +414,8 @@ QLORA_API int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_t
  * dT and s T enter the products of dL1 and dL2 unrounded (three bf16 terms
  * each, whose sum is the fp32 value).  drop names the forward's mask.  dX, dL1 or dL2 may be NULL to
  * skip that output (wt may then be NULL with dX, L1 and L2 must not).  Requires
- * K % 32 == 0, N % 32 == 0; r as in the forward; r = 0: dX alone.
+ * K % 32 == 0, N % 32 == 0; r as in the forward; r = 0: dX alone.  A non-finite
+ * dY sets *status_dev = QLORA_ERR_NONFINITE and gives NaN in its row of dX.
  */
 QLORA_API int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const float* T_saved,
                                   const qlora_mx_tensor* wt, int64_t N, int64_t K, const uint16_t* L1,
