@@ -319,12 +319,15 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
     for (int i = tid; i < nc * 64; i += C::THREADS) {
       const int c = c0 + (i >> 6), rp = (i & 63) * 2;
       if (!good || col0 + c >= args.cols || row0 + rp >= args.rows) continue;
-      float2 acc = ld_peer_f2(red + (uint32_t)(c * 128 + rp) * 4u, 0);
-      for (int p = 1; p < csize; ++p) {
-        const float2 v = ld_peer_f2(red + (uint32_t)(c * 128 + rp) * 4u, (uint32_t)p);
-        acc.x += v.x;
-        acc.y += v.y;
-      }
+      const uint32_t at = red + (uint32_t)(c * 128 + rp) * 4u;
+      float2 v[8];  // all loads in flight
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p < csize) v[p] = ld_peer_f2(at, (uint32_t)p);
+      float2 acc = v[0];
+#pragma unroll
+      for (int p = 1; p < 8; ++p)
+        if (p < csize) acc = make_float2(acc.x + v[p].x, acc.y + v[p].y);
       const int64_t o = (int64_t)(col0 + c) * args.ldo + row0 + rp;
       if (args.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(args.out) + o) = acc;
       else *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(args.out) + o) = pack_bf16x2(acc.x, acc.y);

@@ -49,12 +49,13 @@ template <bool WIDE>  // r > 64
 struct PrepCfg {
   static constexpr int S = WIDE ? 5 : 6;
   static constexpr int L = WIDE ? 16384 : 8192;  // tile of L: 64 columns x up to 128 / 64 ranks
-  static constexpr int STAGE = 16384 + L;
-  static constexpr int OUT = S * STAGE;          // two staging buffers: 16 KB of codes, 1 KB of scales
+  static constexpr int LT = S * 16384;   // the tiles of L, behind those of X
+  static constexpr int OUT = LT + S * L;  // two staging buffers: 16 KB of codes, 1 KB of scales
   static constexpr int OUTB = 16384 + 1024;
   static constexpr int BAR = OUT + 2 * OUTB;
   static constexpr int TOTAL = BAR + 512 + 1024;
-  static_assert(TOTAL <= 232448 && STAGE % 1024 == 0 && OUTB % 1024 == 0, "budget");
+  static_assert(TOTAL <= 232448 && OUTB % 1024 == 0, "budget");
+  static_assert(S * L >= 128 * ((WIDE ? 128 : 64) + 4) * 4, "a cluster's partial sums go over the tiles of L");
 };
 constexpr int kQGroups = 2;  // quantise groups of 8 warps (3 were a few percent slower)
 constexpr int kPrepThreads = (8 + 8 * kQGroups) * 32;
@@ -118,23 +119,24 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
   const int n_units = (int)(u_hi - u_lo);
   const bool drop = args.drop.threshold != 0;
 
-  if (tid == 0) {
-    for (int s = 0; s < kS; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(ready + s, 8);
-      mbar_init(empty + s, 9);
-    }
-    for (int b = 0; b < 2; ++b) {
+  if (warp == 0) {  // a barrier a lane
+    if (lane < kS) {
+      mbar_init(full + lane, 1);
+      mbar_init(ready + lane, 8);
+      mbar_init(empty + lane, 9);
+    } else if (lane < kS + 2) {
+      const int b = lane - kS;
       mbar_init(ofull + b, 32);
       mbar_init(oempty + b, 1);
       mbar_init(wfull + b, 1);
       mbar_init(wempty + b, 4);
+    } else if (lane == kS + 2) {
+      *abort_flag = 0;
+      tma_prefetch_desc(&args.tmX);
+      tma_prefetch_desc(&args.tmL);
+      tma_prefetch_desc(&args.tmCodes);
     }
-    *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&args.tmX);
-    tma_prefetch_desc(&args.tmL);
-    tma_prefetch_desc(&args.tmCodes);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -159,8 +161,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
         bool ok = true;
         for (int q = 0; q < 4; ++q) {
           if (!(ok = mbar_wait_backoff(empty + s, ph ^ 1u, abort_flag, args.status, 20))) break;
-          uint8_t* sx = smem + s * C::STAGE;
-          uint8_t* sl = sx + 16384;
+          uint8_t* sx = smem + s * 16384;
+          uint8_t* sl = smem + C::LT + s * C::L;
           const int c = c0 + 64 * q;
           mbar_arrive_expect_tx(full + s, 16384u + lbytes);
           tma_load_2d(sx, &args.tmX, full + s, c, row0);
@@ -195,11 +197,12 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
         if (!(ok = warp_poll<40>((drop ? ready : full) + s, ph, abort_flag, args.status, lane))) break;
         tc_fence_after();
         if (one) {
-          const uint8_t* sx = smem + s * C::STAGE;
+          const uint8_t* sx = smem + s * 16384;
+          const uint8_t* sl = smem + C::LT + s * C::L;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem + 128u * (uint32_t)b, operand_desc(sx, 0, kk), operand_desc(sx + 16384, args.l_mn, kk),
-                      idesc, (in_piece | kk) != 0);
+            umma_bf16(tmem + 128u * (uint32_t)b, operand_desc(sx, 0, kk), operand_desc(sl, args.l_mn, kk), idesc,
+                      (in_piece | kk) != 0);
           umma_commit(empty + s);
         }
         __syncwarp();
@@ -249,7 +252,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
       if (!warp_wait_backoff(wfull + b, (uint32_t)(piece >> 1) & 1u, abort_flag, args.status, lane, 100)) break;
       tc_fence_after();
       float* dst = nullptr;
-      if (last && !args.direct) {  // this run's rows of D: the slot of (row tile, ordinal of this CTA in it)
+      if (last && args.direct) {  // for the cluster, over the tiles of L: all of them have been multiplied
+        dst = reinterpret_cast<float*>(smem + C::LT) + (q4 * 32 + lane) * (args.r + 4);
+      } else if (last) {  // this run's rows of D: the slot of (row tile, ordinal of this CTA in it)
         const int64_t tile = (u_lo + u) / upt;
         const int ord = (int)blockIdx.x - prep_owner(args.units, (int)gridDim.x, tile * upt);
         dst = args.part + ((tile * args.maxc + ord) * 128 + q4 * 32 + lane) * args.r;
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
         } else {
           tmem_wait_ld();
         }
-        if (!last || args.direct) {
+        if (!last) {
           tmem_st16(tl + kSumCol + (uint32_t)c, v);
         } else {
 #pragma unroll
@@ -289,6 +294,14 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
     const int rl = t & 127, half = t >> 7;
     const PhiloxKey key = drop ? philox_key(args.drop) : PhiloxKey{0, 0, 0, 0};
     const uint32_t thr = args.drop.threshold << 16;
+    if (args.direct && args.fin.T_in) {  // while the first tiles are on their way
+      const int rows = 128 / csize, r4 = args.r / 4;
+      for (int i = tid - 256; i < rows * r4; i += kPrepThreads - 256) {
+        const int64_t row = tile0 * 128 + rank * rows + i / r4;
+        if (row < args.fin.M) emit_t4(args.fin, row, (i % r4) * 4);
+      }
+      __syncwarp();
+    }
     bool bad = false;
     int s = grp;  // ring stage of iteration `it` (grp < kS)
     uint32_t ph = 0;
@@ -313,7 +326,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
         for (int j = 0; j < 4; ++j) keep_here(rnd[j]);
       }
       if (!warp_poll<20>(full + s, ph, abort_flag, args.status, lane)) break;
-      uint8_t* sx = smem + s * C::STAGE + rl * 128;
+      uint8_t* sx = smem + s * 16384 + rl * 128;
       uint32_t c[4], b = 0;
       if (live) {
         uint32_t w[16];
@@ -380,43 +393,46 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
     __syncthreads();
   }
   if (args.direct) {
-    // The cluster holds its row tile's D: partial sums to shared memory (the
-    // ring is done with), added in rank order, 128 / csize rows a CTA.
+    // The cluster holds its row tile's D: the partial sums are added in rank
+    // order, 128 / csize rows a CTA.  Eight of a peer's loads are in flight at
+    // once, and the CTA tells its peers that it has read them before it stores.
     const int r = args.r, pitch = r + 4;
-    float* red = reinterpret_cast<float*>(smem);
-    if (warp >= 4 && warp < 8) {
-      tc_fence_after();
-      const int row = (warp & 3) * 32 + lane;
-      for (int c = 0; c < args.r16; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kSumCol + (uint32_t)c, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 16; j += 4)
-          if (c + j < r)
-            *reinterpret_cast<uint4*>(red + row * pitch + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-      }
-      tc_fence_before();
-    }
-    __syncwarp();
+    const float* red = reinterpret_cast<const float*>(smem + C::LT);
     cluster_sync_all();
     const MxPrepFinish& f = args.fin;
-    const int rows = 128 / csize, r4 = r / 4;
+    const int rows = 128 / csize, r4 = r / 4, n = rows * r4;
     const bool good = !*abort_flag;
-    for (int i = tid; i < rows * r4; i += kPrepThreads) {
+    for (int i0 = 0; i0 < n; i0 += kPrepThreads) {
+      const int i = i0 + tid;
       const int lr = rank * rows + i / r4, j = (i % r4) * 4;
       const int64_t row = tile0 * 128 + lr;
-      if (!good || row >= f.M) continue;
-      const uint32_t at = smem_u32(red + lr * pitch + j);
-      float4 d = ld_peer_f4(at, 0);
-      for (int c = 1; c < csize; ++c) {
-        const float4 q = ld_peer_f4(at, (uint32_t)c);
-        d = make_float4(__fadd_rn(d.x, q.x), __fadd_rn(d.y, q.y), __fadd_rn(d.z, q.z), __fadd_rn(d.w, q.w));
+      const bool mine = good && i < n && row < f.M;
+      float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mine) {
+        const uint32_t at = smem_u32(red + lr * pitch + j);
+        d = ld_peer_f4(at, 0);
+        int c = 1;
+        for (; c + 7 <= csize; c += 7) {
+          float4 q[7];
+#pragma unroll
+          for (int k = 0; k < 7; ++k) q[k] = ld_peer_f4(at, (uint32_t)(c + k));
+#pragma unroll
+          for (int k = 0; k < 7; ++k)
+            d = make_float4(__fadd_rn(d.x, q[k].x), __fadd_rn(d.y, q[k].y), __fadd_rn(d.z, q[k].z),
+                            __fadd_rn(d.w, q[k].w));
+        }
+        for (; c < csize; ++c) {
+          const float4 q = ld_peer_f4(at, (uint32_t)c);
+          d = make_float4(__fadd_rn(d.x, q.x), __fadd_rn(d.y, q.y), __fadd_rn(d.z, q.z), __fadd_rn(d.w, q.w));
+        }
       }
-      emit4(f, row, j, d);
-      if (f.T_in) emit_t4(f, row, j);
+      reads_done(d);
+      __syncwarp();
+      if (i0 + kPrepThreads >= n) cluster_arrive_read();  // the last rows are read
+      if (mine) emit4(f, row, j, d);
     }
-    cluster_sync_all();  // peers may still be reading this CTA's rows
+    __syncwarp();
+    cluster_wait();  // peers may still be reading this CTA's rows
   }
   if (warp == 1) {
     tc_fence_after();

@@ -6,6 +6,13 @@
 namespace qnf4 {
 namespace {
 
+// Cluster barrier in two halves, by converged warps, where only reads of the
+// peers come before: the values must be there (reads_done), but nothing has
+// to be made visible, which costs a release some 1000 cycles.
+QDEV void reads_done(float4 v) { asm volatile("" ::"f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory"); }
+QDEV void cluster_arrive_read() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+QDEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 constexpr int kMxKB = 256;  // reduction elements of a stage: 128 bytes of codes
 
 // Instruction descriptor, kind::mxf4: E2M1 x E2M1, E8M0 scales; the scale ids
