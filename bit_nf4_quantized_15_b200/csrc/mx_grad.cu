@@ -7,14 +7,13 @@
 // over the tokens and reads all of X or dY: the bound is those bytes, with
 // the terms' 6 r bytes a token read again (from L2) for every 128 columns.
 //
-// A unit is 128 columns of X or dY x 512 tokens (256 for small problems with
-// dropout): one accumulation in tensor memory (the tensor cores' truncation
-// grows with the length of a sum, see mx_prep.cu), three groups of r columns
-// wide; the sum warps add the groups, and units of one run to one another,
-// with rounding.  One CTA per SM takes a run of units of equal cost; both
-// gradients are one launch, so that a small one fills the other's tail.  A
-// tile that is one unit is written at once; other runs end in partial slots
-// that a second kernel adds in order.
+// A unit is 128 columns of X or dY x up to 512 tokens: one accumulation in
+// tensor memory (the tensor cores' truncation grows with the length of a sum,
+// see mx_prep.cu), three groups of r columns wide; the sum warps add the
+// groups, and units of one run to one another, with rounding.  One CTA per SM
+// takes a run of units of equal cost; both gradients are one launch, so that a
+// small one fills the other's tail.  A tile that is one unit is written at
+// once; other runs end in partial slots that a second kernel adds in order.
 //
 // With dropout the X tile is masked in shared memory before the MMAs read it.
 //
@@ -31,6 +30,8 @@
 #include "mx_util.cuh"
 #include "pair_util.cuh"
 #include "philox.cuh"
+
+#include <algorithm>
 
 namespace qnf4 {
 namespace {
@@ -87,17 +88,25 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
   const int nbuf = args.nbuf;
   const uint32_t sum_col = (uint32_t)(nbuf * args.n16);
 
-  if (tid == 0) {
-    for (int s = 0; s < kS; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(ready + s, 8);
-      mbar_init(empty + s, 1);
+  if (warp == 0) {  // a barrier a lane
+    if (lane < kS) {
+      mbar_init(full + lane, 1);
+      mbar_init(ready + lane, 8);
+      mbar_init(empty + lane, 1);
+    } else if (lane < kS + 2) {
+      mbar_init(wfull + lane - kS, 1);
+      mbar_init(wempty + lane - kS, 4);
+    } else if (lane == kS + 2) {
+      *abort_flag = 0;
+      if (args.sh.units0) {
+        tma_prefetch_desc(&args.p[0].tmZ);
+        tma_prefetch_desc(&args.p[0].tmV);
+      }
+      if (args.sh.units > args.sh.units0) {
+        tma_prefetch_desc(&args.p[1].tmZ);
+        tma_prefetch_desc(&args.p[1].tmV);
+      }
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(wfull + b, 1);
-      mbar_init(wempty + b, 4);
-    }
-    *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -191,11 +200,15 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
       if (!warp_wait_backoff(wfull + b, wph, abort_flag, args.status, lane, 100)) break;
       tc_fence_after();
       const MxGradProblem& p = args.p[x.prob];
+      float* const out = p.out;
+      const int64_t cols = p.cols;
+      const bool transposed = p.transposed, whole = args.pieces == 1;
       // this run's slot of the tile: its ordinal among the CTAs that share it
       const int64_t tile_u = (x.prob ? args.sh.units0 : 0) + (int64_t)x.tile * args.pieces;
       const int ord = (int)blockIdx.x - grad_owner(args.sh, tile_u);
       float* slot = p.part + ((int64_t)x.tile * args.maxc + ord) * 128 * r;
       const int row = q4 * 32 + lane;
+      const int64_t col = (int64_t)x.tile * 128 + row;
       for (int c = 0; c < r16; c += 16) {
         uint32_t v[16], w[16], z[16];
         const uint32_t at = tl + (uint32_t)(b * args.n16 + c);
@@ -213,22 +226,22 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(w[j])));
         }
-        const int64_t col = (int64_t)x.tile * 128 + row;
         if (!x.last) {
           tmem_st16(tl + sum_col + (uint32_t)c, v);
-        } else if (args.pieces == 1) {  // this CTA has the whole sum
-          if (col >= p.cols) continue;
-          if (p.transposed) {
+        } else if (whole) {  // this CTA has the whole sum
+          if (col >= cols) continue;
+          if (transposed) {
+            float* at = out + c * cols + col;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < r) p.out[(c + j) * p.cols + col] = __uint_as_float(v[j]);
+            for (int j = 0; j < 16; ++j, at += cols)
+              if (c + j < r) *at = __uint_as_float(v[j]);
           } else {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
               if (c + j < r)
-                *reinterpret_cast<uint4*>(p.out + col * r + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                *reinterpret_cast<uint4*>(out + col * r + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           }
-        } else if (p.transposed) {  // slot [r][128]
+        } else if (transposed) {  // slot [r][128]
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (c + j < r) slot[(c + j) * 128 + row] = __uint_as_float(v[j]);
@@ -344,16 +357,22 @@ __global__ void __launch_bounds__(256) mx_grad_finish_kernel(const __grid_consta
 MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool drop, int num_sms) {
   MxGradPlan p{};
   const int64_t t0 = (cols0 + 127) / 128, t1 = (cols1 + 127) / 128;
-  // The masked stages of a unit follow one another at 1.2 us; units of half the
-  // length are worth their second kernel while there is no unit for every SM
-  // (gradients of 512 x 512 x 512, r = 64: 21 us with dropout against 27, but
-  // without 16.3 and 17.8, and for 400 x 4096 x 4096 21.6 against 18.5).
-  p.piece = drop && (t0 + t1) * ((M + 64 * kGPiece - 1) / (64 * kGPiece)) < num_sms ? kGPiece / 2 : kGPiece;
-  p.pieces = (int)((M + 64 * p.piece - 1) / (64 * p.piece));
+  if (!t0 && !t1) return p;
+  const bool masked = drop && t0;
+  // As few pieces of the tokens as their greatest length allows, cut evenly.  The
+  // masked stages of a unit follow one another at 1.2 us, so with dropout pieces
+  // of about half that length are worth their second kernel and balance the
+  // CTAs while those do not have a longer unit each (gradients of 512 x 512 x
+  // 512, r = 64: 21 us in two pieces, 27 in one, but without dropout 17.8 and
+  // 16.3; backward of 1024 x 4096 x 4096: 44 us in four, 49 in two).
+  const int64_t stages = (M + 63) / 64;
+  int64_t n = (stages + kGPiece - 1) / kGPiece;
+  if (masked && (t0 + t1) * n < num_sms) n = std::max(n, (stages + kGPiece / 4) / (kGPiece / 2));
+  p.piece = (int)((stages + n - 1) / n);
+  p.pieces = (int)((stages + p.piece - 1) / p.piece);
   p.sh.units0 = t0 * p.pieces;
   p.sh.units = p.sh.units0 + t1 * p.pieces;
-  p.sh.w0 = drop && t0 ? 3 : 2;
-  if (!p.sh.units) return p;
+  p.sh.w0 = masked ? 3 : 2;
   // no more CTAs than leave each the cost of a unit, so that none is empty
   // (the slots of a tile's CTAs are then all written)
   const int64_t cost = grad_cost(p.sh, p.sh.units), fit = cost / p.sh.w0;
