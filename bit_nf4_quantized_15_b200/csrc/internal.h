@@ -248,7 +248,7 @@ cudaError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t c
                                int* status, cudaStream_t st);
 // X [R][C] -> the MXFP4 form of its transpose [C][R].
 cudaError_t launch_mx_quantize_t(const void* X, int dtype, int64_t R, int64_t C, uint8_t* codes, uint8_t* scales,
-                                 int* status, cudaStream_t st);
+                                 int* status, int sms, cudaStream_t st);
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int dtype,
                               void* out, cudaStream_t st);
 cudaError_t launch_dropout(const void* X, int dtype, int64_t n, const DropArgs& d, void* out, cudaStream_t st);

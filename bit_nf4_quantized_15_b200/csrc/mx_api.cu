@@ -222,7 +222,7 @@ int qlora_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int 
   if (int rc = current_device_info(&di)) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = transpose
-                            ? launch_mx_quantize_t(X, dtype, rows, cols, out->codes, out->scales, status_dev, st)
+                            ? launch_mx_quantize_t(X, dtype, rows, cols, out->codes, out->scales, status_dev, di.sms, st)
                             : launch_mx_quantize(X, dtype, rows, cols, out->codes, out->scales, status_dev, st);
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }

@@ -15,7 +15,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 
-#include "common.cuh"
+#include "engine_util.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "mx_codec.cuh"
@@ -135,75 +135,114 @@ __global__ void __launch_bounds__(kQT) mx_quantize_kernel(const void* __restrict
   if (t < 32) reinterpret_cast<uint4*>(scales)[(int64_t)blockIdx.x * 32 + t] = reinterpret_cast<const uint4*>(s_sc)[t];
 }
 
-// Transposed: X [R][C], output [C][R] with blocks along R.  A CTA takes 128 r
-// x 64 c, half the rows of an output scale tile: the piece goes through
-// shared memory as stored, a lane 16 bytes of a row (rows padded by 16 bytes:
-// neither the row writes nor the column reads conflict); a thread then owns a
-// 32-block of one c.  The codes meet in shared memory too and leave as 64
-// bytes a row of the output.  (128 c a CTA left room for three CTAs an SM and
-// took longer: 45 against 41 us for 11008 x 4096 fp32, 204 MB.)
+// Transposed: X [R][C], output [C][R] with blocks along R.  A tile is 128 r x
+// 64 c, half the rows of an output scale tile.  It comes by TMA as it is
+// stored, into a ring (the next tiles travel while this one is worked on); a
+// thread owns a 32-block of one c, and a warp's reads of a row are consecutive
+// words, so the tile needs neither padding nor a swizzle.  The codes meet in
+// shared memory too and leave as 64 bytes a row of the output.
+//
+// Bound by HBM: 11008 x 4096 fp32, 204 MB, 34.4 us (5.9 TB/s); 8192 x 8192 bf16,
+// 170 MB, 30 us (5.6).  With loads to registers and a CTA a tile it was 41 and
+// 35; with two CTAs an SM and longer rings 34.9 and 32.8, with one or two 35.6
+// of fp32, with four CTAs 30.9 of bf16.
 template <int DT>
-__global__ void __launch_bounds__(kQT) mx_quantize_t_kernel(const void* __restrict__ X, int64_t R, int64_t C,
-                                                            uint8_t* __restrict__ codes,
-                                                            uint8_t* __restrict__ scales, int kt, int* status) {
-  constexpr int kE = DT == QLORA_DTYPE_F32 ? 4 : 2;      // bytes an element
-  constexpr int kPitch = 64 * kE + 16, kLanes = 4 * kE;  // bytes of a row; lanes that share one
-  constexpr int kStep = kQT / kLanes, kLoads = 128 / kStep;
-  __shared__ __align__(16) uint8_t s_x[128 * kPitch];
-  __shared__ __align__(16) uint4 s_c[64][5];             // codes, 64 bytes a row, padded
-  __shared__ __align__(8) uint8_t s_sc[256];             // scales: 32 x (2 groups of 32 rows) x 4 blocks
-  const int t = threadIdx.x;
+struct QtCfg {
+  static constexpr int E = DT == QLORA_DTYPE_F32 ? 4 : 2;  // bytes an element
+  static constexpr int TILE = 128 * 64 * E;
+  static constexpr int S = E == 4 ? 2 : 3;      // stages
+  static constexpr int CTAS = 3;                // that share an SM
+  static constexpr int CODES = S * TILE;        // two buffers of 64 rows of 4 x 16 bytes, padded
+  static constexpr int SC = CODES + 2 * 64 * 80;  // two of 256: 32 x (2 groups of 32 rows) x 4 blocks
+  static constexpr int BAR = SC + 2 * 256;
+  static constexpr int TOTAL = BAR + 64 + 128;
+  static_assert(CTAS * (TOTAL + 1024) <= 228 * 1024, "budget");
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kQT, QtCfg<DT>::CTAS)
+    mx_quantize_t_kernel(const __grid_constant__ CUtensorMap tm, int64_t R, int64_t C, uint8_t* __restrict__ codes,
+                         uint8_t* __restrict__ scales, int kt, int* status) {
+  using G = QtCfg<DT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::BAR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(full + G::S);
+  const int t = threadIdx.x, lane = t & 31;
   // consecutive CTAs walk along C, so that their row pieces share DRAM pages
-  const unsigned n_ct = (unsigned)((C + 63) / 64);
-  const unsigned ct = blockIdx.x % n_ct, rt = blockIdx.x / n_ct;  // 64 output rows, output scale-tile column
-  const int64_t r0 = (int64_t)rt * 128, c0 = (int64_t)ct * 64;
-  const int nr = (int)(R - r0 < 128 ? R - r0 : 128), nc = (int)(C - c0 < 64 ? C - c0 : 64);
-  {
-    const int ch = t % kLanes, rl = t / kLanes;  // 16-byte piece of the row, first row
-    const uint4* p = reinterpret_cast<const uint4*>(X) + ((r0 + rl) * C + c0) / (16 / kE) + ch;
-    const int64_t step = kStep * (C / (16 / kE));
-    const int n = ch * (16 / kE) < nc ? nr : 0;
-    uint4 v[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) v[i] = rl + kStep * i < n ? __ldg(p + i * step) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) *reinterpret_cast<uint4*>(s_x + (rl + kStep * i) * kPitch + ch * 16) = v[i];
+  const unsigned n_ct = (unsigned)((C + 63) / 64), tiles = n_ct * (unsigned)kt;
+  auto load = [&](unsigned tile, int s) {
+    mbar_arrive_expect_tx(full + s, (uint32_t)G::TILE);  // zeros outside the matrix
+    tma_load_2d(smem + s * G::TILE, &tm, full + s, (int)(tile % n_ct) * 64, (int)(tile / n_ct) * 128);
+  };
+  if (t == 0) {
+    for (int s = 0; s < G::S; ++s) mbar_init(full + s, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    unsigned tile = blockIdx.x;
+    for (int s = 0; s < G::S && tile < tiles; ++s, tile += gridDim.x) load(tile, s);
   }
   __syncthreads();
+
   const int cl = t & 63, blk = t >> 6;
-  float v[32];
-  uint32_t m = 0;
+  bool bad = false;
+  int s = 0, o = 0;  // stage, output buffer
+  uint32_t ph = 0;
+  for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x, o ^= 1) {
+    const unsigned ct = tile % n_ct, rt = tile / n_ct;  // 64 output rows, output scale-tile column
+    const int64_t r0 = (int64_t)rt * 128, c0 = (int64_t)ct * 64;
+    const int nr = (int)(R - r0 < 128 ? R - r0 : 128), nc = (int)(C - c0 < 64 ? C - c0 : 64);
+    uint4(*s_c)[5] = reinterpret_cast<uint4(*)[5]>(smem + G::CODES + o * 64 * 80);
+    uint8_t* s_sc = smem + G::SC + o * 256;
+    const bool ok = warp_wait(full + s, ph, abort_flag, status, lane);
+    if (ok) {
+      const uint8_t* x = smem + s * G::TILE + blk * 32 * 64 * G::E;
+      float v[32];
+      uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    v[j] = load1<DT>(s_x + (blk * 32 + j) * kPitch, cl);
-    m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  }
-  const uint32_t b = mx_scale_byte(m);  // 0 outside the matrix
-  const float f = mx_inv_scale(b);
-  uint32_t w[4];
+      for (int j = 0; j < 32; ++j) {
+        v[j] = load1<DT>(x + j * 64 * G::E, cl);
+        m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+      }
+      const uint32_t b = mx_scale_byte(m);  // 0 outside the matrix
+      const float f = mx_inv_scale(b);
+      uint32_t w[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float2 u[4];
+      for (int q = 0; q < 4; ++q) {
+        float2 u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      u[j] = __fmul2_rn(make_float2(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]), make_float2(f, f));
-    w[q] = mx_codes8(u);
+        for (int j = 0; j < 4; ++j)
+          u[j] = __fmul2_rn(make_float2(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]), make_float2(f, f));
+        w[q] = mx_codes8(u);
+      }
+      s_c[cl][blk] = make_uint4(w[0], w[1], w[2], w[3]);
+      s_sc[(cl & 31) * 8 + (cl >> 5) * 4 + blk] = (uint8_t)b;
+      bad |= b == 255u;
+    }
+    // The stage has been read and the codes are in place.  (Those of the tile
+    // before last, in the same buffer, were read before the last barrier.)
+    if (__syncthreads_or(!ok)) break;
+    if (t == 0 && (uint64_t)tile + (uint64_t)G::S * gridDim.x < tiles) load(tile + G::S * gridDim.x, s);
+    {
+      const int row = t >> 2, q = t & 3;  // 4 lanes a row of codes
+      if (row < nc && q * 32 < nr) reinterpret_cast<uint4*>(codes)[((c0 + row) * R + r0) / 32 + q] = s_c[row][q];
+    }
+    // this tile's half of the scale tile: 8 of every 16 bytes
+    uint8_t* sc = scales + ((int64_t)(ct >> 1) * kt + rt) * 512 + t * 16 + (ct & 1) * 8;
+    if (t < 32) *reinterpret_cast<uint2*>(sc) = *reinterpret_cast<const uint2*>(s_sc + t * 8);
+    // the last half tile of rows has no tile of its own: its padding is zero too
+    if (t < 32 && ct + 1 == n_ct && (ct & 1) == 0) *reinterpret_cast<uint2*>(sc + 8) = make_uint2(0u, 0u);
+    if (++s == G::S) {
+      s = 0;
+      ph ^= 1u;
+    }
   }
-  s_c[cl][blk] = make_uint4(w[0], w[1], w[2], w[3]);
-  s_sc[(cl & 31) * 8 + (cl >> 5) * 4 + blk] = (uint8_t)b;
-  if (b == 255u) report(status, QLORA_ERR_NONFINITE);
-  __syncthreads();
-  {
-    const int row = t >> 2, q = t & 3;  // 4 lanes a row of codes
-    if (row < nc && q * 32 < nr) reinterpret_cast<uint4*>(codes)[((c0 + row) * R + r0) / 32 + q] = s_c[row][q];
+  if (bad) report(status, QLORA_ERR_NONFINITE);
+  if (*abort_flag && t == 0) {  // error path: let the loads in flight finish
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000ull) {
+    }
   }
-  // this CTA's half of the scale tile: 8 of every 16 bytes
-  if (t < 32)
-    *reinterpret_cast<uint2*>(scales + ((int64_t)(ct >> 1) * kt + rt) * 512 + t * 16 + (ct & 1) * 8) =
-        *reinterpret_cast<const uint2*>(s_sc + t * 8);
-  // the last half tile of rows has no CTA of its own: its padding is zero too
-  if (t < 32 && ct + 1 == n_ct && (ct & 1) == 0)
-    *reinterpret_cast<uint2*>(scales + ((int64_t)(ct >> 1) * kt + rt) * 512 + t * 16 + 8) = make_uint2(0u, 0u);
 }
 
 // Value of a code times 2^(b - 127).  The E2M1 value is exact in fp16 and the
@@ -335,20 +374,24 @@ cudaError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t c
 
 template <int DT>
 static cudaError_t quantize_t(const void* X, int64_t R, int64_t C, uint8_t* codes, uint8_t* scales, int* status,
-                              cudaStream_t st) {
+                              int sms, cudaStream_t st) {
+  using G = QtCfg<DT>;
+  CUtensorMap tm;
+  if (make_map(&tm, X, G::E == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, G::E, (uint64_t)C,
+               (uint64_t)R, 64, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
   const int kt = (int)((R + 127) / 128);
-  const unsigned grid = (unsigned)(((C + 63) / 64) * kt);
-  mx_quantize_t_kernel<DT><<<grid, kQT, 0, st>>>(X, R, C, codes, scales, kt, status);
-  count_launches(1);
-  return cudaGetLastError();
+  const int64_t tiles = (C + 63) / 64 * kt, most = (int64_t)sms * G::CTAS;
+  return launch_kernel<mx_quantize_t_kernel<DT>>(
+      {dim3((unsigned)(tiles < most ? tiles : most)), kQT, G::TOTAL, 1, false}, st, tm, R, C, codes, scales, kt, status);
 }
 
 cudaError_t launch_mx_quantize_t(const void* X, int dtype, int64_t R, int64_t C, uint8_t* codes, uint8_t* scales,
-                                 int* status, cudaStream_t st) {
+                                 int* status, int sms, cudaStream_t st) {
   switch (dtype) {
-    case QLORA_DTYPE_BF16: return quantize_t<QLORA_DTYPE_BF16>(X, R, C, codes, scales, status, st);
-    case QLORA_DTYPE_F16: return quantize_t<QLORA_DTYPE_F16>(X, R, C, codes, scales, status, st);
-    default: return quantize_t<QLORA_DTYPE_F32>(X, R, C, codes, scales, status, st);
+    case QLORA_DTYPE_BF16: return quantize_t<QLORA_DTYPE_BF16>(X, R, C, codes, scales, status, sms, st);
+    case QLORA_DTYPE_F16: return quantize_t<QLORA_DTYPE_F16>(X, R, C, codes, scales, status, sms, st);
+    default: return quantize_t<QLORA_DTYPE_F32>(X, R, C, codes, scales, status, sms, st);
   }
 }
 
