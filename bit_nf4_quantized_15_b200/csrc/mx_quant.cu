@@ -304,40 +304,64 @@ QDEV void store1(void* out, int64_t i, float v) {
   else reinterpret_cast<__half*>(out)[i] = __float2half_rn(v);
 }
 
-// out = x inv where kept, else 0 (a selection: a dropped Inf or NaN is 0).
-// Eight elements (one generator evaluation) a thread and step.  Bound by HBM:
-// 8192 x 8192 bf16, 268 MB, 50 us (5.4 TB/s), with the integer pipes 60 % busy.
+// Eight elements as stored: dropped ones to zero (a selection: a dropped Inf
+// or NaN is 0), the others times inv.
+template <int DT>
+QDEV void drop_store8(void* out, int64_t i, uint32_t* w, const uint4& rnd, const DropArgs& d) {
+  const uint32_t thr = d.threshold << 16;
+  if constexpr (DT == QLORA_DTYPE_F32) {
+    const uint32_t ws[4] = {rnd.x, rnd.y, rnd.z, rnd.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if ((ws[j] << 16) < thr) w[2 * j] = 0u;
+      if (ws[j] < thr) w[2 * j + 1] = 0u;
+    }
+  } else {
+    drop8_bf16(w, rnd, thr);  // two 16-bit elements a word, of either kind
+  }
+  float2 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = pair_of<DT>(w, j);
+    v[j] = make_float2(__fmul_rn(v[j].x, d.inv), __fmul_rn(v[j].y, d.inv));
+  }
+  if constexpr (DT == QLORA_DTYPE_F32) {
+    reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  } else {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == QLORA_DTYPE_BF16) {
+        o[j] = pack_bf16x2(v[j].x, v[j].y);
+      } else {
+        const __half2 h = __floats2half2_rn(v[j].x, v[j].y);
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    reinterpret_cast<uint4*>(out)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// out = x inv where kept, else 0.  Eight elements (one generator evaluation) a
+// thread and turn; a step has two turns with their loads in flight.  Bound by
+// HBM: 8192 x 8192 bf16, 268 MB, 46 us (5.8 TB/s), fp32 87 us (6.2 TB/s; with
+// one turn 93); a copy of the bf16 tensor takes 42.
 template <int DT>
 __global__ void __launch_bounds__(kQT) dropout_kernel(const void* __restrict__ X, int64_t n, DropArgs d,
                                                       void* __restrict__ out) {
+  constexpr int kTurns = 2;
   const PhiloxKey key = philox_key(d);
   const int64_t n8 = n / 8, stride = (int64_t)gridDim.x * kQT;
-  for (int64_t i = (int64_t)blockIdx.x * kQT + threadIdx.x; i < n8; i += stride) {
-    uint32_t w[kWords<DT>];
-    load8<DT>(reinterpret_cast<const uint4*>(X) + i * (kWords<DT> / 4), w);
-    float v[8];
+  for (int64_t i = (int64_t)blockIdx.x * kQT + threadIdx.x; i < n8; i += kTurns * stride) {
+    uint32_t w[kTurns][kWords<DT>];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = pair_of<DT>(w, j);
-      v[2 * j] = f.x, v[2 * j + 1] = f.y;
-    }
-    const uint32_t keep = keep8((uint64_t)i, key, d.threshold);
+    for (int k = 0; k < kTurns; ++k)
+      if (i + k * stride < n8) load8<DT>(reinterpret_cast<const uint4*>(X) + (i + k * stride) * (kWords<DT> / 4), w[k]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (keep >> j) & 1u ? __fmul_rn(v[j], d.inv) : 0.0f;
-    if constexpr (DT == QLORA_DTYPE_F32) {
-      reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if constexpr (DT == QLORA_DTYPE_BF16) {
-      reinterpret_cast<uint4*>(out)[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      reinterpret_cast<uint4*>(out)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    for (int k = 0; k < kTurns; ++k)
+      if (i + k * stride < n8)
+        drop_store8<DT>(out, i + k * stride, w[k], philox4x32_10((uint64_t)(i + k * stride), key), d);
   }
   const int64_t tail = n8 * 8;
   if (blockIdx.x == 0 && threadIdx.x < n - tail) {
