@@ -268,33 +268,33 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
     // Units of dL1 come first in a run, so every stage up to the last masked
     // one is masked and the ready barriers' phases follow the ring's.
     const PhiloxKey key = philox_key(args.drop);
-    const int grp = (warp - 8) >> 3, t = tid & 255;  // two groups of 8 warps, alternate stages
+    // two groups of 8 warps take alternate stages; a thread has 8 columns of
+    // tokens tok and tok + 32, in both boxes
+    const int grp = (warp - 8) >> 3, tok = (tid & 255) >> 3, ch = tid & 7;
+    const int64_t c8 = args.p[0].cols >> 3;
+    const uint32_t off = (uint32_t)(tok * 128 + ((ch ^ (tok & 7)) << 4)), thr = args.drop.threshold << 16;
     int s = 0, turn = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int64_t u = u_lo; u < u_hi && u < args.sh.units0 && ok; ++u) {
       const UnitAt x = unit_at(args, u, u_hi);
       const int t0 = x.piece * 64 * args.piece, n = min(args.piece, (args.M - t0 + 63) / 64);
-      for (int i = 0; i < n; ++i, turn ^= 1) {
+      uint64_t ctr = (uint64_t)((t0 + tok) * c8 + x.tile * 16 + ch);
+      for (int i = 0; i < n; ++i, turn ^= 1, ctr += 64 * c8) {
         if (turn == grp) {
           // this thread's evaluations before the wait: they need no data
           uint4 rnd[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int q = t + 256 * j, tok = (q >> 3) & 63, ch = q & 7, box = q >> 9;
-            const int64_t e = (int64_t)(t0 + 64 * i + tok) * args.p[0].cols + x.tile * 128 + 64 * box + 8 * ch;
-            rnd[j] = philox4x32_10((uint64_t)e >> 3, key);
-          }
+          for (int j = 0; j < 4; ++j) rnd[j] = philox4x32_10(ctr + (j & 1) * 32 * c8 + (j >> 1) * 8, key);
 #pragma unroll
           for (int j = 0; j < 4; ++j) keep_here(rnd[j]);
           if (!(ok = warp_poll<20>(full + s, ph, abort_flag, args.status, lane))) break;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int q = t + 256 * j, tok = (q >> 3) & 63, ch = q & 7, box = q >> 9;
-            uint4* at = reinterpret_cast<uint4*>(smem + s * stage + 8192 * box + tok * 128 + ((ch ^ (tok & 7)) << 4));
+            uint4* at = reinterpret_cast<uint4*>(smem + s * stage + off + 4096 * (j & 1) + 8192 * (j >> 1));
             const uint4 v = *at;
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            drop8_bf16(w, rnd[j], args.drop.threshold << 16);
+            drop8_bf16(w, rnd[j], thr);
             *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
           fence_proxy_async_smem();
