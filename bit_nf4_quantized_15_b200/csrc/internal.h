@@ -307,6 +307,7 @@ struct MxPairArgs {
   int64_t ldo;
   int out_f32;
   DropArgs drop;     // mask of the LoRA term at element row * ldo + col
+  uint4* keep;       // if set: its bits, [rows][128-column tiles of ldo], 16 bytes each
   int* status;
 };
 size_t mx_pair_smem_bytes();
@@ -384,6 +385,7 @@ struct MxGradArgs {
   int n16, nbuf;       // columns of an accumulator (3r up to 16), accumulators
   int vboxes, stages;
   DropArgs drop;       // mask of X
+  const uint8_t* keep; // its bits as the product of dX left them, or null: evaluated
   int* status;
 };
 MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool drop, int num_sms);

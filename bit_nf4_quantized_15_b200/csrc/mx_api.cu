@@ -66,7 +66,8 @@ int map_scales(CUtensorMap* m, const uint8_t* scales, int64_t rows, int64_t K, i
 }
 
 // out [M][N] = x w^T (+ the LoRA term), x = (xc, xs) the tokens, w = (wc, ws)
-// the features.
+// the features.  *keep, if given: where the mask's bits may be left; null after
+// the call if they were not.
 //
 // CTA pairs when more than a quarter of the SMs would have one of their 256 x
 // 256 tiles, else tiles of 128 features split over clusters.  Both measured:
@@ -74,8 +75,8 @@ int map_scales(CUtensorMap* m, const uint8_t* scales, int64_t rows, int64_t K, i
 // 11008 x 4096 (43) 15.6 and 16.2; 512 x 4096 x 4096 (32) 13.5 and 12.2; but
 // 128 x 22016 x 8192 (86, half of each empty) 36.8 and 34.3.
 int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, const uint8_t* ws, int64_t N,
-            int64_t K, const LoraTerm* lora, const DropArgs& drop, void* out, int out_f32, int* status, int sms,
-            bool dependent, cudaStream_t st) {
+            int64_t K, const LoraTerm* lora, const DropArgs& drop, uint8_t** keep, void* out, int out_f32, int* status,
+            int sms, bool dependent, cudaStream_t st) {
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t stall_ns = take_stall_request();
@@ -93,6 +94,7 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
       g.kb_ext = (lora->r + 63) / 64;
       g.b_mn_ext = lora->v_mn;
       g.drop = drop;
+      if (keep && drop.threshold) g.keep = reinterpret_cast<uint4*>(*keep);
     }
     g.rows = (int)M;
     g.cols = (int)N;
@@ -104,6 +106,7 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
     g.status = status;
     return launch_mx_gemm_pair(g, sms, dependent, st) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
   }
+  if (keep) *keep = nullptr;
   const MxGemmPlan p = plan_mx_gemm(N, M, K, sms);
   MxGemmArgs g;
   std::memset(&g, 0, sizeof(g));
@@ -163,9 +166,11 @@ int prep(const uint16_t* X, int64_t M, int64_t C, const uint16_t* L, int l_mn, i
 //   q      MXFP4 of X (forward) or dY (backward): codes, then scales
 //   u, v   bf16 [M][3r]: the scaled dT (u) and s T (v) in three terms, the
 //          first RNbf16; the forward keeps RNbf16(s T) in u
+//   keep   bits of the dropout mask, [M][128-column tiles of K], 16 bytes each,
+//          from the product of dX to the kernel of dL1
 //   part   fp32 partial sums of the adapter products
 struct MxWs {
-  size_t q_scales, u, v, part, total;
+  size_t q_scales, u, v, keep, part, total;
   MxPrepPlan prep_x, prep_dy;
 };
 
@@ -180,6 +185,8 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms) {
     o += up256((size_t)M * r * 6);
     w.v = o;
     o += up256((size_t)M * r * 6);
+    w.keep = o;
+    o += up256((size_t)M * ((K + 127) / 128) * 16);
     w.part = o;
     w.prep_x = plan_mx_prep(M, K, r, sms);
     w.prep_dy = plan_mx_prep(M, N, r, sms);
@@ -247,7 +254,7 @@ int qlora_mx_matmul(const qlora_mx_tensor* a, const qlora_mx_tensor* b, void* ou
   if (!all16({a->codes, a->scales, b->codes, b->scales, out})) return QLORA_ERR_ALIGN;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  return product(a->codes, a->scales, a->rows, b->codes, b->scales, b->rows, a->cols, nullptr, DropArgs{}, out,
+  return product(a->codes, a->scales, a->rows, b->codes, b->scales, b->rows, a->cols, nullptr, DropArgs{}, nullptr, out,
                  dtype == QLORA_DTYPE_F32, status_dev, di.sms, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -307,7 +314,7 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
     return QLORA_ERR_CUDA;
   }
   const LoraTerm lora{sT, 0, L2, 1, r};
-  return product(wb, wb + lay.q_scales, M, w->codes, w->scales, N, K, r ? &lora : nullptr, DropArgs{}, Y, 0,
+  return product(wb, wb + lay.q_scales, M, w->codes, w->scales, N, K, r ? &lora : nullptr, DropArgs{}, nullptr, Y, 0,
                  status_dev, di.sms, true, st);
 }
 
@@ -354,15 +361,17 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
              launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
     return QLORA_ERR_CUDA;
   }
+  // the mask's bits, if dX's product leaves them for dL1
+  uint8_t* keep = dX && dL1 && d.threshold ? wb + lay.keep : nullptr;
   if (dX) {
     const LoraTerm lora{sdT, (uint64_t)r * 6, L1, 0, r};
-    if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d, dX, 0,
+    if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d, keep ? &keep : nullptr, dX, 0,
                          status_dev, di.sms, true, st))
       return rc;
   }
   if (dL1 || dL2) {
     if (dL2 && !dX && !dL1 && launch_split3(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
-    const MxGradPlan p = plan_mx_grad(M, dL1 ? K : 0, dL2 ? N : 0, r, d.threshold != 0, di.sms);
+    const MxGradPlan p = plan_mx_grad(M, dL1 ? K : 0, dL2 ? N : 0, r, d.threshold && !keep, di.sms);
     MxGradArgs a;
     std::memset(&a, 0, sizeof(a));
     if (dL1 && (map_operand(&a.p[0].tmZ, X, 1, K, M, 64) || map_operand(&a.p[0].tmV, sdT, 1, 3 * r, M, 64)))
@@ -379,6 +388,7 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
     a.M = (int)M;
     a.r = r;
     a.drop = d;
+    a.keep = keep;
     a.status = status_dev;
     if (launch_mx_grad(a, p, st) != cudaSuccess) return QLORA_ERR_CUDA;
   }

@@ -85,7 +85,8 @@ QDEV TileXY tile_of(int id, int m_tiles, int n_tiles) {
   return TileXY{g * kXGroup + local % gs, local / gs};
 }
 
-// Keep bits of 128 consecutive columns of one row, 32 a word.
+// Keep bits of 128 consecutive columns of one row, 32 a word; also left in
+// memory for the kernel that masks X for dL1, when that is to come.
 QDEV void mask_row(uint32_t (&w)[4], const MxPairArgs& a, const PhiloxKey& key, int64_t row, int col) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -94,6 +95,8 @@ QDEV void mask_row(uint32_t (&w)[4], const MxPairArgs& a, const PhiloxKey& key, 
     for (int j = 0; j < 4; ++j)
       w[i] |= keep8((uint64_t)(row * a.ldo + col + 32 * i + 8 * j) >> 3, key, a.drop.threshold) << (8 * j);
   }
+  if (a.keep && row < a.rows && col < a.cols)
+    a.keep[row * ((a.ldo + 127) / 128) + col / 128] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <bool F32>

@@ -71,6 +71,20 @@ QDEV UnitAt unit_at(const MxGradArgs& a, int64_t u, int64_t u_hi) {
   return x;
 }
 
+// Eight bf16 of which those with a bit in `b` stay.  The products put four
+// bits into the sign bits of four bytes (their copies do not overlap), from
+// where a byte permutation spreads them.
+QDEV uint4 keep_bits(uint4 v, uint32_t b) {
+  const uint32_t lo = (b & 15u) * 0x10204080u, hi = (b >> 4) * 0x10204080u;
+  const auto spread = [](uint32_t x, uint32_t sel) {
+    uint32_t m;
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(m) : "r"(x), "r"(sel));
+    return m;
+  };
+  return make_uint4(v.x & spread(lo, 0x9988u), v.y & spread(lo, 0xBBAAu), v.z & spread(hi, 0x9988u),
+                    v.w & spread(hi, 0xBBAAu));
+}
+
 __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_constant__ MxGradArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -268,10 +282,12 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
     // Units of dL1 come first in a run, so every stage up to the last masked
     // one is masked and the ready barriers' phases follow the ring's.
     const PhiloxKey key = philox_key(args.drop);
+    const uint8_t* keep = args.keep;
+    if (keep) pdl_wait();
     // two groups of 8 warps take alternate stages; a thread has 8 columns of
     // tokens tok and tok + 32, in both boxes
     const int grp = (warp - 8) >> 3, tok = (tid & 255) >> 3, ch = tid & 7;
-    const int64_t c8 = args.p[0].cols >> 3;
+    const int64_t c8 = args.p[0].cols >> 3, kt = (args.p[0].cols + 127) / 128 * 16;
     const uint32_t off = (uint32_t)(tok * 128 + ((ch ^ (tok & 7)) << 4)), thr = args.drop.threshold << 16;
     int s = 0, turn = 0;
     uint32_t ph = 0;
@@ -282,6 +298,25 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
       uint64_t ctr = (uint64_t)((t0 + tok) * c8 + x.tile * 16 + ch);
       for (int i = 0; i < n; ++i, turn ^= 1, ctr += 64 * c8) {
         if (turn == grp) {
+          if (keep) {
+            uint32_t kb[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int m = t0 + 64 * i + tok + 32 * (j & 1);
+              kb[j] = m < args.M ? keep[m * kt + x.tile * 16 + ch + 8 * (j >> 1)] : 0u;
+            }
+            if (!(ok = warp_poll<20>(full + s, ph, abort_flag, args.status, lane))) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint4* at = reinterpret_cast<uint4*>(smem + s * stage + off + 4096 * (j & 1) + 8192 * (j >> 1));
+              *at = keep_bits(*at, kb[j]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready + s);
+          }
+        }
+        if (turn == grp && !keep) {
           // this thread's evaluations before the wait: they need no data
           uint4 rnd[4];
 #pragma unroll

@@ -251,6 +251,21 @@ def test_linear(lib, M, N, K, r, p):
     assert lib.read_status() == 0
 
 
+@pytest.mark.parametrize("M", [129, 250, 256])
+def test_dL1_alike_with_the_mask_of_dX_and_without_dX(lib, M):
+    """dL1 takes the mask's bits from the product of dX where that is wide
+    enough to leave them, and evaluates them without it: bit for bit the same
+    (one piece of the tokens either way).  The last columns end inside a tile."""
+    N, K, r = 64, 9760, 32
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=31 + M)
+    T = _rand((M, r), 1.0, 32).float()
+    drop = lib.Dropout(0.4, 8, 9)
+    dX, with_dX, _ = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop)
+    none, alone, _ = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop, need_dX=False)
+    assert dX is not None and none is None and torch.equal(with_dX, alone)
+    assert lib.read_status() == 0
+
+
 def test_linear_dropped_elements_get_the_base_gradient_alone(lib):
     """Where the mask drops an element of X, dX is the product's alone, bit
     for bit; elsewhere the adapter's term is there."""
