@@ -388,7 +388,8 @@ struct MxGradArgs {
   const uint8_t* keep; // its bits as the product of dX left them, or null: evaluated
   int* status;
 };
-MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool drop, int num_sms);
+enum MxGradMask { kMaskNone, kMaskEvaluated, kMaskBits };
+MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, MxGradMask mask, int num_sms);
 cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st);
 
 // scale * in [M][r] as three bf16 terms [M][3r] (their sum is exact in fp32).

@@ -193,8 +193,9 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms) {
     size_t part = 0;
     for (size_t b : {w.prep_x.part_bytes, w.prep_dy.part_bytes})
       part = b > part ? b : part;
-    for (int i = 0; i < 6; ++i) {  // dL1 and dL2 or one of them, with dropout or without
-      const size_t b = plan_mx_grad(M, i % 3 == 2 ? 0 : K, i % 3 == 1 ? 0 : N, r, i >= 3, sms).part_bytes;
+    for (int i = 0; i < 9; ++i) {  // dL1 and dL2 or one of them, with dropout or without
+      const MxGradMask mask = i < 3 ? kMaskNone : i < 6 ? kMaskEvaluated : kMaskBits;
+      const size_t b = plan_mx_grad(M, i % 3 == 2 ? 0 : K, i % 3 == 1 ? 0 : N, r, mask, sms).part_bytes;
       part = b > part ? b : part;
     }
     o += up256(part);
@@ -371,7 +372,8 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   }
   if (dL1 || dL2) {
     if (dL2 && !dX && !dL1 && launch_split3(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
-    const MxGradPlan p = plan_mx_grad(M, dL1 ? K : 0, dL2 ? N : 0, r, d.threshold && !keep, di.sms);
+    const MxGradMask mask = !d.threshold ? kMaskNone : keep ? kMaskBits : kMaskEvaluated;
+    const MxGradPlan p = plan_mx_grad(M, dL1 ? K : 0, dL2 ? N : 0, r, mask, di.sms);
     MxGradArgs a;
     std::memset(&a, 0, sizeof(a));
     if (dL1 && (map_operand(&a.p[0].tmZ, X, 1, K, M, 64) || map_operand(&a.p[0].tmV, sdT, 1, 3 * r, M, 64)))

@@ -15,14 +15,16 @@
 // small one fills the other's tail.  A tile that is one unit is written at
 // once; other runs end in partial slots that a second kernel adds in order.
 //
-// With dropout the X tile is masked in shared memory before the MMAs read it.
+// With dropout the X tile is masked in shared memory before the MMAs read it:
+// by the bits that the product of dX has left, an eighth of a byte an element,
+// or, without them (dL1 alone, few tokens), by evaluating the generator.
 //
 // Measured, dL2 of 8192 x 8192 with r = 64: 35 us, 134 MB at 3.9 TB/s (4.5
 // TB/s by the slope over longer ones).  Without the loads of the terms the
 // slope is 5.9 TB/s: of a stage's 40 KB the terms are 24, and L2 gives them
-// out at about 11 TB/s.  With dropout (dL1 of the same size) 62 us: the
-// generator costs 1024 evaluations a stage, 90 cycles each a scheduler, on
-// the same pipes as the masking.
+// out at about 11 TB/s.  An evaluated mask costs 1024 evaluations a stage, 90
+// cycles each for a warp and scheduler, on the pipes of the masking: backward
+// of 4096 x 4096 x 4096 with dropout 96 us, with the bits 93.5.
 //
 // Roles: warp 0 TMA producer, 1 MMA issuer, 4-7 sum, 8-23 mask.
 #include "engine_util.cuh"
@@ -41,8 +43,8 @@ constexpr int kGMaxS = 6;
 constexpr int kGBudget = 220 * 1024;  // bytes of the stages
 constexpr int kGPiece = 8;            // 64-token stages of a unit, at most
 
-// Runs are equal in cost: a unit of dL1 with dropout counts 3, others 2 (the
-// mask takes about as long as half a unit's loads).  CTA of a unit, and the
+// Runs are equal in cost: a masked unit of dL1 may count 3, others 2 (the mask
+// takes about as long as half a unit's loads).  CTA of a unit, and the
 // first unit of a CTA.
 __host__ __device__ inline int64_t grad_cost(const MxGradShare& a, int64_t u) {
   return u < a.units0 ? u * a.w0 : a.units0 * a.w0 + (u - a.units0) * 2;
@@ -389,11 +391,11 @@ __global__ void __launch_bounds__(256) mx_grad_finish_kernel(const __grid_consta
 
 }  // namespace
 
-MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool drop, int num_sms) {
+MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, MxGradMask mask, int num_sms) {
   MxGradPlan p{};
   const int64_t t0 = (cols0 + 127) / 128, t1 = (cols1 + 127) / 128;
   if (!t0 && !t1) return p;
-  const bool masked = drop && t0;
+  if (!t0) mask = kMaskNone;
   // As few pieces of the tokens as their greatest length allows, cut evenly.  The
   // masked stages of a unit follow one another at 1.2 us, so with dropout pieces
   // of about half that length are worth their second kernel and balance the
@@ -402,12 +404,15 @@ MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, bool dro
   // 16.3; backward of 1024 x 4096 x 4096: 44 us in four, 49 in two).
   const int64_t stages = (M + 63) / 64;
   int64_t n = (stages + kGPiece - 1) / kGPiece;
-  if (masked && (t0 + t1) * n < num_sms) n = std::max(n, (stages + kGPiece / 4) / (kGPiece / 2));
+  if (mask == kMaskEvaluated && (t0 + t1) * n < num_sms) n = std::max(n, (stages + kGPiece / 4) / (kGPiece / 2));
   p.piece = (int)((stages + n - 1) / n);
   p.pieces = (int)((stages + p.piece - 1) / p.piece);
   p.sh.units0 = t0 * p.pieces;
   p.sh.units = p.sh.units0 + t1 * p.pieces;
-  p.sh.w0 = masked ? 3 : 2;
+  // (with the bits at hand a CTA alone with its unit has no use for the weight:
+  // backward of 1024 x 4096 x 4096 40 us, 44 with it; 4096 x 11008 x 4096 167 us
+  // without, 162 with it)
+  p.sh.w0 = mask == kMaskEvaluated || (mask == kMaskBits && p.sh.units > num_sms) ? 3 : 2;
   // no more CTAs than leave each the cost of a unit, so that none is empty
   // (the slots of a tile's CTAs are then all written)
   const int64_t cost = grad_cost(p.sh, p.sh.units), fit = cost / p.sh.w0;

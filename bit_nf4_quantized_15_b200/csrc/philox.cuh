@@ -7,7 +7,7 @@
 // are at least `threshold` = round(65536 p), so the drop probability is a
 // multiple of 2^-16 and eight neighbours share one evaluation (about 50
 // integer instructions): cheap enough to recompute wherever the mask is
-// needed, so no mask is ever stored.
+// needed, so no mask outlives a call.
 #pragma once
 
 #include "common.cuh"
