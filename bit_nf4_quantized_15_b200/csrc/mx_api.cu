@@ -229,9 +229,9 @@ int qlora_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int 
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = transpose
-                            ? launch_mx_quantize_t(X, dtype, rows, cols, out->codes, out->scales, status_dev, di.sms, st)
-                            : launch_mx_quantize(X, dtype, rows, cols, out->codes, out->scales, status_dev, st);
+  const cudaError_t e =
+      transpose ? launch_mx_quantize_t(X, dtype, rows, cols, out->codes, out->scales, status_dev, di.sms, st)
+                : launch_mx_quantize(X, dtype, rows, cols, out->codes, out->scales, status_dev, st);
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
@@ -366,8 +366,8 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   uint8_t* keep = dX && dL1 && d.threshold ? wb + lay.keep : nullptr;
   if (dX) {
     const LoraTerm lora{sdT, (uint64_t)r * 6, L1, 0, r};
-    if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d, keep ? &keep : nullptr, dX, 0,
-                         status_dev, di.sms, true, st))
+    if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d,
+                         keep ? &keep : nullptr, dX, 0, status_dev, di.sms, true, st))
       return rc;
   }
   if (dL1 || dL2) {

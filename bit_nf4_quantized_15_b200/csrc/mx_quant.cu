@@ -407,7 +407,8 @@ static cudaError_t quantize_t(const void* X, int64_t R, int64_t C, uint8_t* code
   const int kt = (int)((R + 127) / 128);
   const int64_t tiles = (C + 63) / 64 * kt, most = (int64_t)sms * G::CTAS;
   return launch_kernel<mx_quantize_t_kernel<DT>>(
-      {dim3((unsigned)(tiles < most ? tiles : most)), kQT, G::TOTAL, 1, false}, st, tm, R, C, codes, scales, kt, status);
+      {dim3((unsigned)(tiles < most ? tiles : most)), kQT, G::TOTAL, 1, false}, st, tm, R, C, codes, scales, kt,
+      status);
 }
 
 cudaError_t launch_mx_quantize_t(const void* X, int dtype, int64_t R, int64_t C, uint8_t* codes, uint8_t* scales,
