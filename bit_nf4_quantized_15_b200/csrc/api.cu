@@ -51,11 +51,11 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t inner, uint64_t outer,
-             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw, uint64_t pitch) {
+             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
   auto fn = encode_fn();
   if (!fn) return QLORA_ERR_CUDA;
   const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {pitch ? pitch : inner * (uint64_t)esize};
+  const cuuint64_t strides[1] = {inner * (uint64_t)esize};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
@@ -63,13 +63,26 @@ int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize
   return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows,
-                uint64_t pitch) {
+int make_map3(CUtensorMap* m, const void* base, uint64_t n0, uint64_t n1, uint64_t n2, uint64_t s1, uint64_t s2,
+              uint32_t b0, uint32_t b1, uint32_t b2) {
+  auto fn = encode_fn();
+  if (!fn) return QLORA_ERR_CUDA;
+  const cuuint64_t dims[3] = {n0, n1, n2};
+  const cuuint64_t strides[2] = {s1, s2};
+  const cuuint32_t box[3] = {b0, b1, b2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows) {
   if (!mn_major)
     return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k_extent, mn_extent, 64, (uint32_t)rows,
-                    CU_TENSOR_MAP_SWIZZLE_128B, pitch);
+                    CU_TENSOR_MAP_SWIZZLE_128B);
   return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, mn_extent, k_extent, 64, 64,
-                  CU_TENSOR_MAP_SWIZZLE_128B, pitch);
+                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace qnf4

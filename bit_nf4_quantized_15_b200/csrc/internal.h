@@ -14,14 +14,16 @@ struct DevInfo {
   int sms = 148;
 };
 int current_device_info(DevInfo* out);
-// 2-D map over a matrix [outer][inner] of `esize`-byte elements, rows
-// `pitch` bytes apart (0: contiguous).
+// 2-D map over a row-major matrix [outer][inner] of `esize`-byte elements.
 int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t inner, uint64_t outer,
-             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw, uint64_t pitch = 0);
+             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// 3-D map of bf16 with dimensions n0 (contiguous) x n1 x n2, `s1` and `s2` bytes
+// apart, 128-byte swizzle.
+int make_map3(CUtensorMap* m, const void* base, uint64_t n0, uint64_t n1, uint64_t n2, uint64_t s1, uint64_t s2,
+              uint32_t b0, uint32_t b1, uint32_t b2);
 // bf16 operand of the engines.  K-major: matrix [mn][k] (k contiguous), box
 // 64 k x `rows` mn.  MN-major: matrix [k][mn] (mn contiguous), box 64 x 64.
-int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows,
-                uint64_t pitch = 0);
+int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows);
 // Takes the pending request of qlora_debug_stall_next_gemm (0: none).
 uint64_t take_stall_request();
 
@@ -253,20 +255,26 @@ cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64
                               void* out, cudaStream_t st);
 cudaError_t launch_dropout(const void* X, int dtype, int64_t n, const DropArgs& d, void* out, cudaStream_t st);
 
+// bf16 terms of the LoRA term's token side (s T or the scaled dT) in a product.
+// One, its rounding to bf16, would leave an error of up to 2^-9 of the LoRA
+// term, as large as the rounding of the result where that term carries it (1.83e-3
+// of dX of 1088 x 256 x 64, r = 16, in place of 1.65e-3); two leave 2^-16.
+constexpr int kLoraTerms = 2;
+
 // D[col][row] = sum_k A[row, k] B[col, k] (+ the LoRA term, masked when
 // drop.threshold > 0), A and B in MXFP4.
 struct MxGemmArgs {
   CUtensorMap tmA;   // codes of A, uint8 [rows][K/2], box 128 x 128, 128-byte swizzle
   CUtensorMap tmB;   // codes of B, uint8 [cols][K/2], box 128 x BN
   CUtensorMap tmAx;  // LoRA term: A side, bf16 (K- or MN-major per a_mn_ext)
-  CUtensorMap tmBx;  // LoRA term: B side, bf16 [cols][r], K-major
+  CUtensorMap tmBx;  // LoRA term: B side, bf16 (r, kLoraTerms, cols), box 64 x 1 x BN
   const uint8_t* sfA;  // tiled scales
   const uint8_t* sfB;
   int rows, cols;
   int64_t K;
   int kt;            // scale tiles along K
   int kb;            // 256-wide reduction blocks
-  int kb_ext;        // 64-wide reduction blocks of the LoRA term (0: none)
+  int r;             // rank of the LoRA term (0: none)
   int a_mn_ext;
   void* out;         // [cols][ldo]
   int64_t ldo;
@@ -295,13 +303,13 @@ struct MxPairArgs {
   CUtensorMap tmB;   // codes of B (weight), the same
   CUtensorMap tmSA;  // tiled scales as uint32 [row tiles][kt * 128], box 256 x 1
   CUtensorMap tmSB;  // the same, box 256 x 2
-  CUtensorMap tmAx;  // LoRA term: bf16 [rows][r], K-major
+  CUtensorMap tmAx;  // LoRA term: bf16 (r, kLoraTerms, rows), box 64 x 1 x 128
   CUtensorMap tmBx;  // LoRA term: B side (K- or MN-major per b_mn_ext)
   CUtensorMap tmOut; // bf16 output [rows][ldo], box 64 x 32, 128-byte swizzle
   int rows, cols;
   int64_t K;
   int kb;            // 256-wide reduction blocks
-  int kb_ext;
+  int r;             // rank of the LoRA term (0: none)
   int b_mn_ext;
   void* out;         // [rows][ldo]
   int64_t ldo;

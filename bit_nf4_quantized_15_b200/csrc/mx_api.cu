@@ -49,14 +49,21 @@ int drop_args(const qlora_dropout_config* c, DropArgs* d) {
   return QLORA_OK;
 }
 
-// The LoRA term of a product: u [M][r] bf16 (rows `u_pitch` bytes apart) times
-// the feature side v, MN-major ([r][features]) or K-major ([features][r]).
+// The LoRA term of a product: u [M][kLoraTerms of `terms`][r] bf16, whose terms
+// add up to the fp32 operand, times the feature side v, MN-major
+// ([r][features]) or K-major ([features][r]).
 struct LoraTerm {
   const uint16_t* u;
-  uint64_t u_pitch;
+  int terms;
   const uint16_t* v;
   int v_mn, r;
 };
+
+// u as (r, kLoraTerms, M); a box is 64 x 1 x `rows`, zeros past r.
+int map_terms(CUtensorMap* m, const LoraTerm& l, int64_t M, int rows) {
+  return make_map3(m, l.u, (uint64_t)l.r, kLoraTerms, (uint64_t)M, (uint64_t)l.r * 2, (uint64_t)l.r * 2 * l.terms, 64,
+                   1, (uint32_t)rows);
+}
 
 // Scales as a map of uint32 [row tiles][kt * 128]: a box is two tiles of
 // `tiles` row ranges.
@@ -88,10 +95,9 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
         map_scales(&g.tmSB, ws, N, K, 2) || (!out_f32 && map_operand(&g.tmOut, out, 0, M, N, 32)))
       return QLORA_ERR_CUDA;
     if (lora) {
-      if (map_operand(&g.tmAx, lora->u, 0, M, lora->r, 128, lora->u_pitch) ||
-          map_operand(&g.tmBx, lora->v, lora->v_mn, N, lora->r, 128))
+      if (map_terms(&g.tmAx, *lora, M, 128) || map_operand(&g.tmBx, lora->v, lora->v_mn, N, lora->r, 128))
         return QLORA_ERR_CUDA;
-      g.kb_ext = (lora->r + 63) / 64;
+      g.r = lora->r;
       g.b_mn_ext = lora->v_mn;
       g.drop = drop;
       if (keep && drop.threshold) g.keep = reinterpret_cast<uint4*>(*keep);
@@ -114,10 +120,9 @@ int product(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, 
       make_map(&g.tmB, xc, u8, 1, (uint64_t)K / 2, (uint64_t)M, 128, (uint32_t)p.BN, sw))
     return QLORA_ERR_CUDA;
   if (lora) {
-    if (map_operand(&g.tmAx, lora->v, lora->v_mn, N, lora->r, 128) ||
-        map_operand(&g.tmBx, lora->u, 0, M, lora->r, p.BN, lora->u_pitch))
+    if (map_operand(&g.tmAx, lora->v, lora->v_mn, N, lora->r, 128) || map_terms(&g.tmBx, *lora, M, p.BN))
       return QLORA_ERR_CUDA;
-    g.kb_ext = (lora->r + 63) / 64;
+    g.r = lora->r;
     g.a_mn_ext = lora->v_mn;
     g.drop = drop;
   }
@@ -164,8 +169,8 @@ int prep(const uint16_t* X, int64_t M, int64_t C, const uint16_t* L, int l_mn, i
 // Workspace of the linear layer (offsets in bytes).  Forward and backward use
 // the same regions for their own data:
 //   q      MXFP4 of X (forward) or dY (backward): codes, then scales
-//   u, v   bf16 [M][3r]: the scaled dT (u) and s T (v) in three terms, the
-//          first RNbf16; the forward keeps RNbf16(s T) in u
+//   u, v   bf16 [M][3r]: the scaled dT (u) and s T (v) in three terms; the
+//          forward keeps s T in u, [M][2r], in two
 //   keep   bits of the dropout mask, [M][128-column tiles of K], 16 bytes each,
 //          from the product of dX to the kernel of dL1
 //   part   fp32 partial sums of the adapter products
@@ -308,13 +313,13 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
     f.T = T_save;
     f.alpha = d.inv;
     f.out = sT;
-    f.terms = 1;
+    f.terms = kLoraTerms;
     f.beta = s * d.inv;
     if (int rc = prep(X, M, K, L1, 1, r, d, wb, wb + lay.q_scales, part, lay.prep_x, f, status_dev, st)) return rc;
   } else if (launch_mx_quantize(X, QLORA_DTYPE_BF16, M, K, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
     return QLORA_ERR_CUDA;
   }
-  const LoraTerm lora{sT, 0, L2, 1, r};
+  const LoraTerm lora{sT, kLoraTerms, L2, 1, r};
   return product(wb, wb + lay.q_scales, M, w->codes, w->scales, N, K, r ? &lora : nullptr, DropArgs{}, nullptr, Y, 0,
                  status_dev, di.sms, true, st);
 }
@@ -365,7 +370,7 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   // the mask's bits, if dX's product leaves them for dL1
   uint8_t* keep = dX && dL1 && d.threshold ? wb + lay.keep : nullptr;
   if (dX) {
-    const LoraTerm lora{sdT, (uint64_t)r * 6, L1, 0, r};
+    const LoraTerm lora{sdT, 3, L1, 0, r};
     if (int rc = product(wb, wb + lay.q_scales, M, wt->codes, wt->scales, K, N, r ? &lora : nullptr, d,
                          keep ? &keep : nullptr, dX, 0, status_dev, di.sms, true, st))
       return rc;

@@ -7,9 +7,10 @@
 // scales in the MMA; the accumulator is fp32 in tensor memory.  So nothing is
 // dequantised: codes and scales go HBM -> shared memory by TMA, the scales
 // on to tensor memory by tcgen05.cp, and the loop has no arithmetic of its
-// own.  The optional second sum is the LoRA term (bf16, kind::f16) of the
-// linear layer; it is formed first, so that it can be masked by the dropout
-// of the adapter path in tensor memory before the main sum is added to it.
+// own.  The optional second sum is the LoRA term (bf16, kind::f16, the token
+// side in two terms) of the linear layer; it is formed first, so that it can be
+// masked by the dropout of the adapter path in tensor memory before the main
+// sum is added to it.
 //
 // This kernel gives a 128 (rows) x BN (cols) tile to a cluster of 1, 2, 4 or
 // 8 CTAs that split the reduction; the partial tiles meet through distributed
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   const int row_tile = id / n_tiles, col_tile = id % n_tiles;
   const int row0 = row_tile * 128, col0 = col_tile * BN;
   const int kb_lo = (int)((int64_t)rank * args.kb / csize), kb_hi = (int)((int64_t)(rank + 1) * args.kb / csize);
-  const int n_ext = rank == 0 ? args.kb_ext : 0;
+  const int rb = (args.r + 63) / 64;                      // 64-wide blocks of the rank
+  const int n_ext = rank == 0 ? kLoraTerms * rb : 0;      // term by term
   const int n_iters = n_ext + kb_hi - kb_lo;
   const bool masked = n_ext && args.drop.threshold;
   const uint64_t lim = args.wait_ns ? args.wait_ns : QNF4_WAIT_NS;
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
         uint8_t* sa = smem + s * C::STAGE;
         if (it < n_ext) {
           mbar_arrive_expect_tx(full + s, tx_bytes(args.a_mn_ext, 128) + tx_bytes(0, BN));
-          load_operand(sa, &args.tmAx, full + s, args.a_mn_ext, row0, it * 64, 128);
+          load_operand(sa, &args.tmAx, full + s, args.a_mn_ext, row0, it % rb * 64, 128);
         } else {
           const int kb = kb_lo + it - n_ext;
           const uint32_t sbytes = 512u * (uint32_t)min(2, args.kt - 2 * kb);  // scale tiles along K
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
       auto load_b = [&](int it, int s) {
         uint8_t* sb = smem + s * C::STAGE + C::A;
         if (it < n_ext) {
-          load_operand(sb, &args.tmBx, full + s, 0, col0, it * 64, BN);
+          tma_load_3d(sb, &args.tmBx, full + s, it % rb * 64, it / rb, col0);
         } else {
           const int kb = kb_lo + it - n_ext;
           const uint32_t sbytes = 512u * (uint32_t)min(2, args.kt - 2 * kb);
@@ -200,10 +202,12 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
       if (it < n_ext) {
         const uint8_t* sa = smem + s * C::STAGE;
         if (one) {
+          const int steps = (min(64, args.r - it % rb * 64) + 15) / 16;  // zeros past r
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem, operand_desc(sa, args.a_mn_ext, kk), operand_desc(sa + C::A, 0, kk), id_ext,
-                      (it | kk) != 0);
+            if (kk < steps)
+              umma_bf16(tmem, operand_desc(sa, args.a_mn_ext, kk), operand_desc(sa + C::A, 0, kk), id_ext,
+                        (it | kk) != 0);
           umma_commit(empty + s);
           if (it == n_ext - 1) umma_commit(ext_done);
         }

@@ -118,7 +118,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const int pair = (int)(blockIdx.x >> 1), n_pairs = (int)(gridDim.x >> 1);
   const int m_tiles = (args.rows + 255) / 256, n_tiles = (args.cols + 255) / 256, tiles = m_tiles * n_tiles;
-  const int n_ext = args.kb_ext, n_main = args.kb;
+  const int rb = (args.r + 63) / 64;  // 64-wide blocks of the rank
+  const int n_ext = kLoraTerms * rb, n_main = args.kb;
   const bool use_mask = n_ext && args.drop.threshold;
 
   if (tid == 0) {
@@ -164,10 +165,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
         if (i < n_ext) {
           if (leader) mbar_arrive_expect_tx(full + s, 2u * (kXA + kXB));
           if (args.b_mn_ext) {
-            tma_load_2d_pair(sb, &args.tmBx, bar, bcol0, i * 64);
-            tma_load_2d_pair(sb + 8192, &args.tmBx, bar, bcol0 + 64, i * 64);
+            tma_load_2d_pair(sb, &args.tmBx, bar, bcol0, i % rb * 64);
+            tma_load_2d_pair(sb + 8192, &args.tmBx, bar, bcol0 + 64, i % rb * 64);
           } else {
-            tma_load_2d_pair(sb, &args.tmBx, bar, i * 64, bcol0);
+            tma_load_2d_pair(sb, &args.tmBx, bar, i % rb * 64, bcol0);
           }
         } else {
           if (leader) mbar_arrive_expect_tx(full + s, 2u * kXStage);
@@ -180,7 +181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
         uint8_t* sa = smem + s * kXStage;
         const uint32_t bar = full0 + 8u * (uint32_t)s;
         if (i < n_ext) {
-          tma_load_2d_pair(sa, &args.tmAx, bar, i * 64, row0);
+          tma_load_3d_pair(sa, &args.tmAx, bar, i % rb * 64, i / rb, row0);
         } else {
           tma_load_2d_pair(sa, &args.tmA, bar, (i - n_ext) * 128, row0);
           tma_load_2d_pair(sa + kXA + kXB, &args.tmSA, bar, (i - n_ext) * 256, row0 >> 7);
@@ -231,10 +232,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
           if (i < n_ext) {
             const uint8_t* sa = smem + s * kXStage;
             if (one) {
+              const int steps = (min(64, args.r - i % rb * 64) + 15) / 16;  // zeros past r
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                umma_pair(tmem, operand_desc(sa, 0, kk), operand_desc(sa + kXA, args.b_mn_ext, kk), id_ext,
-                          (i | kk) != 0);
+                if (kk < steps)
+                  umma_pair(tmem, operand_desc(sa, 0, kk), operand_desc(sa + kXA, args.b_mn_ext, kk), id_ext,
+                            (i | kk) != 0);
               umma_commit_both(empty + s);
               if (i == n_ext - 1) umma_commit_both(ext);
             }

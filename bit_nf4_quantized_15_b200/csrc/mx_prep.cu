@@ -13,8 +13,9 @@
 //
 // Work is cut into units of 128 rows x 256 columns.  While clusters of up to 8
 // CTAs for every row tile run at once, a cluster takes a row tile, adds its
-// CTAs' sums in rank order through distributed shared memory and forms T,
-// RNbf16(s T) or the three bf16 terms of the scaled D itself.  For more rows
+// CTAs' sums in rank order through distributed shared memory and forms T and
+// the bf16 terms of the scaled D itself (two for the products, three where the
+// adapter gradients take them too).  For more rows
 // one CTA per SM takes an equal run of units in order (the last units of a row
 // tile and the first of the next may share a CTA); a run's rows of D go to a
 // partial slot, and a small second kernel adds the slots of a row tile in
@@ -68,10 +69,29 @@ __host__ __device__ inline int prep_owner(int64_t units, int grid, int64_t u) {
   return (int)(((u + 1) * grid - 1) / units);
 }
 
+// The first bf16 term of v: v rounded toward zero (so it never overflows, and
+// what is left has v's sign), an Inf or NaN as it is.
+QDEV float first_term(float v) {
+  const float h = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+  return v != v ? __uint_as_float(0x7FC00000u) : h;
+}
+// What the other terms stand for.  An Inf or NaN is repeated, and nothing left
+// of a number is 2^-126 of its sign: multiplied with an Inf on the other side
+// every term then gives what v itself gives, where 0 or Inf - Inf would make
+// it NaN.
+QDEV float rest_of(float v, float h) {
+  if ((__float_as_uint(v) & 0x7F800000u) == 0x7F800000u) return h;
+  const float d = __fsub_rn(v, h);  // exact
+  return d == 0.0f && fabsf(h) > 0x1p-100f ? copysignf(0x1p-126f, h) : d;
+}
 // beta v as `terms` bf16 terms, r elements apart; four neighbours at a time.
+// Two terms hold 16 bits of it (2^-16 relative), three all of an fp32.
 QDEV void store_terms(uint16_t* out, float4 v, float beta, int terms, int r) {
   v = make_float4(__fmul_rn(v.x, beta), __fmul_rn(v.y, beta), __fmul_rn(v.z, beta), __fmul_rn(v.w, beta));
-  for (int t = 0; t < terms; ++t) {
+  const float4 h = make_float4(first_term(v.x), first_term(v.y), first_term(v.z), first_term(v.w));
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(h.x, h.y), pack_bf16x2(h.z, h.w));
+  v = make_float4(rest_of(v.x, h.x), rest_of(v.y, h.y), rest_of(v.z, h.z), rest_of(v.w, h.w));
+  for (int t = 1; t < terms; ++t) {
     const uint2 w = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     *reinterpret_cast<uint2*>(out + (int64_t)t * r) = w;
     v = make_float4(__fsub_rn(v.x, __uint_as_float(w.x << 16)), __fsub_rn(v.y, __uint_as_float(w.x & 0xFFFF0000u)),

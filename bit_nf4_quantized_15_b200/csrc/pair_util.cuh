@@ -110,6 +110,13 @@ QDEV void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x,
       "l"((uint64_t)m), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+QDEV void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)m), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 QDEV void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
                "r"(ncols)

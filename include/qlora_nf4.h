@@ -392,9 +392,10 @@ QLORA_API size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K
 /*
  * Forward of the LoRA linear layer on an MXFP4 weight W^ [N][K]:
  *   T = drop(X) . L1                      (fp32, saved for the backward)
- *   Y = RNbf16( Q(X) . W^T + RNbf16(s T) . L2 )
+ *   Y = RNbf16( Q(X) . W^T + s T . L2 )
  * Q is the MXFP4 quantisation along K, drop the dropout of element m K + k of
- * X (drop = NULL: none).  r = 0 (L1, L2, T_save NULL): no adapter.
+ * X (drop = NULL: none).  r = 0 (L1, L2, T_save NULL): no adapter.  s T enters
+ * its product as two bf16 terms (2^-16 of it at most is left out).
  *   X : bf16[M][K]   L1 : bf16[K][r]   L2 : bf16[r][N]   Y : bf16[M][N]
  * Requires K % 32 == 0, N % 8 == 0 and r = 0 or r % 8 == 0, 8 <= r <= 128.
  * A non-finite X sets *status_dev = QLORA_ERR_NONFINITE and gives NaN in its
@@ -408,11 +409,12 @@ QLORA_API int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_t
  * Backward of the same layer.  wt is the weight quantised along the output
  * features, the MXFP4 form of W^T, [K][N] (qlora_mx_quantize, transpose = 1).
  *   dT  = s dY . L2^T
- *   dX  = RNbf16( Q(dY) . Wt^T + drop(RNbf16(dT) . L1^T) )
+ *   dX  = RNbf16( Q(dY) . Wt^T + drop(dT . L1^T) )
  *   dL1 = drop(X)^T . dT        (fp32)
  *   dL2 = s T^T . dY            (fp32)
  * dT and s T enter the products of dL1 and dL2 unrounded (three bf16 terms
- * each, whose sum is the fp32 value).  drop names the forward's mask.  dX, dL1 or dL2 may be NULL to
+ * each, whose sum is the fp32 value); dT enters dX as the first two of its
+ * terms (2^-16 of it at most is left out).  drop names the forward's mask.  dX, dL1 or dL2 may be NULL to
  * skip that output (wt may then be NULL with dX, L1 and L2 must not).  Requires
  * K % 32 == 0, N % 32 == 0; r as in the forward; r = 0: dX alone.  A non-finite
  * dY sets *status_dev = QLORA_ERR_NONFINITE and gives NaN in its row of dX.

@@ -1,0 +1,72 @@
+"""The MXFP4 linear layer, its products and dropout where they can go wrong:
+small reductions that leave the LoRA term to carry the result, infinities, the
+paths that long reductions take, buffers that the caller gives.
+
+Bounds as in test_gpu_mx.py: half a bf16 step of a bf16 result, and one unit
+lost to truncation a step of the tensor cores' fp32 sums."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import to_f64
+from oracle import mx as O
+from test_gpu_mx import HALF_BF16, _acc, _problem, _within
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------- the LoRA term's bits
+@pytest.mark.parametrize("M,N,K,r,p", [(40, 352, 64, 8, 0.0), (1088, 256, 64, 16, 0.05), (257, 64, 96, 128, 0.0),
+                                       (2304, 2304, 64, 8, 0.25), (2100, 2400, 32, 72, 0.1)])
+def test_lora_term_keeps_sixteen_bits(lib, M, N, K, r, p):
+    """Where the LoRA term is as large as the base product, Y and dX are off
+    by the rounding of the result and by 2^-16 of the LoRA term's sizes, not by
+    the 2^-9 of an operand rounded to bf16."""
+    X, w, L1, L2, dY, W64 = _problem(lib, M, N, K, r, seed=M + r)
+    s = 16.0 / r
+    drop = lib.Dropout(p, 5, M) if p else None
+    mask = O.dropout_keep(M * K, p, 5, M).reshape(M, K) * O.dropout_scale(p) if p else np.ones((M, K))
+    Y, T = lib.mx_linear_fwd(X, w, L1, L2, s, dropout=drop)
+    dX, _, _ = lib.mx_linear_bwd(dY, X, T, w, L1, L2, s, dropout=drop)
+    X64, dY64, A, B = to_f64(X), to_f64(dY), to_f64(L1), to_f64(L2)
+    What, Wt = O.mx_rounded(W64), O.mx_rounded(W64.T)
+    Yr, Tr = O.mx_linear_fwd(X64, What, A, B, s, mask)
+    dXr, _, _ = O.mx_linear_bwd(dY64, X64, Tr, Wt, A, B, s, mask)
+    two = _acc(2 * max(r, 16), 16)  # steps of both terms
+    # T: a sum of K < 512 products and one rounding each of it, of s and of their product
+    t_err = _acc(K, 16) * (np.abs(X64 * mask) @ np.abs(A)) + 2.0 ** -22 * np.abs(Tr)
+    lora = s * np.abs(Tr) @ np.abs(B)
+    size = np.abs(O.mx_rounded(X64)) @ np.abs(What).T + lora
+    _within(Y, Yr, 1.01 * (HALF_BF16 * np.abs(Yr) + 2.0 ** -16 * lora + (_acc(K, 64) + two) * size
+                           + s * t_err @ np.abs(B)), "Y")
+    dTr = s * dY64 @ B.T
+    dt_err = (5 * _acc(min(N, 512), 16)) * s * (np.abs(dY64) @ np.abs(B).T) + 2.0 ** -22 * np.abs(dTr)
+    lora = (np.abs(dTr) @ np.abs(A).T) * mask
+    size = np.abs(O.mx_rounded(dY64)) @ np.abs(Wt).T + lora
+    _within(dX, dXr, 1.01 * (HALF_BF16 * np.abs(dXr) + 2.0 ** -16 * lora + (_acc(N, 64) + two) * size
+                             + (dt_err @ np.abs(A).T) * mask), "dX")
+    assert lib.read_status() == 0
+
+
+@pytest.mark.parametrize("M,N", [(40, 352), (300, 9792)])
+def test_infinite_adapter_gives_infinities(lib, M, N):
+    """An infinity in L2 makes its column of Y +-Inf by the sign of s T, also
+    where s T has no bits for a second term; one in L1 its column of dX."""
+    K, r = 64, 16
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=3)
+    L1[:, 3], L1[5, 3] = 0, 1.0           # T[:, 3] = X[:, 5]: a bf16, one term
+    L2[3, 7], L2[9, 11] = float("inf"), float("-inf")
+    Y, T = lib.mx_linear_fwd(X, w, L1, L2, 1.0)
+    assert torch.equal(T[:, 3], X[:, 5].float())
+    inf = torch.tensor(float("inf"), device="cuda")
+    assert torch.equal(Y[:, 7].float(), torch.copysign(inf, T[:, 3]))
+    assert torch.equal(Y[:, 11].float(), torch.copysign(inf, -T[:, 9]))
+    rest = [c for c in range(N) if c not in (7, 11)]
+    assert torch.isfinite(Y[:, rest]).all()
+    L2[3, 7] = L2[9, 11] = 0
+    L1[20, 4] = float("inf")
+    dX, _, _ = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 1.0)
+    dT = to_f64(dY) @ to_f64(L2).T
+    assert np.array_equal(to_f64(dX[:, 20]), np.copysign(np.inf, dT[:, 4]))
+    assert torch.isfinite(dX[:, :20]).all() and torch.isfinite(dX[:, 21:]).all()
