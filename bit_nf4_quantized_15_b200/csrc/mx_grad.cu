@@ -73,6 +73,16 @@ QDEV UnitAt unit_at(const MxGradArgs& a, int64_t u, int64_t u_hi) {
   return x;
 }
 
+// The sum of the three terms' groups.  Where the first is an Inf or NaN it is
+// the sum: the other terms may be zero, and an infinite X or dY makes NaN of
+// them.
+QDEV float add_groups(uint32_t v, uint32_t w, uint32_t z) {
+  const float first = __uint_as_float(v);
+  return (v & 0x7F800000u) == 0x7F800000u
+             ? first
+             : __fadd_rn(first, __fadd_rn(__uint_as_float(w), __uint_as_float(z)));
+}
+
 // Eight bf16 of which those with a bit in `b` stay.  The products put four
 // bits into the sign bits of four bytes (their copies do not overlap), from
 // where a byte permutation spreads them.
@@ -233,9 +243,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
         tmem_ld16(at + 2u * (uint32_t)r, z);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          v[j] = __float_as_uint(
-              __fadd_rn(__uint_as_float(v[j]), __fadd_rn(__uint_as_float(w[j]), __uint_as_float(z[j]))));
+        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(add_groups(v[j], w[j], z[j]));
         if (!first) {
           tmem_ld16(tl + sum_col + (uint32_t)c, w);
           tmem_wait_ld();

@@ -418,6 +418,8 @@ QLORA_API int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_t
  * skip that output (wt may then be NULL with dX, L1 and L2 must not).  Requires
  * K % 32 == 0, N % 32 == 0; r as in the forward; r = 0: dX alone.  A non-finite
  * dY sets *status_dev = QLORA_ERR_NONFINITE and gives NaN in its row of dX.
+ * In dL1 and dL2 an infinite X, dT, T or dY gives what the formula gives: an
+ * infinity, or NaN where infinities cancel or meet a zero (a dropped X is 0).
  */
 QLORA_API int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const float* T_saved,
                                   const qlora_mx_tensor* wt, int64_t N, int64_t K, const uint16_t* L1,

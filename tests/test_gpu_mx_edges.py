@@ -70,3 +70,49 @@ def test_infinite_adapter_gives_infinities(lib, M, N):
     dT = to_f64(dY) @ to_f64(L2).T
     assert np.array_equal(to_f64(dX[:, 20]), np.copysign(np.inf, dT[:, 4]))
     assert torch.isfinite(dX[:, :20]).all() and torch.isfinite(dX[:, 21:]).all()
+
+
+# ------------------------------------------------ non-finite values, gradients
+def _same_non_finite(got, ref, what):
+    """NaN and infinities where the formula has them, finite elsewhere."""
+    got = to_f64(got)
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), what
+    assert np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)]), what
+    assert np.isfinite(got[np.isfinite(ref)]).all(), what
+
+
+@pytest.mark.parametrize("p", [0.0, 0.25])
+@pytest.mark.parametrize("M", [40, 1100])
+@pytest.mark.parametrize("where", ["X", "dY", "T", "dT"])
+def test_infinities_in_the_adapter_gradients(lib, where, M, p):
+    """dL1 and dL2 of an infinite X, dY, T or dT are the formula's, whether the
+    other side has bits in all three terms or in the first alone, in one piece
+    of the tokens and in several."""
+    N, K, r, s = 96, 160, 16, 0.5
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=M)
+    L2[:, 5], L2[3] = 0.0, 0.0
+    L2[3, 9] = 1.0                       # dT[:, 3] = s dY[:, 9]: a bf16
+    T = torch.randn((M, r), generator=torch.Generator("cuda").manual_seed(M), device="cuda")
+    T[:, 4] = T[:, 4].bfloat16().float()
+    drop = lib.Dropout(p, 3, 4) if p else None
+    keep = O.dropout_keep(M * K, p, 3, 4).reshape(M, K)
+    m = M - 7
+    if where == "X":
+        X[m, int(np.flatnonzero(keep[m])[2])], X[m - 3, int(np.flatnonzero(keep[m - 3])[4])] = float("inf"), float("-inf")
+    elif where == "dY":
+        dY[m, 5] = float("-inf")         # where L2 has no column: dT meets 0 Inf
+    elif where == "T":
+        T[m, 2], T[m - 1, 4] = float("inf"), float("-inf")
+    else:
+        s, dY[m, 9], L2[6, 9] = 1e3, 1e30, 1e7   # s dT[m, 6] is past the largest fp32
+    dX, dL1, dL2 = lib.mx_linear_bwd(dY, X, T, w, L1, L2, s, dropout=drop, need_dX=False)
+    with np.errstate(all="ignore"):
+        dT = to_f64(dY) @ to_f64(L2).T
+        dT = (s * dT).astype(np.float32).astype(np.float64)
+        Xm = np.where(keep, to_f64(X), 0.0)
+        ref1, ref2 = Xm.T @ dT, s * to_f64(T).T @ to_f64(dY)
+    _same_non_finite(dL1, ref1, "dL1")
+    _same_non_finite(dL2, ref2, "dL2")
+    assert not np.isfinite(ref1).all() or not np.isfinite(ref2).all()
+    assert dX is None
+    lib.read_status()
