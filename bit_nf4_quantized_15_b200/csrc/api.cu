@@ -258,7 +258,7 @@ const char* qlora_status_string(int code) {
     case QLORA_ERR_RANK: return "unsupported LoRA rank (need r % 8 == 0, 8 <= r <= 128)";
     case QLORA_ERR_WORKSPACE: return "workspace too small";
     case QLORA_ERR_CUDA: return "CUDA runtime or driver call failed";
-    case QLORA_ERR_NONFINITE: return "weight holds an Inf or NaN";
+    case QLORA_ERR_NONFINITE: return "an operand (NF4: the weight) holds an Inf or NaN";
     case QLORA_ERR_TIMEOUT: return "an internal GPU wait expired";
     case QLORA_ERR_DEVICE: return "current device is not an sm_100 GPU";
     case QLORA_ERR_FORMAT: return "unknown code format (QLORA_FMT_*) or scale codec (QLORA_SCALE_*)";

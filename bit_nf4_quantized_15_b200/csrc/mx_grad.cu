@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
     const int r = args.r, r16 = (r + 15) / 16 * 16;
     int b = 0;
     uint32_t wph = 0;
-    bool first = true;
+    bool first = true, bad = false;
     for (int64_t u = u_lo; u < u_hi; ++u) {
       const UnitAt x = unit_at(args, u, u_hi);
       if (!warp_wait_backoff(wfull + b, wph, abort_flag, args.status, lane, 100)) break;
@@ -249,6 +249,10 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(w[j])));
+        }
+        if (x.last) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) bad |= c + j < r && (v[j] & 0x7F800000u) == 0x7F800000u;
         }
         if (!x.last) {
           tmem_st16(tl + sum_col + (uint32_t)c, v);
@@ -287,6 +291,8 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
         wph ^= 1u;
       }
     }
+    // dY is looked at where it is quantised, X and T (and dY for dL2 alone) only here
+    if (bad) report(args.status, QLORA_ERR_NONFINITE);
   } else if (warp >= 8 && args.drop.threshold) {
     // ----------------------------------------------------------------- mask
     // Units of dL1 come first in a run, so every stage up to the last masked

@@ -55,7 +55,7 @@ enum {
   QLORA_ERR_RANK = -4,        /* r not a multiple of 8 in [8, 128] */
   QLORA_ERR_WORKSPACE = -5,   /* ws too small (see qlora_workspace_bytes) */
   QLORA_ERR_CUDA = -6,        /* a CUDA runtime / driver call failed */
-  QLORA_ERR_NONFINITE = -7,   /* device status: W holds an Inf or NaN */
+  QLORA_ERR_NONFINITE = -7,   /* device status: W (MXFP4: any operand) holds an Inf or NaN */
   QLORA_ERR_TIMEOUT = -8,     /* device status: an internal wait expired */
   QLORA_ERR_DEVICE = -9,      /* current device is not sm_100 */
   QLORA_ERR_SCRATCH_LIMIT = -10, /* problem needs more than the library's static scratch */
@@ -417,7 +417,8 @@ QLORA_API int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_t
  * terms (2^-16 of it at most is left out).  drop names the forward's mask.  dX, dL1 or dL2 may be NULL to
  * skip that output (wt may then be NULL with dX, L1 and L2 must not).  Requires
  * K % 32 == 0, N % 32 == 0; r as in the forward; r = 0: dX alone.  A non-finite
- * dY sets *status_dev = QLORA_ERR_NONFINITE and gives NaN in its row of dX.
+ * dY, or a non-finite sum in dL1 or dL2, sets *status_dev = QLORA_ERR_NONFINITE;
+ * the dY gives NaN in its row of dX.
  * In dL1 and dL2 an infinite X, dT, T or dY gives what the formula gives: an
  * infinity, or NaN where infinities cancel or meet a zero (a dropped X is 0).
  */

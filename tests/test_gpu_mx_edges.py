@@ -116,3 +116,30 @@ def test_infinities_in_the_adapter_gradients(lib, where, M, p):
     assert not np.isfinite(ref1).all() or not np.isfinite(ref2).all()
     assert dX is None
     lib.read_status()
+
+
+@pytest.mark.parametrize("M", [33, 1100])
+def test_non_finite_operands_of_single_gradients_are_reported(lib, M):
+    """Also where the call does not quantise dY (dL2 alone), and for X and T."""
+    N, K, r = 96, 160, 24
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=M)
+    T = torch.ones((M, r), device="cuda")
+    lib.read_status()
+
+    def status(dY=dY, X=X, T=T, **need):
+        lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, need_dX=False, **need)
+        return lib.read_status()
+
+    def broken(t, value):
+        t = t.clone()
+        t[M - 1, 9] = value
+        return t
+
+    only1, only2 = dict(need_dL2=False), dict(need_dL1=False)
+    assert status() == status(**only1) == status(**only2) == 0
+    for value in (float("nan"), float("inf")):
+        assert status(dY=broken(dY, value), **only2) == -7
+        assert status(dY=broken(dY, value), **only1) == -7
+        assert status(T=broken(T, value), **only2) == -7
+        assert status(X=broken(X, value), **only1) == -7
+        assert status(T=broken(T, value), **only1) == status(X=broken(X, value), **only2) == 0
