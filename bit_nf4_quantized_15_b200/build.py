@@ -18,9 +18,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libqlora_nf4.so")
-SOURCES = ["api.cu", "mx_api.cu", "mx_gemm.cu", "mx_gemm_pair.cu", "mx_prep.cu", "mx_grad.cu", "mx_quant.cu", "engine.cu", "engine_pair.cu", "gemv.cu", "gemv_bwd.cu", "quant.cu", "adapters.cu",
-           "noalloc.cu", "nf4_tables.cpp"]
-HEADERS = ["common.cuh", "philox.cuh", "mx_codec.cuh", "launch.cuh", "mx_util.cuh", "pair_util.cuh", "engine_util.cuh", "internal.h"]
+SOURCES = ["api.cu", "mx_api.cu", "mx_gemm.cu", "mx_gemm_pair.cu", "mx_prep.cu", "mx_grad.cu", "mx_quant.cu", "engine.cu",
+           "engine_pair.cu", "gemv.cu", "gemv_bwd.cu", "quant.cu", "adapters.cu", "noalloc.cu", "nf4_tables.cpp"]
+HEADERS = ["common.cuh", "philox.cuh", "mx_codec.cuh", "mx_plan.h", "launch.cuh", "mx_util.cuh", "pair_util.cuh",
+           "engine_util.cuh", "internal.h"]
 
 
 def nvcc_path() -> str:

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "mx_plan.h"
+
 namespace qnf4 {
 
 // ------------------------------------------------- host helpers (api.cu)
@@ -322,14 +324,6 @@ size_t mx_pair_smem_bytes();
 cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, bool dependent, cudaStream_t st);
 
 // Quantise X and form D = drop(X).L in one pass (mx_prep.cu).
-struct MxPrepPlan {
-  int units_per_tile;   // units (128 rows x 256 columns) of a row tile
-  int64_t units;
-  bool direct;          // a cluster of `cluster` CTAs finishes a row tile
-  int cluster;
-  int grid, maxc;       // CTAs; most CTAs that share a row tile (not direct)
-  size_t part_bytes;    // fp32 [row tiles][maxc][128][r] (not direct)
-};
 // What becomes of D.
 struct MxPrepFinish {
   int64_t M;
@@ -344,7 +338,7 @@ struct MxPrepFinish {
   const float* part;    // from here filled by the launch
   int r;
   int64_t units;
-  int units_per_tile, grid, maxc;
+  int units_per_tile, grid;
 };
 struct MxPrepArgs {
   CUtensorMap tmX;      // bf16 [M][C], box 64 x 128, 128-byte swizzle
@@ -355,14 +349,13 @@ struct MxPrepArgs {
   int64_t cols;
   int r, r16, l_mn;     // r16: r rounded up to 16
   int64_t units;
-  int units_per_tile, maxc;
+  int units_per_tile;
   int direct;
   float* part;
   MxPrepFinish fin;
   DropArgs drop;
   int* status;
 };
-MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms);
 cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st);
 
 // Adapter gradients (mx_grad.cu): problem 0 is dL1 = drop(X)^T.u, problem 1
@@ -372,32 +365,20 @@ struct MxGradProblem {
   CUtensorMap tmV;  // bf16 [M][3r], the same box
   int64_t cols;
   int transposed;   // out is [r][cols], else [cols][r]
-  float* part;
   float* out;
-};
-struct MxGradShare {  // how the units are shared out
-  int64_t units0, units;  // 128 columns x 512 tokens: of problem 0, of both
-  int w0, grid;           // cost of a unit of problem 0 (the other's: 2), CTAs
-};
-struct MxGradPlan {
-  MxGradShare sh;
-  int piece, pieces;      // 64-token stages of a unit, units of a tile
-  int maxc, n16, nbuf, vboxes, stages;
-  size_t part0_bytes, part_bytes;
 };
 struct MxGradArgs {
   MxGradProblem p[2];
   int M, r;
   MxGradShare sh;
-  int piece, pieces, maxc;
+  int piece, pieces;
+  float* part;         // slots, the tiles of problem 0 first
   int n16, nbuf;       // columns of an accumulator (3r up to 16), accumulators
   int vboxes, stages;
   DropArgs drop;       // mask of X
   const uint8_t* keep; // its bits as the product of dX left them, or null: evaluated
   int* status;
 };
-enum MxGradMask { kMaskNone, kMaskEvaluated, kMaskBits };
-MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, MxGradMask mask, int num_sms);
 cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st);
 
 // scale * in [M][r] as three bf16 terms [M][3r] (their sum is exact in fp32).

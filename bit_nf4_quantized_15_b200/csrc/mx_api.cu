@@ -1,5 +1,6 @@
 // The C ABI of the MXFP4 calls and of dropout (include/qlora_nf4.h):
 // argument checks, tensor maps, workspace layout and launches.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -167,7 +168,8 @@ int prep(const uint16_t* X, int64_t M, int64_t C, const uint16_t* L, int l_mn, i
 }
 
 // Workspace of the linear layer (offsets in bytes).  Forward and backward use
-// the same regions for their own data:
+// the same regions for their own data.  Every region's size only grows with M,
+// so a workspace sized for the largest batch holds the smaller ones:
 //   q      MXFP4 of X (forward) or dY (backward): codes, then scales
 //   u, v   bf16 [M][3r]: the scaled dT (u) and s T (v) in three terms; the
 //          forward keeps s T in u, [M][2r], in two
@@ -195,15 +197,7 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms) {
     w.part = o;
     w.prep_x = plan_mx_prep(M, K, r, sms);
     w.prep_dy = plan_mx_prep(M, N, r, sms);
-    size_t part = 0;
-    for (size_t b : {w.prep_x.part_bytes, w.prep_dy.part_bytes})
-      part = b > part ? b : part;
-    for (int i = 0; i < 9; ++i) {  // dL1 and dL2 or one of them, with dropout or without
-      const MxGradMask mask = i < 3 ? kMaskNone : i < 6 ? kMaskEvaluated : kMaskBits;
-      const size_t b = plan_mx_grad(M, i % 3 == 2 ? 0 : K, i % 3 == 1 ? 0 : N, r, mask, sms).part_bytes;
-      part = b > part ? b : part;
-    }
-    o += up256(part);
+    o += up256(std::max({w.prep_x.part_bytes, w.prep_dy.part_bytes, mx_grad_part_bound(M, K, N, r, sms)}));
   }
   w.total = o;
   return w;
@@ -386,14 +380,13 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
     if (dL2 && (map_operand(&a.p[1].tmZ, dY, 1, N, M, 64) || map_operand(&a.p[1].tmV, sT, 1, 3 * r, M, 64)))
       return QLORA_ERR_CUDA;
     a.p[0].cols = K;
-    a.p[0].part = part;
     a.p[0].out = dL1;
     a.p[1].cols = N;
     a.p[1].transposed = 1;
-    a.p[1].part = part + p.part0_bytes / sizeof(float);
     a.p[1].out = dL2;
     a.M = (int)M;
     a.r = r;
+    a.part = part;
     a.drop = d;
     a.keep = keep;
     a.status = status_dev;

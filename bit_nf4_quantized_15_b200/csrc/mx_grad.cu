@@ -33,30 +33,10 @@
 #include "pair_util.cuh"
 #include "philox.cuh"
 
-#include <algorithm>
-
 namespace qnf4 {
 namespace {
 
 constexpr int kGThreads = 24 * 32;
-constexpr int kGMaxS = 6;
-constexpr int kGBudget = 220 * 1024;  // bytes of the stages
-constexpr int kGPiece = 8;            // 64-token stages of a unit, at most
-
-// Runs are equal in cost: a masked unit of dL1 may count 3, others 2 (the mask
-// takes about as long as half a unit's loads).  CTA of a unit, and the
-// first unit of a CTA.
-__host__ __device__ inline int64_t grad_cost(const MxGradShare& a, int64_t u) {
-  return u < a.units0 ? u * a.w0 : a.units0 * a.w0 + (u - a.units0) * 2;
-}
-__host__ __device__ inline int grad_owner(const MxGradShare& a, int64_t u) {
-  return (int)(grad_cost(a, u) * a.grid / grad_cost(a, a.units));
-}
-__host__ __device__ inline int64_t grad_first(const MxGradShare& a, int64_t c) {
-  const int64_t x = (c * grad_cost(a, a.units) + a.grid - 1) / a.grid, x0 = a.units0 * a.w0;
-  return x <= x0 ? (x + a.w0 - 1) / a.w0 : a.units0 + (x - x0 + 1) / 2;
-}
-
 struct UnitAt {
   int prob;      // 0: dL1, 1: dL2
   int tile;      // 128-column tile
@@ -102,9 +82,9 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stage = 16384 + args.vboxes * 8192, kS = args.stages;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kS * stage);
-  uint64_t* ready = full + kGMaxS;
-  uint64_t* empty = ready + kGMaxS;
-  uint64_t* wfull = empty + kGMaxS;
+  uint64_t* ready = full + kGradMaxStages;
+  uint64_t* empty = ready + kGradMaxStages;
+  uint64_t* wfull = empty + kGradMaxStages;
   uint64_t* wempty = wfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -229,10 +209,8 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
       float* const out = p.out;
       const int64_t cols = p.cols;
       const bool transposed = p.transposed, whole = args.pieces == 1;
-      // this run's slot of the tile: its ordinal among the CTAs that share it
-      const int64_t tile_u = (x.prob ? args.sh.units0 : 0) + (int64_t)x.tile * args.pieces;
-      const int ord = (int)blockIdx.x - grad_owner(args.sh, tile_u);
-      float* slot = p.part + ((int64_t)x.tile * args.maxc + ord) * 128 * r;
+      // this run's slot of the tile (those of dL1 come first)
+      float* slot = args.part + mx_slot(u / args.pieces, blockIdx.x) * 128 * r;
       const int row = q4 * 32 + lane;
       const int64_t col = (int64_t)x.tile * 128 + row;
       for (int c = 0; c < r16; c += 16) {
@@ -386,10 +364,10 @@ __global__ void __launch_bounds__(256) mx_grad_finish_kernel(const __grid_consta
   const int prob = blockIdx.x >= tiles0;
   const MxGradProblem& p = a.p[prob];
   const int64_t tile = blockIdx.x - (prob ? tiles0 : 0), tile_u = (int64_t)blockIdx.x * a.pieces;
-  const int nc = grad_owner(a.sh, tile_u + a.pieces - 1) - grad_owner(a.sh, tile_u);
+  const int first = grad_owner(a.sh, tile_u), nc = grad_owner(a.sh, tile_u + a.pieces - 1) - first;
   const int64_t left = p.cols - tile * 128;
   const int ncol = (int)(left < 128 ? left : 128), slot = 128 * a.r;
-  const float* s = p.part + tile * a.maxc * slot;
+  const float* s = a.part + mx_slot(blockIdx.x, first) * slot;
   for (int i = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4; i < slot; i += (int)gridDim.y * 1024) {
     if (p.transposed ? (i & 127) >= ncol : i >= ncol * a.r) continue;
     float4 d = *reinterpret_cast<const float4*>(s + i);
@@ -405,52 +383,10 @@ __global__ void __launch_bounds__(256) mx_grad_finish_kernel(const __grid_consta
 
 }  // namespace
 
-MxGradPlan plan_mx_grad(int64_t M, int64_t cols0, int64_t cols1, int r, MxGradMask mask, int num_sms) {
-  MxGradPlan p{};
-  const int64_t t0 = (cols0 + 127) / 128, t1 = (cols1 + 127) / 128;
-  if (!t0 && !t1) return p;
-  if (!t0) mask = kMaskNone;
-  // As few pieces of the tokens as their greatest length allows, cut evenly.  The
-  // masked stages of a unit follow one another at 1.2 us, so with dropout pieces
-  // of about half that length are worth their second kernel and balance the
-  // CTAs while those do not have a longer unit each (gradients of 512 x 512 x
-  // 512, r = 64: 21 us in two pieces, 27 in one, but without dropout 17.8 and
-  // 16.3; backward of 1024 x 4096 x 4096: 44 us in four, 49 in two).
-  const int64_t stages = (M + 63) / 64;
-  int64_t n = (stages + kGPiece - 1) / kGPiece;
-  if (mask == kMaskEvaluated && (t0 + t1) * n < num_sms) n = std::max(n, (stages + kGPiece / 4) / (kGPiece / 2));
-  p.piece = (int)((stages + n - 1) / n);
-  p.pieces = (int)((stages + p.piece - 1) / p.piece);
-  p.sh.units0 = t0 * p.pieces;
-  p.sh.units = p.sh.units0 + t1 * p.pieces;
-  // (with the bits at hand a CTA alone with its unit has no use for the weight:
-  // backward of 1024 x 4096 x 4096 40 us, 44 with it; 4096 x 11008 x 4096 167 us
-  // without, 162 with it)
-  p.sh.w0 = mask == kMaskEvaluated || (mask == kMaskBits && p.sh.units > num_sms) ? 3 : 2;
-  // no more CTAs than leave each the cost of a unit, so that none is empty
-  // (the slots of a tile's CTAs are then all written)
-  const int64_t cost = grad_cost(p.sh, p.sh.units), fit = cost / p.sh.w0;
-  p.sh.grid = (int)(fit < num_sms ? fit : num_sms);
-  // most CTAs that share a tile: its cost over a CTA's, and one at either end
-  p.maxc = (int)((int64_t)p.pieces * p.sh.w0 * p.sh.grid / cost) + 2;
-  if (p.pieces > 1) {
-    p.part0_bytes = (size_t)t0 * p.maxc * 128 * r * sizeof(float);
-    p.part_bytes = p.part0_bytes + (size_t)t1 * p.maxc * 128 * r * sizeof(float);
-  }
-  p.n16 = (3 * r + 15) / 16 * 16;
-  const int r16 = (r + 15) / 16 * 16;
-  p.nbuf = 2 * p.n16 + r16 <= 512 ? 2 : 1;
-  p.vboxes = (p.n16 + 63) / 64;
-  const int stage = 16384 + p.vboxes * 8192;
-  p.stages = kGBudget / stage < kGMaxS ? kGBudget / stage : kGMaxS;
-  return p;
-}
-
 cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st) {
   a.sh = p.sh;
   a.pieces = p.pieces;
   a.piece = p.piece;
-  a.maxc = p.maxc;
   a.n16 = p.n16;
   a.nbuf = p.nbuf;
   a.vboxes = p.vboxes;

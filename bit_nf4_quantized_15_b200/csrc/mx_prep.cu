@@ -62,13 +62,6 @@ constexpr int kQGroups = 2;  // quantise groups of 8 warps (3 were a few percent
 constexpr int kPrepThreads = (8 + 8 * kQGroups) * 32;
 constexpr uint32_t kSumCol = 256;  // tensor memory: work accumulators at 0 and 128, the sum at 256
 
-// Units [lo, hi) of CTA c.
-__host__ __device__ inline int64_t prep_unit(int64_t units, int grid, int64_t c) { return c * units / grid; }
-// CTA that owns unit u.
-__host__ __device__ inline int prep_owner(int64_t units, int grid, int64_t u) {
-  return (int)(((u + 1) * grid - 1) / units);
-}
-
 // The first bf16 term of v: v rounded toward zero (so it never overflows, and
 // what is left has v's sign), an Inf or NaN as it is.
 QDEV float first_term(float v) {
@@ -274,10 +267,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
       float* dst = nullptr;
       if (last && args.direct) {  // for the cluster, over the tiles of L: all of them have been multiplied
         dst = reinterpret_cast<float*>(smem + C::LT) + (q4 * 32 + lane) * (args.r + 4);
-      } else if (last) {  // this run's rows of D: the slot of (row tile, ordinal of this CTA in it)
+      } else if (last) {  // this run's rows of D
         const int64_t tile = (u_lo + u) / upt;
-        const int ord = (int)blockIdx.x - prep_owner(args.units, (int)gridDim.x, tile * upt);
-        dst = args.part + ((tile * args.maxc + ord) * 128 + q4 * 32 + lane) * args.r;
+        dst = args.part + (mx_slot(tile, blockIdx.x) * 128 + q4 * 32 + lane) * args.r;
       }
       for (int c = 0; c < args.r16; c += 16) {
         uint32_t v[16];
@@ -467,11 +459,11 @@ __global__ void __launch_bounds__(256) mx_prep_finish_kernel(const __grid_consta
   pdl_trigger();
   pdl_wait();
   const int64_t tile = blockIdx.x;
-  const int nc = prep_owner(a.units, a.grid, (tile + 1) * a.units_per_tile - 1) -
-                 prep_owner(a.units, a.grid, tile * a.units_per_tile);
+  const int first = prep_owner(a.units, a.grid, tile * a.units_per_tile);
+  const int nc = prep_owner(a.units, a.grid, (tile + 1) * a.units_per_tile - 1) - first;
   const int64_t left = (a.M - tile * 128) * a.r;
   const int n = (int)(left < 128 * a.r ? left : 128 * a.r);
-  const float* p = a.part + tile * a.maxc * 128 * a.r;
+  const float* p = a.part + mx_slot(tile, first) * 128 * a.r;
   for (int i = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4; i < n; i += (int)gridDim.y * 1024) {
     float4 d = *reinterpret_cast<const float4*>(p + i);
 #pragma unroll 4
@@ -495,37 +487,9 @@ __global__ void __launch_bounds__(256) split3_kernel(const float* __restrict__ i
 
 }  // namespace
 
-// Up to 8 row tiles of up to two units a CTA go to clusters of 8 (16 for up to
-// 4 tiles) that finish their tile alone; the rest is cut into equal runs of
-// units, with a second kernel for what the runs share.  Forward with 1024
-// features, both measured: 1 x 8192 13.6 us on a cluster, 15.1 in runs; 600 x
-// 4096 22.9 and 22.6 (and a launch less); 2000 x 4096 30.2 and 24.7 (16
-// clusters of 8 do not all fit at once).
-MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms) {
-  MxPrepPlan p{};
-  p.units_per_tile = (int)((C + 255) / 256);
-  const int64_t tiles = (M + 127) / 128;
-  p.units = tiles * p.units_per_tile;
-  p.cluster = 1;
-  while (p.cluster < (tiles <= 4 ? 16 : 8) && 2 * p.cluster <= p.units_per_tile) p.cluster *= 2;
-  p.direct = (tiles <= 8 && p.units_per_tile <= 2 * p.cluster) || p.units_per_tile == 1;
-  if (p.direct) {
-    p.grid = (int)(tiles * p.cluster);
-    return p;
-  }
-  p.cluster = 1;
-  p.grid = (int)(p.units < num_sms ? p.units : num_sms);
-  const int64_t per = p.units / p.grid;  // the least units of a CTA
-  p.maxc = (int)((p.units_per_tile + per - 1) / per) + 1;
-  if (p.maxc > p.grid) p.maxc = p.grid;
-  p.part_bytes = (size_t)tiles * p.maxc * 128 * r * sizeof(float);
-  return p;
-}
-
 cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) {
   a.units = p.units;
   a.units_per_tile = p.units_per_tile;
-  a.maxc = p.maxc;
   a.direct = p.direct;
   a.r16 = (a.r + 15) / 16 * 16;
   a.fin.part = a.part;
@@ -533,7 +497,6 @@ cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) 
   a.fin.units = p.units;
   a.fin.units_per_tile = p.units_per_tile;
   a.fin.grid = p.grid;
-  a.fin.maxc = p.maxc;
   const LaunchShape narrow{dim3((unsigned)p.grid), kPrepThreads, PrepCfg<false>::TOTAL, (unsigned)p.cluster, false};
   const LaunchShape wide{dim3((unsigned)p.grid), kPrepThreads, PrepCfg<true>::TOTAL, (unsigned)p.cluster, false};
   const cudaError_t e = a.r > 64 ? launch_kernel<mx_prep_kernel<true>>(wide, st, a)

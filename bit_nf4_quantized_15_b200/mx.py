@@ -226,7 +226,8 @@ def mx_weight(W, backward: bool = True, status=None) -> MXWeight:
 
 
 def mx_linear_workspace_bytes(M: int, N: int, K: int, r: int = 0) -> int:
-    """Workspace of mx_linear_fwd and mx_linear_bwd (the larger of the two)."""
+    """Workspace of mx_linear_fwd and mx_linear_bwd (the larger of the two); it
+    does not fall with M, so one for the largest batch serves smaller ones."""
     n = _q.lib().qlora_mx_linear_workspace_bytes(M, N, K, r)
     if not n:
         _bad("invalid shape or rank for mx_linear_workspace_bytes")

@@ -385,8 +385,9 @@ QLORA_API int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dro
                             qlora_stream_t stream);
 
 /* Workspace bytes of qlora_mx_linear_fwd and qlora_mx_linear_bwd (the maximum
- * of both) for M tokens, an N x K weight and rank r (0: no adapter).  0 for
- * an invalid shape. */
+ * of both) for M tokens, an N x K weight and rank r (0: no adapter).  It does
+ * not fall with M: a workspace for the largest batch serves smaller ones.  0
+ * for an invalid shape. */
 QLORA_API size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
 
 /*

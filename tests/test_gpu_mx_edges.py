@@ -143,3 +143,21 @@ def test_non_finite_operands_of_single_gradients_are_reported(lib, M):
         assert status(T=broken(T, value), **only2) == -7
         assert status(X=broken(X, value), **only1) == -7
         assert status(T=broken(T, value), **only1) == status(X=broken(X, value), **only2) == 0
+
+
+# ------------------------------------------------------------ callers' buffers
+def test_one_workspace_for_the_largest_batch(lib):
+    """A workspace sized for the largest batch serves every smaller one, and
+    what the calls before have left in it changes nothing."""
+    N, K, r = 576, 1056, 64
+    most = 2432
+    X, w, L1, L2, dY, _ = _problem(lib, most, N, K, r, seed=8)
+    ws = torch.full((lib.mx_linear_workspace_bytes(most, N, K, r),), 255, dtype=torch.uint8, device="cuda")
+    for M in (most, 2304, 1100, 300, 40, 1):
+        drop = lib.Dropout(0.2, M)
+        Y, T = lib.mx_linear_fwd(X[:M], w, L1, L2, 0.5, dropout=drop)
+        ref = (Y, T) + lib.mx_linear_bwd(dY[:M], X[:M], T, w, L1, L2, 0.5, dropout=drop)
+        Y, T = lib.mx_linear_fwd(X[:M], w, L1, L2, 0.5, dropout=drop, ws=ws)
+        got = (Y, T) + lib.mx_linear_bwd(dY[:M], X[:M], T, w, L1, L2, 0.5, dropout=drop, ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(ref, got)), M
+    assert lib.read_status() == 0

@@ -3,6 +3,9 @@ and every refusal before a device is touched.  The pointers are fake and never
 dereferenced; a launch with them would fault."""
 
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -127,3 +130,26 @@ def test_binding_refuses_what_is_not_a_cuda_tensor(q):
     for p, seed, off in ((0.1, -1, 0), (0.1, 0, -1), (0.1, 1 << 64, 0)):
         with pytest.raises(q.QLoRAError):
             q.Dropout(p, seed, off).config(X.device)
+
+
+def test_workspace_never_falls_with_the_tokens(q):
+    """One buffer for the largest batch serves the smaller ones."""
+    n = q.mx_linear_workspace_bytes
+    for N, K, r in ((4096, 4096, 64), (1024, 1024, 128), (64, 22016, 8), (22016, 8192, 16), (96, 64, 128), (4096, 64, 0)):
+        sizes = [n(M, N, K, r) for M in [*range(1, 4097), *range(4097, 20000, 61)]]
+        falls = [i + 1 for i in range(len(sizes) - 1) if sizes[i + 1] < sizes[i]]
+        assert not falls, (N, K, r, falls[:5])
+
+
+def test_units_runs_and_slots(tmp_path):
+    """The kernels' shares of the work, replayed on the host."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "mx_plan_check")
+    subprocess.run([cxx, "-O2", "-std=c++17", "-I", os.path.join(root, "bit_nf4_quantized_15_b200", "csrc"),
+                    os.path.join(root, "tests", "mx_plan_check.cpp"), "-o", exe], check=True, capture_output=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stdout
+    assert int(out.stdout.split("plans=")[1].split()[0]) > 20000
