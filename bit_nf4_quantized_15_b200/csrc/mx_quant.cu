@@ -29,12 +29,13 @@ constexpr int kQT = 256;  // threads of the element kernels
 template <int DT>
 constexpr int kWords = DT == QLORA_DTYPE_F32 ? 8 : 4;  // 32-bit words of eight elements
 
-// Eight consecutive elements as they are stored.
-template <int DT>
+// Eight consecutive elements as they are stored.  CONST: nothing writes them
+// while the kernel runs, so they may come through the read-only path.
+template <int DT, bool CONST>
 QDEV void load8(const uint4* p, uint32_t* w) {
 #pragma unroll
   for (int j = 0; j < kWords<DT>; j += 4) {
-    const uint4 r = __ldg(p + j / 4);
+    const uint4 r = CONST ? __ldg(p + j / 4) : p[j / 4];
     w[j] = r.x, w[j + 1] = r.y, w[j + 2] = r.z, w[j + 3] = r.w;
   }
 }
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kQT) mx_quantize_kernel(const void* __restrict
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       if (rl0 + 16 * (p + i) < n) {
-        load8<DT>(px + (p + i) * step * (kW / 4), w[i]);
+        load8<DT, true>(px + (p + i) * step * (kW / 4), w[i]);
       } else {
 #pragma unroll
         for (int j = 0; j < kW; ++j) w[i][j] = 0u;
@@ -346,10 +347,10 @@ QDEV void drop_store8(void* out, int64_t i, uint32_t* w, const uint4& rnd, const
 // out = x inv where kept, else 0.  Eight elements (one generator evaluation) a
 // thread and turn; a step has two turns with their loads in flight.  Bound by
 // HBM: 8192 x 8192 bf16, 268 MB, 46 us (5.8 TB/s), fp32 87 us (6.2 TB/s; with
-// one turn 93); a copy of the bf16 tensor takes 42.
+// one turn 93); a copy of the bf16 tensor takes 42.  out may be X: a thread
+// reads what it writes, by ordinary loads.
 template <int DT>
-__global__ void __launch_bounds__(kQT) dropout_kernel(const void* __restrict__ X, int64_t n, DropArgs d,
-                                                      void* __restrict__ out) {
+__global__ void __launch_bounds__(kQT) dropout_kernel(const void* X, int64_t n, DropArgs d, void* out) {
   constexpr int kTurns = 2;
   const PhiloxKey key = philox_key(d);
   const int64_t n8 = n / 8, stride = (int64_t)gridDim.x * kQT;
@@ -357,7 +358,8 @@ __global__ void __launch_bounds__(kQT) dropout_kernel(const void* __restrict__ X
     uint32_t w[kTurns][kWords<DT>];
 #pragma unroll
     for (int k = 0; k < kTurns; ++k)
-      if (i + k * stride < n8) load8<DT>(reinterpret_cast<const uint4*>(X) + (i + k * stride) * (kWords<DT> / 4), w[k]);
+      if (i + k * stride < n8)
+        load8<DT, false>(reinterpret_cast<const uint4*>(X) + (i + k * stride) * (kWords<DT> / 4), w[k]);
 #pragma unroll
     for (int k = 0; k < kTurns; ++k)
       if (i + k * stride < n8)

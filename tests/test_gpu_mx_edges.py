@@ -161,3 +161,12 @@ def test_one_workspace_for_the_largest_batch(lib):
         got = (Y, T) + lib.mx_linear_bwd(dY[:M], X[:M], T, w, L1, L2, 0.5, dropout=drop, ws=ws)
         assert all(torch.equal(a, b) for a, b in zip(ref, got)), M
     assert lib.read_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_dropout_in_place_over_many_turns(lib, dtype):
+    """out = X where every thread takes several groups of eight, and a tail."""
+    X = torch.randn((1 << 24) + 13, generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(dtype)
+    out = lib.dropout(X, 0.3, 7, 1)
+    assert lib.dropout(X, 0.3, 7, 1, out=X) is X
+    assert torch.equal(X, out)
