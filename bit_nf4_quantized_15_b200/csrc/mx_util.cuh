@@ -6,11 +6,10 @@
 namespace qnf4 {
 namespace {
 
-// Cluster barrier in two halves, by converged warps, where only reads of the
-// peers come before: the values must be there (reads_done), but nothing has
-// to be made visible, which costs a release some 1000 cycles.
-QDEV void reads_done(float4 v) { asm volatile("" ::"f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory"); }
-QDEV void cluster_arrive_read() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+// Cluster barrier in two halves, by converged warps.  The arrival is a release:
+// it orders the reads of the peers' shared memory before it, so that a peer
+// that leaves after its wait gives up nothing that is still being read.
+QDEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 QDEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 constexpr int kMxKB = 256;  // reduction elements of a stage: 128 bytes of codes

@@ -170,3 +170,19 @@ def test_dropout_in_place_over_many_turns(lib, dtype):
     out = lib.dropout(X, 0.3, 7, 1)
     assert lib.dropout(X, 0.3, 7, 1, out=X) is X
     assert torch.equal(X, out)
+
+
+# ---------------------------------------------------------------- repetitions
+@pytest.mark.parametrize("M,N,K,r", [(1, 4096, 8192, 16), (300, 1024, 4128, 128), (1000, 2080, 4096, 64)])
+def test_cluster_sums_repeat_bit_for_bit(lib, M, N, K, r):
+    """Many calls back to back, whose clusters start as those before leave:
+    every one gives the first one's bits."""
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=5)
+    ref = lib.mx_linear_fwd(X, w, L1, L2, 1.0)
+    ref += lib.mx_linear_bwd(dY, X, ref[1], w, L1, L2, 1.0)
+    runs = []
+    for _ in range(100):
+        Y, T = lib.mx_linear_fwd(X, w, L1, L2, 1.0)
+        runs.append((Y, T) + lib.mx_linear_bwd(dY, X, T, w, L1, L2, 1.0))
+    assert all(torch.equal(a, b) for run in runs for a, b in zip(ref, run))
+    assert lib.read_status() == 0
