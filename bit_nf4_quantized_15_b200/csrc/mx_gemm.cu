@@ -285,15 +285,17 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
         for (int j = 0; j < 16; ++j) red[j * 128] = __uint_as_float(v[j]);
         continue;
       }
-      if (!ok || *abort_flag || row >= args.rows) continue;
-      const int ncol = min(16, args.cols - (col0 + c));
-      const int64_t o = (int64_t)(col0 + c) * args.ldo + row;
+      if (ok && !*abort_flag && row < args.rows) {
+        const int ncol = min(16, args.cols - (col0 + c));
+        const int64_t o = (int64_t)(col0 + c) * args.ldo + row;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (j >= ncol) continue;
-        if (args.out_f32) reinterpret_cast<float*>(args.out)[o + j * args.ldo] = __uint_as_float(v[j]);
-        else reinterpret_cast<__nv_bfloat16*>(args.out)[o + j * args.ldo] = __float2bfloat16_rn(__uint_as_float(v[j]));
+        for (int j = 0; j < 16; ++j) {
+          if (j >= ncol) continue;
+          if (args.out_f32) reinterpret_cast<float*>(args.out)[o + j * args.ldo] = __uint_as_float(v[j]);
+          else reinterpret_cast<__nv_bfloat16*>(args.out)[o + j * args.ldo] = __float2bfloat16_rn(__uint_as_float(v[j]));
+        }
       }
+      __syncwarp();  // the next load takes the whole warp
     }
   }
 

@@ -329,14 +329,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
           uint32_t v[16];
           tmem_ld16(tl + (uint32_t)c, v);
           tmem_wait_ld();
-          if (row >= args.rows) continue;
+          if (row < args.rows) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            if (col + c + j < args.cols)
-              *reinterpret_cast<uint4*>(dst + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            for (int j = 0; j < 16; j += 4)
+              if (col + c + j < args.cols)
+                *reinterpret_cast<uint4*>(dst + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          }
+          __syncwarp();  // the next load takes the whole warp
         }
         tc_fence_before();
-        __syncwarp();
         if (lane == 0) mbar_arrive_cluster(drained0);
       } else {
         uint32_t v[8][16];  // the whole row half, loads all in flight; packed once the accumulator is released

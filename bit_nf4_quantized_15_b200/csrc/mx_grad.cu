@@ -235,13 +235,12 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
         if (!x.last) {
           tmem_st16(tl + sum_col + (uint32_t)c, v);
         } else if (whole) {  // this CTA has the whole sum
-          if (col >= cols) continue;
-          if (transposed) {
+          if (col < cols && transposed) {
             float* at = out + c * cols + col;
 #pragma unroll
             for (int j = 0; j < 16; ++j, at += cols)
               if (c + j < r) *at = __uint_as_float(v[j]);
-          } else {
+          } else if (col < cols) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
               if (c + j < r)
@@ -258,6 +257,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_grad_kernel(const __grid_cons
               *reinterpret_cast<uint4*>(slot + (int64_t)row * r + c + j) =
                   make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
+        __syncwarp();  // the next load takes the whole warp
       }
       tmem_wait_st();
       tc_fence_before();

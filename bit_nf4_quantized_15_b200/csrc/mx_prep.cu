@@ -438,11 +438,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) mx_prep_kernel(const __grid_c
           d = make_float4(__fadd_rn(d.x, q.x), __fadd_rn(d.y, q.y), __fadd_rn(d.z, q.z), __fadd_rn(d.w, q.w));
         }
       }
-      __syncwarp();
       if (i0 + kPrepThreads >= n) cluster_arrive();  // the last rows are read
       if (mine) emit4(f, row, j, d);
     }
-    __syncwarp();
     cluster_wait();  // peers may still be reading this CTA's rows
   }
   if (warp == 1) {

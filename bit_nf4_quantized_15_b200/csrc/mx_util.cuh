@@ -6,11 +6,17 @@
 namespace qnf4 {
 namespace {
 
-// Cluster barrier in two halves, by converged warps.  The arrival is a release:
+// Cluster barrier in two halves, by whole warps (the lanes meet first).  The arrival is a release:
 // it orders the reads of the peers' shared memory before it, so that a peer
 // that leaves after its wait gives up nothing that is still being read.
-QDEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-QDEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+QDEV void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+QDEV void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 constexpr int kMxKB = 256;  // reduction elements of a stage: 128 bytes of codes
 

@@ -42,7 +42,9 @@ QDEV float4 ld_peer_f4(uint32_t addr, uint32_t rank) {
                : "memory");
   return v;
 }
+// By whole warps: the barrier is .aligned, so the lanes meet first.
 QDEV void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 QDEV void mbar_arrive_cluster(uint32_t cluster_addr) {
