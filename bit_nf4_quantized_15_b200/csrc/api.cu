@@ -175,15 +175,16 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Diagnostic events around the fused dequant-GEMM (qlora_set_gemm_events).
 cudaEvent_t g_ev_start = nullptr, g_ev_end = nullptr;
-// Failure-detection hook (qlora_debug_stall_next_gemm): wait bound of the
-// next fused dequant-GEMM launch, whose producer then issues no loads.
-uint64_t g_stall_ns = 0;
+// Failure-detection hook (qlora_debug_stall_next_gemm): wait bound of this
+// thread's next fused dequant-GEMM or MXFP4 product launch, whose producer then
+// issues no loads.  One for each thread, so that calls on several neither race
+// for it nor take each other's.
+thread_local uint64_t t_stall_ns = 0;
 
 int run_timed(EngineArgs& a, int amode, const GemmPlan& p, float* partial, cudaStream_t st) {
   cudaEvent_t e0 = g_ev_start, e1 = g_ev_end;
   g_ev_start = g_ev_end = nullptr;
-  const uint64_t stall_ns = g_stall_ns;
-  g_stall_ns = 0;
+  const uint64_t stall_ns = take_stall_request();
   if (stall_ns && amode != A_PAIR_K) {
     a.stall = 1;
     a.wait_ns = stall_ns;
@@ -242,8 +243,8 @@ bool shape_ok(int64_t M, int64_t N, int64_t K) {
 }  // namespace
 
 uint64_t qnf4::take_stall_request() {
-  const uint64_t ns = g_stall_ns;
-  g_stall_ns = 0;
+  const uint64_t ns = t_stall_ns;
+  t_stall_ns = 0;
   return ns;
 }
 
@@ -291,7 +292,7 @@ int qlora_nf4_storage_bytes(int64_t N, int64_t K, size_t* codes_bytes, size_t* c
 uint64_t qlora_kernel_launches(void) { return launches_so_far(); }
 
 int qlora_debug_stall_next_gemm(uint64_t wait_ns) {
-  g_stall_ns = wait_ns;
+  t_stall_ns = wait_ns;
   return QLORA_OK;
 }
 
@@ -587,7 +588,7 @@ int qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const flo
     for (int i = 0; i < 16; ++i) ga.q[i] = tb.q[i];
     cudaEvent_t e0 = g_ev_start, e1 = g_ev_end;
     g_ev_start = g_ev_end = nullptr;
-    g_stall_ns = 0;
+    take_stall_request();
     if (e0 && cudaEventRecord(e0, st) != cudaSuccess) return QLORA_ERR_CUDA;
     if (launch_gemv_t(ga, gp, dY, L2, T_saved, dL2, st) != cudaSuccess) return QLORA_ERR_CUDA;
     if (e1 && cudaEventRecord(e1, st) != cudaSuccess) return QLORA_ERR_CUDA;

@@ -26,7 +26,7 @@ int make_map3(CUtensorMap* m, const void* base, uint64_t n0, uint64_t n1, uint64
 // bf16 operand of the engines.  K-major: matrix [mn][k] (k contiguous), box
 // 64 k x `rows` mn.  MN-major: matrix [k][mn] (mn contiguous), box 64 x 64.
 int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows);
-// Takes the pending request of qlora_debug_stall_next_gemm (0: none).
+// Takes this thread's pending request of qlora_debug_stall_next_gemm (0: none).
 uint64_t take_stall_request();
 
 // NF4 codebook and decision thresholds as the kernels use them.

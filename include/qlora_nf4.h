@@ -445,8 +445,8 @@ QLORA_API int qlora_set_gemm_events(void* ev_start, void* ev_end);
  * instead of 4 s.  Its waits then expire: the kernel writes
  * QLORA_ERR_TIMEOUT to *status_dev, frees its tensor memory and returns
  * with nothing in flight, so the context stays usable; that call's outputs
- * are unspecified.  One-shot and process-wide, not thread-safe; 0 cancels a
- * pending request. */
+ * are unspecified.  One-shot; the next launch of the calling host thread is
+ * meant, calls on other threads are unaffected.  0 cancels a pending request. */
 QLORA_API int qlora_debug_stall_next_gemm(uint64_t wait_ns);
 
 /* Number of kernels this process has launched through the library so far

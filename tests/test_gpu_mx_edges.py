@@ -5,6 +5,8 @@ paths that long reductions take, buffers that the caller gives.
 Bounds as in test_gpu_mx.py: half a bf16 step of a bf16 result, and one unit
 lost to truncation a step of the tensor cores' fp32 sums."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -186,3 +188,25 @@ def test_cluster_sums_repeat_bit_for_bit(lib, M, N, K, r):
         runs.append((Y, T) + lib.mx_linear_bwd(dY, X, T, w, L1, L2, 1.0))
     assert all(torch.equal(a, b) for run in runs for a, b in zip(ref, run))
     assert lib.read_status() == 0
+
+
+def test_stall_request_belongs_to_its_thread(lib):
+    """A request armed on one host thread is not taken by another's product."""
+    a, b = (lib.mx_quantize(torch.randn((n, 512), device="cuda")) for n in (40, 200))
+    ref = lib.mx_matmul(a, b)
+    torch.cuda.synchronize()
+    other = []
+
+    def elsewhere():
+        out = lib.mx_matmul(a, b)
+        torch.cuda.synchronize()
+        other.append((lib.read_status(), torch.equal(out, ref)))
+
+    lib.debug_stall_next_gemm(5_000_000)
+    t = threading.Thread(target=elsewhere)
+    t.start()
+    t.join()
+    assert other == [(0, True)]
+    lib.mx_matmul(a, b)
+    assert lib.read_status() == -8
+    assert torch.equal(lib.mx_matmul(a, b), ref) and lib.read_status() == 0
