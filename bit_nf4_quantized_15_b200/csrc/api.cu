@@ -18,6 +18,13 @@ namespace qnf4 {
 int current_device_info(DevInfo* out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QLORA_ERR_CUDA;
+  // The tensor maps are encoded by the driver, which wants a current context;
+  // a host thread has none until the runtime has given it the device's.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return QLORA_ERR_CUDA;
+    bound = dev;
+  }
   static DevInfo cache[64];
   static std::mutex mu;
   std::lock_guard<std::mutex> g(mu);

@@ -210,3 +210,32 @@ def test_stall_request_belongs_to_its_thread(lib):
     lib.mx_matmul(a, b)
     assert lib.read_status() == -8
     assert torch.equal(lib.mx_matmul(a, b), ref) and lib.read_status() == 0
+
+
+def test_first_cuda_call_of_a_host_thread(lib):
+    """A thread whose first CUDA work is one of the calls."""
+    M, N, K, r = 40, 128, 256, 16
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=6)
+    nf4 = lib.quantize(torch.randn((N, K), device="cuda").bfloat16())
+
+    def step(i):
+        if i == 0:
+            Y, T = lib.mx_linear_fwd(X, w, L1, L2, 0.5)
+            return (Y, T) + lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5)
+        if i == 1:
+            return (lib.mx_matmul(lib.mx_quantize(X, transpose=False), w.fwd),)
+        if i == 2:
+            return (lib.mx_quantize(L2.t().contiguous(), transpose=True).codes,)
+        Y, T = lib.linear_fwd(X, nf4, L1, L2, 0.5)
+        return (Y, T) + lib.linear_bwd(dY, X, T, nf4, L1, L2, 0.5)
+
+    ref = [step(i) for i in range(4)]
+    torch.cuda.synchronize()
+    got = {}
+    for i in range(4):
+        t = threading.Thread(target=lambda: got.__setitem__(i, step(i)))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert sorted(got) == [0, 1, 2, 3]
+    assert all(torch.equal(a, b) for i in range(4) for a, b in zip(ref[i], got[i]))
