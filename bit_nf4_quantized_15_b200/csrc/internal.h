@@ -356,6 +356,7 @@ struct MxPrepArgs {
   DropArgs drop;
   int* status;
 };
+int mx_prep_max_cluster();
 cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st);
 
 // Adapter gradients (mx_grad.cu): problem 0 is dL1 = drop(X)^T.u, problem 1

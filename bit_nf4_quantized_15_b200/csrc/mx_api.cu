@@ -181,7 +181,7 @@ struct MxWs {
   MxPrepPlan prep_x, prep_dy;
 };
 
-MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms) {
+MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms, int max_cluster) {
   MxWs w{};
   const size_t qk = up256(codes_bytes(M, K)), qn = up256(codes_bytes(M, N));
   w.q_scales = qk > qn ? qk : qn;
@@ -195,8 +195,8 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms) {
     w.keep = o;
     o += up256((size_t)M * ((K + 127) / 128) * 16);
     w.part = o;
-    w.prep_x = plan_mx_prep(M, K, r, sms);
-    w.prep_dy = plan_mx_prep(M, N, r, sms);
+    w.prep_x = plan_mx_prep(M, K, r, sms, max_cluster);
+    w.prep_dy = plan_mx_prep(M, N, r, sms, max_cluster);
     o += up256(std::max({w.prep_x.part_bytes, w.prep_dy.part_bytes, mx_grad_part_bound(M, K, N, r, sms)}));
   }
   w.total = o;
@@ -276,8 +276,8 @@ int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_confi
 size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
   if (!linear_shape_ok(M, N, K, 8) || !rank_ok(r)) return 0;
   DevInfo di;
-  if (current_device_info(&di)) di.sms = 148;
-  return mx_ws(M, N, K, r, di.sms).total;
+  const bool gpu = current_device_info(&di) == QLORA_OK;
+  return mx_ws(M, N, K, r, gpu ? di.sms : 148, gpu ? mx_prep_max_cluster() : 16).total;
 }
 
 int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, const uint16_t* L1,
@@ -293,7 +293,7 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
   if (!all16({X, w->codes, w->scales, L1, L2, Y, T_save, ws})) return QLORA_ERR_ALIGN;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  const MxWs lay = mx_ws(M, N, K, r, di.sms);
+  const MxWs lay = mx_ws(M, N, K, r, di.sms, mx_prep_max_cluster());
   if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* wb = static_cast<uint8_t*>(ws);
@@ -335,7 +335,7 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   if (dX && !all16({wt->codes, wt->scales})) return QLORA_ERR_ALIGN;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  const MxWs lay = mx_ws(M, N, K, r, di.sms);
+  const MxWs lay = mx_ws(M, N, K, r, di.sms, mx_prep_max_cluster());
   if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* wb = static_cast<uint8_t*>(ws);

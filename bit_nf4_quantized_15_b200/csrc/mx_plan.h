@@ -44,14 +44,15 @@ QPLAN int prep_owner(int64_t units, int grid, int64_t u) { return (int)(((u + 1)
 // is cut into equal runs of units, with a second kernel for what the runs
 // share.  Forward with 1024 features, both measured: 1 x 8192 13.6 us on a
 // cluster, 15.1 in runs; 600 x 4096 22.9 and 22.6 (and a launch less); 2000 x
-// 4096 30.2 and 24.7 (16 clusters of 8 do not all fit at once).
-inline MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms) {
+// 4096 30.2 and 24.7 (16 clusters of 8 do not all fit at once).  max_cluster: 16,
+// or 8 on a device (a partition of one) that has no room for one of 16.
+inline MxPrepPlan plan_mx_prep(int64_t M, int64_t C, int r, int num_sms, int max_cluster) {
   MxPrepPlan p{};
   p.units_per_tile = (int)((C + 255) / 256);
   const int64_t tiles = (M + 127) / 128;
   p.units = tiles * p.units_per_tile;
   p.cluster = 1;
-  while (p.cluster < (tiles <= 4 ? 16 : 8) && 2 * p.cluster <= p.units_per_tile) p.cluster *= 2;
+  while (p.cluster < (tiles <= 4 ? max_cluster : 8) && 2 * p.cluster <= p.units_per_tile) p.cluster *= 2;
   p.direct = (tiles <= 8 && p.units_per_tile <= 2 * p.cluster) || p.units_per_tile == 1;
   if (p.direct) {
     p.grid = (int)(tiles * p.cluster);

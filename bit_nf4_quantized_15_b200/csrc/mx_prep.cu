@@ -484,6 +484,33 @@ __global__ void __launch_bounds__(256) split3_kernel(const float* __restrict__ i
 
 }  // namespace
 
+// Largest cluster that the current device can hold: 16, else the portable 8.
+int mx_prep_max_cluster() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 8;
+  int most = known[dev].load(std::memory_order_relaxed);
+  if (most) return most;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 16;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kPrepThreads);
+  cfg.dynamicSmemBytes = std::max(PrepCfg<true>::TOTAL, PrepCfg<false>::TOTAL);
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  most = allow_big<mx_prep_kernel<true>>(false) == cudaSuccess &&
+                 cudaOccupancyMaxActiveClusters(&clusters, mx_prep_kernel<true>, &cfg) == cudaSuccess && clusters > 0
+             ? 16
+             : 8;
+  (void)cudaGetLastError();
+  known[dev].store(most, std::memory_order_relaxed);
+  return most;
+}
+
 cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) {
   a.units = p.units;
   a.units_per_tile = p.units_per_tile;

@@ -49,19 +49,20 @@ int main() {
   for (int i = 0; i < 20000; ++i) {
     const int64_t M = log_rand(1, 9000), C = log_rand(1, 900) * 32, N = log_rand(1, 900) * 32;
     const int r = 8 * (1 + std::rand() % 16), sms = std::rand() % 4 ? 148 : 1 + std::rand() % 160;
-    const MxPrepPlan p = plan_mx_prep(M, C, r, sms);
+    const int most = std::rand() % 2 ? 16 : 8;  // largest cluster of the device
+    const MxPrepPlan p = plan_mx_prep(M, C, r, sms, most);
     const int64_t tiles = (M + 127) / 128;
     NEED(p.units == tiles * ((C + 255) / 256) && p.grid >= 1);
     if (p.direct) {
       NEED(p.grid == tiles * p.cluster && p.part_bytes == 0);
-      NEED(p.cluster <= p.units_per_tile && 128 % p.cluster == 0);
+      NEED(p.cluster <= most && p.cluster <= p.units_per_tile && 128 % p.cluster == 0);
     } else {
       NEED(p.grid <= sms && p.cluster == 1);
       check_slots(p.units, p.units_per_tile, p.grid, p.part_bytes, r,
                   [&](int64_t c) { return prep_unit(p.units, p.grid, c); },
                   [&](int64_t u) { return prep_owner(p.units, p.grid, u); });
     }
-    NEED(plan_mx_prep(M + 1 + std::rand() % 300, C, r, sms).part_bytes >= p.part_bytes);
+    NEED(plan_mx_prep(M + 1 + std::rand() % 300, C, r, sms, most).part_bytes >= p.part_bytes);
     for (int k = 0; k < 9; ++k) {
       const int64_t c0 = k % 3 == 2 ? 0 : C, c1 = k % 3 == 1 ? 0 : N;
       const MxGradPlan g = plan_mx_grad(M, c0, c1, r, (MxGradMask)(k / 3), sms);
