@@ -273,6 +273,7 @@ const char* qlora_status_string(int code) {
     case QLORA_ERR_SCRATCH_LIMIT: return "problem needs more workspace than the library's 8 MiB static scratch";
     case QLORA_ERR_DTYPE: return "unknown or unsupported element type (QLORA_DTYPE_*)";
     case QLORA_ERR_DROPOUT: return "dropout probability outside [0, 1)";
+    case QLORA_ERR_OVERLAP: return "an output overlaps an input that is read after it is written";
     case QLORA_ERR_MX_SHAPE:
       return "invalid MXFP4 shape (need a block axis that is a multiple of 32, other axes a multiple of 8 where "
              "they are contiguous, equal reduction lengths)";

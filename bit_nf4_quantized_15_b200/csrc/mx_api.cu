@@ -17,6 +17,10 @@ bool all16(std::initializer_list<const void*> ps) {
     if (!ok16(p)) return false;
   return true;
 }
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int64_t kMaxDim = 1 << 24;
@@ -266,6 +270,8 @@ int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_confi
   DropArgs d;
   if (int rc = drop_args(cfg, &d)) return rc;
   if (!all16({X, out})) return QLORA_ERR_ALIGN;
+  const size_t bytes = (size_t)n * (dtype == QLORA_DTYPE_F32 ? 4 : 2);
+  if (out != X && overlap(X, bytes, out, bytes)) return QLORA_ERR_OVERLAP;
   if (n == 0) return QLORA_OK;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
@@ -333,6 +339,9 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   if (int rc = drop_args(drop, &d)) return rc;
   if (!all16({dY, X, T_saved, L1, L2, dX, dL1, dL2, ws})) return QLORA_ERR_ALIGN;
   if (dX && !all16({wt->codes, wt->scales})) return QLORA_ERR_ALIGN;
+  // dX is written before the adapter gradients read X and dY
+  const size_t mk = (size_t)M * K * 2, mn = (size_t)M * N * 2;
+  if (dX && ((dL1 && overlap(dX, mk, X, mk)) || (dL2 && overlap(dX, mk, dY, mn)))) return QLORA_ERR_OVERLAP;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
   const MxWs lay = mx_ws(M, N, K, r, di.sms, mx_prep_max_cluster());

@@ -291,7 +291,8 @@ def mx_linear_bwd(dY, X, T, w: MXWeight, L1=None, L2=None, s: float = 1.0, dropo
                   need_dX=True, need_dL1=True, need_dL2=True, status=None, dX=None, dL1=None, dL2=None):
     """dX = Q(dY).W + drop(s.dT.L1^T), dL1 = s.drop(X)^T.dT, dL2 = s.T^T.dY
     with dT = dY.L2^T; ``dropout`` names the forward's mask.  Without an
-    adapter: dX alone.  dX needs ``w.bwd``."""
+    adapter: dX alone.  dX needs ``w.bwd``; it must not share memory with X
+    where dL1 is asked for, nor with dY where dL2 is."""
     _matrix(dY, "dY", (torch.bfloat16,))
     M, N = dY.shape
     dev, K = dY.device, w.fwd.cols
@@ -330,7 +331,8 @@ def dropout(X, p: float, seed: int, offset=0, out=None) -> torch.Tensor:
     """X with elements zeroed with probability p and the others scaled by
     1 / (1 - p) (p in steps of 2^-16), the mask named by (seed, offset) and
     never stored; the gradient is the same call on the upstream gradient.
-    X: contiguous bf16, fp16 or fp32 CUDA tensor of any shape; out may be X."""
+    X: contiguous bf16, fp16 or fp32 CUDA tensor of any shape; out may be X,
+    but not overlap it otherwise."""
     if not (isinstance(X, torch.Tensor) and X.is_cuda and X.dtype in DTYPES and X.is_contiguous()):
         _bad("X must be a contiguous bfloat16, float16 or float32 CUDA tensor")
     dev = X.device

@@ -62,7 +62,8 @@ enum {
   QLORA_ERR_FORMAT = -11,       /* unknown code format or scale codec */
   QLORA_ERR_DTYPE = -12,        /* unknown or unsupported element type */
   QLORA_ERR_DROPOUT = -13,      /* dropout probability outside [0, 1) */
-  QLORA_ERR_MX_SHAPE = -14      /* invalid MXFP4 shape */
+  QLORA_ERR_MX_SHAPE = -14,     /* invalid MXFP4 shape */
+  QLORA_ERR_OVERLAP = -15       /* an output overlaps an input that is read after it is written */
 };
 
 /*
@@ -379,8 +380,9 @@ typedef struct qlora_dropout_config {
   const uint64_t* offset_dev;
 } qlora_dropout_config;
 
-/* out[n] = dropout(X[n]), any QLORA_DTYPE_*; out may be X.  The gradient is
- * the same call on the upstream gradient. */
+/* out[n] = dropout(X[n]), any QLORA_DTYPE_*; out may be X, but not overlap it
+ * otherwise (QLORA_ERR_OVERLAP).  The gradient is the same call on the
+ * upstream gradient. */
 QLORA_API int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_config* cfg, void* out,
                             qlora_stream_t stream);
 
@@ -422,6 +424,8 @@ QLORA_API int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_t
  * the dY gives NaN in its row of dX.
  * In dL1 and dL2 an infinite X, dT, T or dY gives what the formula gives: an
  * infinity, or NaN where infinities cancel or meet a zero (a dropped X is 0).
+ * dX is written before dL1 reads X and dL2 reads dY: it must not overlap an
+ * operand of a gradient that is asked for (QLORA_ERR_OVERLAP).
  */
 QLORA_API int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const float* T_saved,
                                   const qlora_mx_tensor* wt, int64_t N, int64_t K, const uint16_t* L1,

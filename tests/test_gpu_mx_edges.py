@@ -239,3 +239,28 @@ def test_first_cuda_call_of_a_host_thread(lib):
     torch.cuda.synchronize()
     assert sorted(got) == [0, 1, 2, 3]
     assert all(torch.equal(a, b) for i in range(4) for a, b in zip(ref[i], got[i]))
+
+
+def test_outputs_over_inputs_that_are_no_longer_read(lib):
+    """Y over X, dX over X without dL1 and over dY without dL2 give the bits of
+    separate buffers; where the operand is still read the call is refused."""
+    M, N, r = 300, 544, 32
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, N, r, seed=14)
+    drop = lib.Dropout(0.1, 5)
+    Y, T = lib.mx_linear_fwd(X, w, L1, L2, 0.5, dropout=drop)
+    dX, dL1, dL2 = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop)
+
+    def bwd(over, **need):
+        g, x = dY.clone(), X.clone()
+        return lib.mx_linear_bwd(g, x, T, w, L1, L2, 0.5, dropout=drop, dX=x if over == "X" else g, **need)
+
+    a, _, b = bwd("X", need_dL1=False)
+    assert torch.equal(a, dX) and torch.equal(b, dL2)
+    a, b, _ = bwd("dY", need_dL2=False)
+    assert torch.equal(a, dX) and torch.equal(b, dL1)
+    for over in ("X", "dY"):
+        with pytest.raises(lib.QLoRAError):
+            bwd(over)
+    x = X.clone()
+    assert torch.equal(lib.mx_linear_fwd(x, w, L1, L2, 0.5, dropout=drop, Y=x)[0], Y)
+    assert torch.equal(x, Y)

@@ -13,6 +13,7 @@ import torch
 P = ctypes.c_void_p
 FAKE, ODD = P(0x10000), P(0x10008)
 NULL, ALIGN, SHAPE, RANK, WORKSPACE, DTYPE, DROPOUT, MX_SHAPE = -1, -2, -3, -4, -5, -12, -13, -14
+OVERLAP = -15
 
 
 @pytest.fixture(scope="module")
@@ -153,3 +154,24 @@ def test_units_runs_and_slots(tmp_path):
     out = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert out.returncode == 0, out.stdout
     assert int(out.stdout.split("plans=")[1].split()[0]) > 20000
+
+
+def test_overlapping_outputs_are_refused(q):
+    """dX over an operand that a later gradient reads; dropout over a part of
+    its input."""
+    L = q.lib()
+    M, N, K = 4, 32, 64
+    p = lambda at: P(0x100000 + at)  # noqa: E731
+
+    def bwd(dX, dL1=p(0x5000), dL2=p(0x6000)):
+        return L.qlora_mx_linear_bwd(p(0), p(0x1000), M, p(0x2000), _t(q, K, N), N, K, p(0x3000), p(0x4000), 16, 1.0,
+                                     None, dX, dL1, dL2, p(0x8000), 1 << 40, None, None)
+
+    for at in (0x1000, 0x1000 + 2 * M * K - 16, 0x1000 - 2 * M * K + 16):   # X: all of it, its end, its start
+        assert bwd(p(at)) == bwd(p(at), dL2=None) == OVERLAP
+    assert bwd(p(0)) == bwd(p(0), dL1=None) == bwd(p(2 * M * N - 16)) == OVERLAP    # dY
+    for n, dtype, size in ((64, 0, 2), (64, 1, 2), (64, 2, 4)):
+        for step in (16, size * n - 16):
+            assert L.qlora_dropout(p(0x400), dtype, n, _d(q), p(0x400 + step), None) == OVERLAP
+            assert L.qlora_dropout(p(0x400), dtype, n, _d(q), p(0x400 - step), None) == OVERLAP
+    assert b"overlap" in L.qlora_status_string(OVERLAP)
