@@ -121,7 +121,9 @@ class MXTensor:
 
     @staticmethod
     def empty(rows: int, cols: int, device="cuda") -> "MXTensor":
-        nc, ns = mx_storage_bytes(rows, cols)
+        nc, ns = mx_storage_bytes(rows or 1, cols)
+        if rows == 0:
+            nc = ns = 0
         return MXTensor(torch.empty(nc, dtype=torch.uint8, device=device),
                         torch.empty(ns, dtype=torch.uint8, device=device), rows, cols)
 
@@ -171,7 +173,7 @@ class Dropout:
 def mx_quantize(X, transpose: bool = False, out: MXTensor | None = None, status=None) -> MXTensor:
     """MXFP4 form of a bf16, fp16 or fp32 CUDA matrix [R, C], blocks of 32
     along its rows (C % 32 == 0); ``transpose``: of X^T, [C, R] (R % 32 == 0,
-    C % 8 == 0)."""
+    C % 8 == 0).  A matrix without rows has an empty form."""
     _matrix(X, "X", DTYPES)
     R, C = X.shape
     shape = (C, R) if transpose else (R, C)
@@ -180,6 +182,8 @@ def mx_quantize(X, transpose: bool = False, out: MXTensor | None = None, status=
     if (out.rows, out.cols) != shape or out.device != X.device:
         _bad(f"out must be {shape[0]} x {shape[1]} on {X.device}")
     d = out.descriptor()
+    if out.rows == 0:
+        return out
     _call(X.device, _q.lib().qlora_mx_quantize, X.data_ptr(), DTYPES[X.dtype], R, C, int(transpose), ctypes.byref(d),
           _status_ptr(status, X.device))
     return out
@@ -198,6 +202,8 @@ def mx_dequant(t: MXTensor, dtype=torch.bfloat16, out=None) -> torch.Tensor:
         out = t.codes.new_empty((t.rows, t.cols), dtype=dtype)
     else:
         _tensor(out, "out", (t.rows, t.cols), dtype, dev)
+    if t.rows == 0:
+        return out
     _call(dev, _q.lib().qlora_mx_dequant, ctypes.byref(d), out.data_ptr(), kind)
     return out
 
@@ -213,6 +219,10 @@ def mx_matmul(a: MXTensor, b: MXTensor, dtype=torch.bfloat16, out=None, status=N
         out = a.codes.new_empty((a.rows, b.rows), dtype=dtype)
     else:
         _tensor(out, "out", (a.rows, b.rows), dtype, dev)
+    if a.cols != b.cols or b.rows % 8:
+        _bad("a and b must have equal cols, b a multiple of 8 rows")
+    if a.rows == 0 or b.rows == 0:
+        return out
     _call(dev, _q.lib().qlora_mx_matmul, ctypes.byref(da), ctypes.byref(db), out.data_ptr(), kind,
           _status_ptr(status, dev))
     return out

@@ -264,3 +264,25 @@ def test_outputs_over_inputs_that_are_no_longer_read(lib):
     x = X.clone()
     assert torch.equal(lib.mx_linear_fwd(x, w, L1, L2, 0.5, dropout=drop, Y=x)[0], Y)
     assert torch.equal(x, Y)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_matrices_without_rows(lib, dtype):
+    """No tokens, no features: empty results of the right shapes, as the
+    linear layer gives them."""
+    X = torch.randn((3, 96), device="cuda").to(dtype)
+    none = lib.mx_quantize(X[:0])
+    assert (none.rows, none.cols) == (0, 96)
+    assert lib.mx_dequant(none, dtype=dtype).shape == (0, 96)
+    turned = lib.mx_quantize(torch.empty((64, 0), dtype=dtype, device="cuda"), transpose=True)
+    assert (turned.rows, turned.cols) == (0, 64) and lib.mx_dequant(turned).shape == (0, 64)
+    w = lib.mx_quantize(torch.randn((16, 96), device="cuda"))
+    assert lib.mx_matmul(none, w, dtype=dtype).shape == (0, 16)
+    assert lib.mx_matmul(w, none, dtype=dtype).shape == (16, 0)
+    assert lib.dropout(X[:0], 0.5, 1).shape == (0, 96)
+    for bad in (lambda: lib.mx_quantize(X[:0, :40].contiguous()), lambda: lib.mx_matmul(none, turned),
+                lambda: lib.MXTensor.empty(0, 40), lambda: lib.MXTensor.empty(-1, 32),
+                lambda: lib.mx_matmul(none, lib.mx_quantize(torch.randn((12, 96), device="cuda")))):
+        with pytest.raises(lib.QLoRAError):
+            bad()
+    assert lib.read_status() == 0
