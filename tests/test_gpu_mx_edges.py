@@ -286,3 +286,112 @@ def test_matrices_without_rows(lib, dtype):
         with pytest.raises(lib.QLoRAError):
             bad()
     assert lib.read_status() == 0
+
+
+# ------------------------------------------------------ long adapter reductions
+@pytest.mark.parametrize("p", [0.0, 0.1])
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 22016, 16), (1, 22016, 64, 128), (70, 4128, 22016, 64), (70, 22016, 4128, 8),
+                                     (600, 64, 8224, 128), (1100, 4128, 4128, 64), (4500, 128, 96, 16)])
+def test_long_adapter_sums_are_those_of_fp32(lib, M, N, K, r, p):
+    """T, dL1 and dL2 over long reductions, by the kernels that finish a tile in
+    a cluster and by those that leave partial sums, with dropout and without.
+
+    The operands are exact, so the error is that of the sums.  In a piece of 512
+    terms (32 steps) a step loses at most a unit of the running sum to
+    truncation, half of one of 2^-23 to 2^-24 on average: 0.36 2^-23 |S_i|, with
+    |S_i| growing as the root of the step 0.36 (2/3) 32 2^-23 = 0.92e-6 of the
+    piece, toward zero.  Pieces are added with rounding (2^-24 each time, up to 43
+    of them, at random: 0.3e-6).  A sum of 4128 terms in one piece would lose
+    seven times that.  dL1 has dT's error on top of its own."""
+    g = torch.Generator("cuda").manual_seed(M + N + K)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    X, dY = rnd(M, K).bfloat16(), (rnd(M, N) * 0.01).bfloat16()
+    L1, L2 = (rnd(K, r) * K ** -0.5).bfloat16(), (rnd(r, N) * 0.05).bfloat16()
+    w = lib.mx_weight((rnd(N, K) * 0.02).bfloat16())
+    drop = lib.Dropout(p, 9, M) if p else None
+    m = 1.0
+    if p:
+        m = torch.from_numpy(O.dropout_keep(M * K, p, 9, M).reshape(M, K)).cuda().double() * O.dropout_scale(p)
+    Y, T = lib.mx_linear_fwd(X, w, L1, L2, 0.5, dropout=drop)
+    dX, dL1, dL2 = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop)
+    alone = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop, need_dX=False)
+    Xm = X.double() * m
+    refs = (Xm @ L1.double(), Xm.t() @ (0.5 * dY.double() @ L2.double().t()), 0.5 * T.double().t() @ dY.double())
+    for got, ref, bound, what in ((T, refs[0], 1.25e-6, "T"), (dL1, refs[1], 2.5e-6, "dL1"), (dL2, refs[2], 1.25e-6, "dL2"),
+                                  (alone[1], refs[1], 2.5e-6, "dL1 alone"), (alone[2], refs[2], 1.25e-6, "dL2 alone")):
+        err = float((got.double() - ref).norm() / ref.norm())
+        assert err <= bound, f"{what}: {err:.2e}"
+    assert torch.isfinite(Y).all() and torch.isfinite(dX).all() and lib.read_status() == 0
+
+
+# ------------------------------------------------------- offsets on the device
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 96, 8), (40, 96, 160, 16), (300, 2080, 544, 128), (2100, 2336, 2400, 64)])
+def test_linear_reads_its_offset_on_the_device(lib, M, N, K, r):
+    """Dropout with its offset in a CUDA tensor: each kernel that evaluates the
+    mask reads it when it runs, eagerly and from one captured graph."""
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=M)
+    off = torch.tensor([3], dtype=torch.int64, device="cuda")
+
+    def step(offset):
+        drop = lib.Dropout(0.3, 11, offset)
+        Y, T = lib.mx_linear_fwd(X, w, L1, L2, 0.5, dropout=drop)
+        both = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop)
+        return (Y, T) + both + lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop, need_dX=False)[1:]
+
+    refs = {o: step(o) for o in (3, 4, (1 << 40) + 1)}
+    assert not torch.equal(refs[3][0], refs[4][0])
+    for o in refs:
+        off.fill_(o)
+        assert all(torch.equal(a, b) for a, b in zip(step(off), refs[o]))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(off)
+    for o in refs:
+        off.fill_(o)
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, refs[o])), o
+    assert lib.read_status() == 0
+
+
+# ------------------------------------------------------------- given outputs
+@pytest.mark.parametrize("M", [5, 300, 1100])
+def test_outputs_go_to_the_buffers_given(lib, M):
+    """Y, T, dX, dL1 and dL2 in the caller's memory, all of it and nothing else."""
+    N, K, r = 96, 160, 24
+    X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=M + 1)
+    drop = lib.Dropout(0.2, 2)
+
+    def inside(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 128,), 3.0, dtype=dtype, device="cuda")
+        bufs.append((buf, n))
+        return buf[64:64 + n].view(shape)
+
+    bufs = []
+    Y, T = lib.mx_linear_fwd(X, w, L1, L2, 0.5, dropout=drop)
+    grads = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop)
+    y, t = inside((M, N), torch.bfloat16), inside((M, r), torch.float32)
+    got = lib.mx_linear_fwd(X, w, L1, L2, 0.5, dropout=drop, Y=y, T=t)
+    assert got[0] is y and got[1] is t and torch.equal(y, Y) and torch.equal(t, T)
+    outs = [inside((M, K), torch.bfloat16), inside((K, r), torch.float32), inside((r, N), torch.float32)]
+    got = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop, dX=outs[0], dL1=outs[1], dL2=outs[2])
+    assert all(a is b for a, b in zip(got, outs)) and all(torch.equal(a, b) for a, b in zip(got, grads))
+    for buf, n in bufs:
+        assert (buf[:64] == 3).all() and (buf[64 + n:] == 3).all()
+
+
+def test_gradients_in_the_flat_buffer_of_data_parallelism(lib):
+    """AdapterGrads' views as the gradients of two layers: each writes its own
+    part of the flat buffer, which is what a collective then sums."""
+    from bit_nf4_quantized_15_b200.data_parallel import AdapterGrads
+    M, r, shapes = 520, 16, [(96, 160), (320, 64)]
+    grads = AdapterGrads(shapes, r)
+    parts = []
+    for i, (N, K) in enumerate(shapes):
+        X, w, L1, L2, dY, _ = _problem(lib, M, N, K, r, seed=i)
+        Y, T = lib.mx_linear_fwd(X, w, L1, L2, 0.5)
+        _, a, b = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5)
+        parts += [a.reshape(-1), b.reshape(-1)]
+        lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dL1=grads.dL1[i], dL2=grads.dL2[i])
+    assert torch.equal(grads.flat, torch.cat(parts))
+    assert grads.all_reduce() is grads
