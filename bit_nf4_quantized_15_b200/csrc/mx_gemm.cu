@@ -89,7 +89,8 @@ QDEV void mask_chunk(uint32_t (&v)[16], const MxGemmArgs& a, const PhiloxKey& ke
   }
 }
 
-template <int BN>
+// F32: fp32 output (no LoRA term), in pieces of the reduction.
+template <int BN, bool F32>
 __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __grid_constant__ MxGemmArgs args) {
   using C = MxCfg<BN>;
   constexpr int kS = C::S;
@@ -99,8 +100,9 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   uint64_t* empty = full + kS;
   uint64_t* ext_done = empty + kS;    // the LoRA term is in tensor memory
   uint64_t* ext_masked = ext_done + 1;  // ... and masked
-  uint64_t* accum = ext_masked + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
+  uint64_t* accum = ext_masked + 1;     // the sum (F32: of a piece) is in tensor memory
+  uint64_t* drained = accum + 1;        // F32: ... and in registers
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -111,9 +113,10 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   const int row0 = row_tile * 128, col0 = col_tile * BN;
   const int kb_lo = (int)((int64_t)rank * args.kb / csize), kb_hi = (int)((int64_t)(rank + 1) * args.kb / csize);
   const int rb = (args.r + 63) / 64;                      // 64-wide blocks of the rank
-  const int n_ext = rank == 0 ? kLoraTerms * rb : 0;      // term by term
+  const int n_ext = !F32 && rank == 0 ? kLoraTerms * rb : 0;  // term by term
   const int n_iters = n_ext + kb_hi - kb_lo;
   const bool masked = n_ext && args.drop.threshold;
+  const int pieces = F32 ? (n_iters + kMxPiece - 1) / kMxPiece : 1;
   const uint64_t lim = args.wait_ns ? args.wait_ns : QNF4_WAIT_NS;
 
   if (tid == 0) {
@@ -124,6 +127,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
     mbar_init(ext_done, 1);
     mbar_init(ext_masked, C::EW);
     mbar_init(accum, 1);
+    mbar_init(drained, C::EW);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&args.tmA);
@@ -139,6 +143,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   pdl_trigger();  // not before this CTA has its tensor memory: a dependent CTA must not take it first
   bool committed = false;
+  uint32_t last_ph = 0;  // of accum
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -237,11 +242,19 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
           if (kk < steps)
             umma_mxf4(tmem, kdesc(a0 + so + 2 * kk), kdesc(a0 + so + (C::A >> 4) + 2 * kk),
                       idesc_mxf4(128, BN, 2 * (kk & 1)), sf + 4 * (kk >> 1), sfb0 + sf + 8 + 4 * C::FB * (kk >> 1),
-                      (it | kk) != 0);
+                      ((F32 ? it % kMxPiece : it) | kk) != 0);
         }
         umma_commit(empty + s);
       }
       __syncwarp();
+      if (F32 && (it + 1) % kMxPiece == 0 && it + 1 < n_iters) {
+        if (one) umma_commit(accum);
+        committed = true;
+        __syncwarp();
+        if (!warp_poll(drained, last_ph, abort_flag, args.status, lane, lim)) break;
+        tc_fence_after();
+        last_ph ^= 1u;
+      }
       if (++s == kS) {
         s = 0;
         ph ^= 1u;
@@ -273,12 +286,38 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
       __syncwarp();
       if (lane == 0) mbar_arrive(ext_masked);
     }
-    const bool ok = warp_wait(accum, 0, abort_flag, args.status, lane, lim);
-    tc_fence_after();
-    for (int c = grp * 16; c < BN; c += G * 16) {
+    constexpr int kChunks = BN / (16 * G);
+    float sum[F32 ? kChunks : 1][16] = {};
+    bool ok = true;
+#pragma unroll 1
+    for (int p = 0; p < pieces && ok; ++p) {
+      ok = warp_wait(accum, (uint32_t)p & 1u, abort_flag, args.status, lane, lim);
+      tc_fence_after();
+      if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          uint32_t v[16];
+          tmem_ld16(tl + (uint32_t)((grp + i * G) * 16), v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], __uint_as_float(v[j]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(drained);
+      }
+    }
+#pragma unroll(F32 ? kChunks : 1)
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = (grp + i * G) * 16;
       uint32_t v[16];
-      tmem_ld16(tl + (uint32_t)c, v);
-      tmem_wait_ld();
+      if constexpr (F32) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(sum[i][j]);
+      } else {
+        tmem_ld16(tl + (uint32_t)c, v);
+        tmem_wait_ld();
+      }
       if (csize > 1) {  // this CTA's partial tile, over the stages (all read by now)
         float* red = reinterpret_cast<float*>(smem) + c * 128 + q4 * 32 + lane;
 #pragma unroll
@@ -291,7 +330,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           if (j >= ncol) continue;
-          if (args.out_f32) reinterpret_cast<float*>(args.out)[o + j * args.ldo] = __uint_as_float(v[j]);
+          if (F32) reinterpret_cast<float*>(args.out)[o + j * args.ldo] = __uint_as_float(v[j]);
           else reinterpret_cast<__nv_bfloat16*>(args.out)[o + j * args.ldo] = __float2bfloat16_rn(__uint_as_float(v[j]));
         }
       }
@@ -304,7 +343,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
   if (*abort_flag) {
     // Error path: let MMAs and loads still in flight finish before shared and
     // tensor memory are given back.
-    if (warp == 1 && lane == 0 && committed) mbar_wait_drain(accum, 0, 10000000ull);
+    if (warp == 1 && lane == 0 && committed) mbar_wait_drain(accum, last_ph, 10000000ull);
     if (tid == 0) {
       const uint64_t t0 = globaltimer();
       while (globaltimer() - t0 < 2000000ull) {
@@ -335,7 +374,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::THREADS, 1) mx_gemm_kernel(const __
       for (int p = 1; p < 8; ++p)
         if (p < csize) acc = make_float2(acc.x + v[p].x, acc.y + v[p].y);
       const int64_t o = (int64_t)(col0 + c) * args.ldo + row0 + rp;
-      if (args.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(args.out) + o) = acc;
+      if (F32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(args.out) + o) = acc;
       else *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(args.out) + o) = pack_bf16x2(acc.x, acc.y);
     }
     cluster_sync_all();  // peers may still be reading this CTA's tile
@@ -346,7 +385,9 @@ template <int BN>
 cudaError_t launch_bn(const MxGemmArgs& a, const MxGemmPlan& p, bool dependent, cudaStream_t st) {
   using C = MxCfg<BN>;
   const dim3 grid((unsigned)(p.m_tiles * p.n_tiles * p.cluster));
-  return launch_kernel<mx_gemm_kernel<BN>>({grid, C::THREADS, C::TOTAL, (unsigned)p.cluster, dependent}, st, a);
+  const LaunchShape shape{grid, C::THREADS, C::TOTAL, (unsigned)p.cluster, dependent};
+  return a.out_f32 ? launch_kernel<mx_gemm_kernel<BN, true>>(shape, st, a)
+                   : launch_kernel<mx_gemm_kernel<BN, false>>(shape, st, a);
 }
 
 }  // namespace

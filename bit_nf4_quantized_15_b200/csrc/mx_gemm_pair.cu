@@ -35,7 +35,7 @@
 //   empty[s]  each: the MMAs that read stage s have finished
 //   ext       each: the LoRA term of the tile is in tensor memory
 //   masked    even: 16 epilogue warps have masked it
-//   accum     each: the tile's accumulator is final
+//   accum     each: the tile's accumulator is final (fp32 output: a piece of it)
 //   drained   even: 16 epilogue warps hold it in registers
 // Every wait is bounded; the pair meets at a cluster barrier before tensor
 // memory is freed.
@@ -119,7 +119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
   const int pair = (int)(blockIdx.x >> 1), n_pairs = (int)(gridDim.x >> 1);
   const int m_tiles = (args.rows + 255) / 256, n_tiles = (args.cols + 255) / 256, tiles = m_tiles * n_tiles;
   const int rb = (args.r + 63) / 64;  // 64-wide blocks of the rank
-  const int n_ext = kLoraTerms * rb, n_main = args.kb;
+  const int n_ext = F32 ? 0 : kLoraTerms * rb, n_main = args.kb;  // fp32 output: no LoRA term
   const bool use_mask = n_ext && args.drop.threshold;
 
   if (tid == 0) {
@@ -223,10 +223,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
       int s = 0;
       uint32_t sph = 0, ph = 0;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += n_pairs, ph ^= 1u) {
-        if (!(ok = warp_poll(drained, ph ^ 1u, abort_flag, args.status, lane))) break;
-        tc_fence_after();
+      for (int t = pair; t < tiles && ok; t += n_pairs) {
         for (int i = 0; i < n_ext + n_main; ++i) {
+          const int in_sum = F32 ? i % kMxPiece : i;  // stage of this accumulation
+          if (in_sum == 0) {
+            if (!(ok = warp_poll(drained, ph ^ 1u, abort_flag, args.status, lane))) break;
+            tc_fence_after();
+          }
           if (!(ok = warp_poll(full + s, sph, abort_flag, args.status, lane))) break;
           tc_fence_after();
           if (i < n_ext) {
@@ -262,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
               if (kk < steps)
                 umma_mxf4_pair(tmem, kdesc(a0 + so + 2 * kk), kdesc(a0 + so + (kXA >> 4) + 2 * kk),
                                idesc_mxf4(256, 256, 2 * (kk & 1)), sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1),
-                               (i | kk) != 0);
+                               (in_sum | kk) != 0);
             }
             umma_commit_both(empty + s);
           }
@@ -271,10 +274,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
             s = 0;
             sph ^= 1u;
           }
+          if (i + 1 == n_ext + n_main || (F32 && in_sum + 1 == kMxPiece)) {
+            if (one) umma_commit_both(accum);
+            committed = true;
+            last_ph = ph;
+            ph ^= 1u;
+          }
         }
-        if (one) umma_commit_both(accum);
-        committed = true;
-        last_ph = ph;
       }
     }
     __syncwarp();
@@ -289,9 +295,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
       const TileXY xy = tile_of(pair, m_tiles, n_tiles);
       mask_row(mw, args, key, (int64_t)xy.m * 256 + rl, xy.n * 256 + half * 128);
     }
-    int no = 0;
-    for (int t = pair; t < tiles; t += n_pairs, ++no) {
-      const uint32_t ph = (uint32_t)no & 1u;
+    uint32_t ph = 0;
+    for (int t = pair; t < tiles; t += n_pairs) {
       const TileXY xy = tile_of(t, m_tiles, n_tiles);
       if (use_mask) {
         if (!warp_wait(ext, ph, abort_flag, args.status, lane)) break;
@@ -318,28 +323,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
           mask_row(mw, args, key, (int64_t)nx.m * 256 + rl, nx.n * 256 + half * 128);
         }
       }
-      if (!warp_wait(accum, ph, abort_flag, args.status, lane)) break;
-      tc_fence_after();
       const int col = xy.n * 256 + half * 128;
       if constexpr (F32) {
+        float sum[8][16] = {};  // of the pieces so far
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < n_main && ok; i += kMxPiece, ph ^= 1u) {
+          ok = warp_wait(accum, ph, abort_flag, args.status, lane);
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t v[16];
+            tmem_ld16(tl + (uint32_t)(16 * q), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[q][j] = __fadd_rn(sum[q][j], __uint_as_float(v[j]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(drained0);
+        }
+        if (!ok) break;
         const int64_t row = (int64_t)xy.m * 256 + rl;
         float* dst = reinterpret_cast<float*>(args.out) + row * args.ldo + col;
+        if (row < args.rows) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(tl + (uint32_t)c, v);
-          tmem_wait_ld();
-          if (row < args.rows) {
-#pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              if (col + c + j < args.cols)
-                *reinterpret_cast<uint4*>(dst + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-          }
-          __syncwarp();  // the next load takes the whole warp
+          for (int c = 0; c < 128; c += 4)
+            if (col + c < args.cols)
+              *reinterpret_cast<float4*>(dst + c) = make_float4(sum[c / 16][c % 16], sum[c / 16][c % 16 + 1],
+                                                                sum[c / 16][c % 16 + 2], sum[c / 16][c % 16 + 3]);
         }
-        tc_fence_before();
-        if (lane == 0) mbar_arrive_cluster(drained0);
+        __syncwarp();
       } else {
+        if (!warp_wait(accum, ph, abort_flag, args.status, lane)) break;
+        tc_fence_after();
         uint32_t v[8][16];  // the whole row half, loads all in flight; packed once the accumulator is released
 #pragma unroll
         for (int q = 0; q < 8; ++q) tmem_ld16(tl + (uint32_t)(16 * q), v[q]);
@@ -370,6 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
             bulk_commit();
           }
         }
+        ph ^= 1u;
       }
     }
     if (!F32 && lane == 0) bulk_wait_all();

@@ -20,6 +20,15 @@ QDEV void cluster_wait() {
 
 constexpr int kMxKB = 256;  // reduction elements of a stage: 128 bytes of codes
 
+// Stages of one accumulation of an fp32 product.  The tensor cores truncate
+// their sums, toward zero and by the length of the sum: blocks of sizes over
+// 2^24 : 1 and 22016 terms in one accumulation were 6.9e-6 off (fp32 arithmetic
+// 1.1e-6; blocks of about one size are exact either way).  So an fp32 result is
+// accumulated in pieces of 2048 terms that are added with rounding: 0.7e-6,
+// whatever the length (8192^3 in 317 us, 302 in one accumulation).  A bf16
+// result takes one accumulation: its own rounding is 1.7e-3.
+constexpr int kMxPiece = 8;
+
 // Instruction descriptor, kind::mxf4: E2M1 x E2M1, E8M0 scales; the scale ids
 // pick bytes 0-1 or 2-3 of each scale column word (two 32-blocks a step).
 __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf_id) {

@@ -355,7 +355,9 @@ QLORA_API int qlora_mx_dequant(const qlora_mx_tensor* t, void* out, int dtype, q
 
 /*
  * out[a->rows][b->rows] = RN( A^ . B^T ), bf16 or fp32: the product of two
- * MXFP4 matrices with the same cols, accumulated in fp32.  b->rows % 8 == 0.
+ * MXFP4 matrices with the same cols, accumulated in fp32 (in pieces of 2048
+ * terms, added with rounding, where the result is fp32: the tensor cores'
+ * own sums truncate).  b->rows % 8 == 0.
  * The order of summation is fixed by the shapes: equal calls give equal bits.
  */
 QLORA_API int qlora_mx_matmul(const qlora_mx_tensor* a, const qlora_mx_tensor* b, void* out, int dtype,

@@ -395,3 +395,27 @@ def test_gradients_in_the_flat_buffer_of_data_parallelism(lib):
         lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dL1=grads.dL1[i], dL2=grads.dL2[i])
     assert torch.equal(grads.flat, torch.cat(parts))
     assert grads.all_reduce() is grads
+
+
+# ---------------------------------------------------------------- fp32 products
+@pytest.mark.parametrize("M,N,K", [(16, 1024, 22016), (40, 22016, 8192), (130, 9600, 4160), (512, 8192, 22016),
+                                   (2304, 2312, 8224)])
+def test_fp32_product_of_blocks_of_many_sizes(lib, M, N, K):
+    """Blocks over 2^24 : 1 in size, where the order of the sum matters: the
+    pieces of 2048 terms are 32 steps each, so the error is as in
+    test_long_adapter_sums_are_those_of_fp32 (0.92e-6 and the rounding of at most
+    11 additions)."""
+    g = torch.Generator("cuda").manual_seed(K + M)
+
+    def mixed(rows):
+        x = torch.randn((rows, K // 32, 32), generator=g, device="cuda")
+        e = torch.rand((rows, K // 32, 1), generator=g, device="cuda") * 24 - 12
+        return lib.mx_quantize((x * torch.exp2(e)).reshape(rows, K))
+
+    a, b = mixed(M), mixed(N)
+    got = lib.mx_matmul(a, b, dtype=torch.float32)
+    ref = lib.mx_dequant(a, torch.float32).double() @ lib.mx_dequant(b, torch.float32).double().t()
+    err = float((got.double() - ref).norm() / ref.norm())
+    assert err <= 1.25e-6, f"{err:.2e}"
+    assert torch.equal(got, lib.mx_matmul(a, b, dtype=torch.float32))
+    assert lib.read_status() == 0
