@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from dataclasses import dataclass
 
 import torch
@@ -165,9 +166,13 @@ class Dropout:
         if isinstance(off, torch.Tensor):
             _tensor(off.reshape(-1), "offset", (1,), torch.int64, device)
             off, dev_ptr = 0, off.data_ptr()
-        if not (0 <= self.seed <= _U64 and 0 <= off <= _U64):
+        try:
+            seed, off = operator.index(self.seed), operator.index(off)
+        except TypeError:
+            seed = off = -1
+        if not (0 <= seed <= _U64 and 0 <= off <= _U64):
             _bad("seed and offset must be 64-bit unsigned integers")
-        return qlora_dropout_config(float(self.p), int(self.seed), int(off), dev_ptr)
+        return qlora_dropout_config(float(self.p), seed, off, dev_ptr)
 
 
 def mx_quantize(X, transpose: bool = False, out: MXTensor | None = None, status=None) -> MXTensor:

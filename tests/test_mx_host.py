@@ -175,3 +175,12 @@ def test_overlapping_outputs_are_refused(q):
             assert L.qlora_dropout(p(0x400), dtype, n, _d(q), p(0x400 + step), None) == OVERLAP
             assert L.qlora_dropout(p(0x400), dtype, n, _d(q), p(0x400 - step), None) == OVERLAP
     assert b"overlap" in L.qlora_status_string(OVERLAP)
+
+
+def test_seeds_and_offsets_are_whole_numbers(q):
+    """A fraction was cut to another seed's mask."""
+    for seed, off in ((1.5, 0), (2.0, 0), (0, 0.5), ("1", 0), (None, 0)):
+        with pytest.raises(q.QLoRAError):
+            q.Dropout(0.1, seed, off).config(torch.device("cpu"))
+    c = q.Dropout(0.1, torch.tensor(7).item(), (1 << 64) - 1).config(torch.device("cpu"))
+    assert (c.seed, c.offset, c.offset_dev) == (7, (1 << 64) - 1, None)
