@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kQT, QtCfg<DT>::CTAS)
 }
 
 // Value of a code times 2^(b - 127).  The E2M1 value is exact in fp16 and the
-// product exact in fp32 (a subnormal one included: at least 2^-128); scale
-// byte 255 is NaN.
+// product exact in fp32 (a subnormal one included: at least 2^-128), or past
+// its range an infinity; scale byte 255 is NaN.
 QDEV float2 values2(uint32_t byte, float lo, float hi) {
   const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
   const float2 f = __half22float2(__half2(h));

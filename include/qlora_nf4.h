@@ -349,8 +349,10 @@ QLORA_API int qlora_mx_storage_bytes(int64_t rows, int64_t cols, size_t* codes_b
 QLORA_API int qlora_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int transpose,
                                 const qlora_mx_tensor* out, int* status_dev, qlora_stream_t stream);
 
-/* The values an MXFP4 matrix stands for, [rows][cols]: bf16 (exact) or fp32
- * (exact). */
+/* The values an MXFP4 matrix stands for, [rows][cols]: bf16 or fp32, both
+ * exact.  (Scale bytes 253 and 254, which the quantiser never writes, stand with
+ * the codes of 4 and 6, resp. 2 and up, for values past both types' range: these
+ * are infinities.) */
 QLORA_API int qlora_mx_dequant(const qlora_mx_tensor* t, void* out, int dtype, qlora_stream_t stream);
 
 /*

@@ -419,3 +419,35 @@ def test_fp32_product_of_blocks_of_many_sizes(lib, M, N, K):
     assert err <= 1.25e-6, f"{err:.2e}"
     assert torch.equal(got, lib.mx_matmul(a, b, dtype=torch.float32))
     assert lib.read_status() == 0
+
+
+# ------------------------------------------------------- scales from elsewhere
+def test_every_scale_byte_with_every_code(lib):
+    """Also bytes that the quantiser never writes: values past the range are
+    infinities, 255 is NaN."""
+    codes = np.tile(np.arange(16, dtype=np.uint8), (256, 2))                 # 32 a row
+    s = np.arange(256, dtype=np.uint8)[:, None]
+    t = lib.MXTensor(torch.from_numpy(O.mx_pack(codes)).cuda(), torch.from_numpy(O.mx_tile_scales(s)).cuda(), 256, 32)
+    with np.errstate(over="ignore"):
+        ref = O.mx_values(codes, s).astype(np.float32)
+    assert np.isinf(ref[253:255]).any() and not np.isinf(ref[:253]).any()
+    for dtype in (torch.float32, torch.bfloat16):
+        got = lib.mx_dequant(t, dtype=dtype).float().cpu().numpy()
+        assert np.array_equal(got, ref, equal_nan=True), dtype
+
+
+def test_product_of_large_scales_with_small_ones(lib):
+    """Every pair of scale bytes whose product is a normal number."""
+    rng = np.random.default_rng(4)
+    s = np.arange(255, dtype=np.uint8)[:, None]
+    a, b = (rng.integers(0, 16, (n, 32)).astype(np.uint8) for n in (255, 256))
+    sb = np.minimum(np.arange(256), 254).astype(np.uint8)[:, None]
+    A = lib.MXTensor(torch.from_numpy(O.mx_pack(a)).cuda(), torch.from_numpy(O.mx_tile_scales(s)).cuda(), 255, 32)
+    B = lib.MXTensor(torch.from_numpy(O.mx_pack(b)).cuda(), torch.from_numpy(O.mx_tile_scales(sb)).cuda(), 256, 32)
+    got = to_f64(lib.mx_matmul(A, B, dtype=torch.float32))
+    A64, B64 = O.mx_values(a, s), O.mx_values(b, sb)
+    ref, size = A64 @ B64.T, np.abs(A64) @ np.abs(B64).T
+    e = s.astype(int) + sb.T.astype(int) - 254
+    plain = (e >= -122) & (e <= 115)     # 32 products of at most 36 fit, and the least of 1/4 is normal
+    assert np.array_equal(got[plain], ref[plain]) and plain.mean() > 0.6
+    assert (size[plain] < 2.0 ** 127).all()
