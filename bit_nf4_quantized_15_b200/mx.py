@@ -100,6 +100,9 @@ def _status_ptr(status, device):
         status = _q._status_bufs.get(device.index)
         if status is None:
             status = _q._status(device)
+    elif not (isinstance(status, torch.Tensor) and status.dtype == torch.int32 and status.device == device
+              and status.numel()):
+        _bad(f"status must be an int32 CUDA tensor on {device}")
     return status.data_ptr()
 
 

@@ -184,3 +184,17 @@ def test_seeds_and_offsets_are_whole_numbers(q):
             q.Dropout(0.1, seed, off).config(torch.device("cpu"))
     c = q.Dropout(0.1, torch.tensor(7).item(), (1 << 64) - 1).config(torch.device("cpu"))
     assert (c.seed, c.offset, c.offset_dev) == (7, (1 << 64) - 1, None)
+
+
+def test_status_words_the_gpu_cannot_write_are_refused(q):
+    """A kernel would store to a host address, or past a narrower word."""
+    dev = torch.device("cuda", 0)
+    for status in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32, device="meta"), 0x1000):
+        with pytest.raises(q.QLoRAError):
+            q.mx._status_ptr(status, dev)
+    cpu = torch.device("cpu")
+    for status in (torch.zeros(1, dtype=torch.uint8), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(q.QLoRAError):
+            q.mx._status_ptr(status, cpu)
+    word = torch.zeros(1, dtype=torch.int32)
+    assert q.mx._status_ptr(word, cpu) == word.data_ptr()
