@@ -255,7 +255,7 @@ cudaError_t launch_mx_quantize_t(const void* X, int dtype, int64_t R, int64_t C,
                                  int* status, int sms, cudaStream_t st);
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int dtype,
                               void* out, cudaStream_t st);
-cudaError_t launch_dropout(const void* X, int dtype, int64_t n, const DropArgs& d, void* out, cudaStream_t st);
+cudaError_t launch_dropout(const void* X, int dtype, int64_t n, const DropArgs& d, void* out, int sms, cudaStream_t st);
 
 // bf16 terms of the LoRA term's token side (s T or the scaled dT) in a product.
 // One, its rounding to bf16, would leave an error of up to 2^-9 of the LoRA
@@ -292,11 +292,9 @@ struct MxGemmPlan {
   int m_tiles, n_tiles, cluster;
 };
 MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms);
-size_t mx_gemm_smem_bytes(int BN);
 // dependent: starts while the kernel before it on the stream (which writes
 // the tokens' side) still runs.
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, bool dependent, cudaStream_t st);
-
 
 // The same product on persistent CTA pairs, tokens on the lanes:
 // out[row][col] = sum_k A[row, k] B[col, k] (+ LoRA term), 256 x 256 tiles.
@@ -320,7 +318,6 @@ struct MxPairArgs {
   uint4* keep;       // if set: its bits, [rows][128-column tiles of ldo], 16 bytes each
   int* status;
 };
-size_t mx_pair_smem_bytes();
 cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, bool dependent, cudaStream_t st);
 
 // Quantise X and form D = drop(X).L in one pass (mx_prep.cu).
@@ -383,6 +380,6 @@ struct MxGradArgs {
 cudaError_t launch_mx_grad(MxGradArgs& a, const MxGradPlan& p, cudaStream_t st);
 
 // scale * in [M][r] as three bf16 terms [M][3r] (their sum is exact in fp32).
-cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st);
+cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, int sms, cudaStream_t st);
 
 }  // namespace qnf4

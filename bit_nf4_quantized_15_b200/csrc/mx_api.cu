@@ -275,8 +275,9 @@ int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_confi
   if (n == 0) return QLORA_OK;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  return launch_dropout(X, dtype, n, d, out, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QLORA_OK
-                                                                                                    : QLORA_ERR_CUDA;
+  return launch_dropout(X, dtype, n, d, out, di.sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? QLORA_OK
+             : QLORA_ERR_CUDA;
 }
 
 size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
@@ -379,7 +380,7 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
       return rc;
   }
   if (dL1 || dL2) {
-    if (dL2 && !dX && !dL1 && launch_split3(T_saved, M, r, s, sT, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (dL2 && !dX && !dL1 && launch_split3(T_saved, M, r, s, sT, di.sms, st) != cudaSuccess) return QLORA_ERR_CUDA;
     const MxGradMask mask = !d.threshold ? kMaskNone : keep ? kMaskBits : kMaskEvaluated;
     const MxGradPlan p = plan_mx_grad(M, dL1 ? K : 0, dL2 ? N : 0, r, mask, di.sms);
     MxGradArgs a;

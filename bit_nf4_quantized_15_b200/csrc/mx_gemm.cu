@@ -417,11 +417,6 @@ MxGemmPlan plan_mx_gemm(int64_t rows, int64_t cols, int64_t K, int num_sms) {
   return p;
 }
 
-size_t mx_gemm_smem_bytes(int BN) {
-  return BN >= 256 ? MxCfg<256>::TOTAL : BN >= 128 ? MxCfg<128>::TOTAL : BN >= 64 ? MxCfg<64>::TOTAL
-         : BN >= 32 ? MxCfg<32>::TOTAL : MxCfg<16>::TOTAL;
-}
-
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, const MxGemmPlan& p, bool dependent, cudaStream_t st) {
   switch (p.BN) {
     case 16: return launch_bn<16>(a, p, dependent, st);

@@ -416,8 +416,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
 
 }  // namespace
 
-size_t mx_pair_smem_bytes() { return kXTotal; }
-
 cudaError_t launch_mx_gemm_pair(const MxPairArgs& a, int num_sms, bool dependent, cudaStream_t st) {
   const int64_t tiles = (int64_t)((a.rows + 255) / 256) * ((a.cols + 255) / 256);
   const int pairs = num_sms / 2;

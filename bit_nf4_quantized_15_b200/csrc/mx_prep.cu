@@ -531,9 +531,9 @@ cudaError_t launch_mx_prep(MxPrepArgs& a, const MxPrepPlan& p, cudaStream_t st) 
       {dim3((unsigned)tiles, (unsigned)((128 * a.r + 1023) / 1024)), 256, 0, 1, true}, st, a.fin);
 }
 
-cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, cudaStream_t st) {
-  const int64_t n4 = M * r / 4, want = (n4 + 255) / 256;
-  split3_kernel<<<(unsigned)(want < 1184 ? want : 1184), 256, 0, st>>>(in, n4, r, scale, out);
+cudaError_t launch_split3(const float* in, int64_t M, int r, float scale, uint16_t* out, int sms, cudaStream_t st) {
+  const int64_t n4 = M * r / 4, want = (n4 + 255) / 256, most = (int64_t)sms * 8;
+  split3_kernel<<<(unsigned)(want < most ? want : most), 256, 0, st>>>(in, n4, r, scale, out);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -373,11 +373,6 @@ __global__ void __launch_bounds__(kQT) dropout_kernel(const void* X, int64_t n, 
   }
 }
 
-int elem_grid(int64_t n) {
-  const int64_t want = (n + kQT - 1) / kQT;
-  return (int)(want < 148 * 16 ? (want > 0 ? want : 1) : 148 * 16);
-}
-
 }  // namespace
 
 cudaError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
@@ -435,8 +430,9 @@ cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64
   return cudaGetLastError();
 }
 
-cudaError_t launch_dropout(const void* X, int dtype, int64_t n, const DropArgs& d, void* out, cudaStream_t st) {
-  const int grid = elem_grid((n + 7) / 8);
+cudaError_t launch_dropout(const void* X, int dtype, int64_t n, const DropArgs& d, void* out, int sms, cudaStream_t st) {
+  const int64_t want = ((n + 7) / 8 + kQT - 1) / kQT, most = (int64_t)sms * 16;
+  const int grid = (int)(want < most ? want : most);
   switch (dtype) {
     case QLORA_DTYPE_BF16: dropout_kernel<QLORA_DTYPE_BF16><<<grid, kQT, 0, st>>>(X, n, d, out); break;
     case QLORA_DTYPE_F16: dropout_kernel<QLORA_DTYPE_F16><<<grid, kQT, 0, st>>>(X, n, d, out); break;
