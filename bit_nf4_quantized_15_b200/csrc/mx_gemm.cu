@@ -19,9 +19,9 @@
 // (the weight), B the tokens: with few tokens BN shrinks to 16 and a call
 // streams the weight once through all SMs.
 //
-// Measured: one token through 4096 x 4096 5.7 us; 16 tokens through 22016 x
-// 8192 19 us, where its 96 MB take 14.6 at the measured copy bandwidth; 1000 x
-// 2056 x 1568 9 us.  The small ones are launch, tensor memory, one round trip
+// Measured in a graph: one token through 4096 x 4096 5.7 us; 16 tokens through
+// 22016 x 8192 19.6 us, where its 96 MB take 14.6 at the measured copy bandwidth
+// (15.4 with the weight in L2); 1000 x 2056 x 1568 7.8 us.  The small ones are launch, tensor memory, one round trip
 // to HBM and the epilogue, one after another.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, then 4 epilogue warps (8 for

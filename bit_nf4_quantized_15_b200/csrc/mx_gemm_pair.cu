@@ -20,9 +20,9 @@
 // the epilogue warps have the tile's mask ready (128 bits a thread, evaluated
 // during the previous tile's main loop).
 //
-// Measured, 8192^3: 213 us in a burst (5.17 PFLOP/s), 253 us sustained, where
-// the 1000 W cap holds the SM clock at 1.61 GHz.  A stage of 256 reduction
-// steps takes about 640 cycles of which the MMAs need 512: with half of the
+// Measured, 8192^3: 201 us in a burst (5.47 PFLOP/s), 235 us sustained, where
+// the 1000 W cap holds the SM clock down.  (The rest was measured when the
+// burst was 213 us.)  A stage of 256 reduction steps takes about 640 cycles of which the MMAs need 512: with half of the
 // MMA work taken out (N = 128 instructions) the kernel was 9 % faster, so the
 // loads, 11 TB/s out of L2, weigh as much as the tensor cores.  A tile ends
 // with some 3000 cycles in which the MMAs wait: 2300 are the drain itself (128

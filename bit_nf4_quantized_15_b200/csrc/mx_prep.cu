@@ -12,7 +12,7 @@
 // tile as the A operand of D.
 //
 // Work is cut into units of 128 rows x 256 columns.  While clusters of up to 8
-// CTAs for every row tile run at once, a cluster takes a row tile, adds its
+// CTAs (16 for up to 4 row tiles) for every row tile run at once, a cluster takes a row tile, adds its
 // CTAs' sums in rank order through distributed shared memory and forms T and
 // the bf16 terms of the scaled D itself (two for the products, three where the
 // adapter gradients take them too).  For more rows

@@ -346,7 +346,7 @@ QDEV void drop_store8(void* out, int64_t i, uint32_t* w, const uint4& rnd, const
 
 // out = x inv where kept, else 0.  Eight elements (one generator evaluation) a
 // thread and turn; a step has two turns with their loads in flight.  Bound by
-// HBM: 8192 x 8192 bf16, 268 MB, 46 us (5.8 TB/s), fp32 87 us (6.2 TB/s; with
+// HBM: 8192 x 8192 bf16, 268 MB, 47 us (5.7 TB/s), fp32 87 us (6.2 TB/s; with
 // one turn 93); a copy of the bf16 tensor takes 42.  out may be X: a thread
 // reads what it writes, by ordinary loads.
 template <int DT>
