@@ -18,13 +18,6 @@ namespace qnf4 {
 int current_device_info(DevInfo* out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QLORA_ERR_CUDA;
-  // The tensor maps are encoded by the driver, which wants a current context;
-  // a host thread has none until the runtime has given it the device's.
-  static thread_local int bound = -1;
-  if (bound != dev) {
-    if (cudaSetDevice(dev) != cudaSuccess) return QLORA_ERR_CUDA;
-    bound = dev;
-  }
   static DevInfo cache[64];
   static std::mutex mu;
   std::lock_guard<std::mutex> g(mu);
@@ -57,31 +50,37 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t inner, uint64_t outer,
-             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
+// A tiled map of `rank` dimensions; `strides` in bytes, of all but the first.
+static int encode_map(CUtensorMap* m, CUtensorMapDataType dt, uint32_t rank, const void* base, const cuuint64_t* dims,
+                      const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw) {
   auto fn = encode_fn();
   if (!fn) return QLORA_ERR_CUDA;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  for (int attempt = 0;; ++attempt) {
+    const CUresult r = fn(m, dt, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return QLORA_OK;
+    // The driver wants a current context, which a host thread has none of until
+    // the runtime has given it its device's.
+    int dev = 0;
+    if (attempt || cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return QLORA_ERR_CUDA;
+  }
+}
+
+int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t inner, uint64_t outer,
+             uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {inner * (uint64_t)esize};
   const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
+  return encode_map(m, dt, 2, base, dims, strides, box, sw);
 }
 
 int make_map3(CUtensorMap* m, const void* base, uint64_t n0, uint64_t n1, uint64_t n2, uint64_t s1, uint64_t s2,
               uint32_t b0, uint32_t b1, uint32_t b2) {
-  auto fn = encode_fn();
-  if (!fn) return QLORA_ERR_CUDA;
   const cuuint64_t dims[3] = {n0, n1, n2};
   const cuuint64_t strides[2] = {s1, s2};
   const cuuint32_t box[3] = {b0, b1, b2};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int map_operand(CUtensorMap* m, const void* base, int mn_major, uint64_t mn_extent, uint64_t k_extent, int rows) {
@@ -102,16 +101,7 @@ namespace {
 // consecutive 64-wide column blocks of box_rows rows.
 int map_blocks3d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                  uint32_t box_blocks) {
-  auto fn = encode_fn();
-  if (!fn) return QLORA_ERR_CUDA;
-  const cuuint64_t dims[3] = {64, rows, cols / 64};
-  const cuuint64_t strides[2] = {cols * 2, 128};
-  const cuuint32_t box[3] = {64, box_rows, box_blocks};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
+  return make_map3(m, base, 64, rows, cols / 64, cols * 2, 128, 64, box_rows, box_blocks);
 }
 
 int map_codes(CUtensorMap* m, const uint8_t* codes, int64_t N, int64_t K, int mn_mode) {

@@ -180,12 +180,13 @@ int prep(const uint16_t* X, int64_t M, int64_t C, const uint16_t* L, int l_mn, i
 //   keep   bits of the dropout mask, [M][128-column tiles of K], 16 bytes each,
 //          from the product of dX to the kernel of dL1
 //   part   fp32 partial sums of the adapter products
+// The partial sums are those of a device without clusters of 16, the most, so
+// that asking for a size makes no context.
 struct MxWs {
   size_t q_scales, u, v, keep, part, total;
-  MxPrepPlan prep_x, prep_dy;
 };
 
-MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms, int max_cluster) {
+MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms) {
   MxWs w{};
   const size_t qk = up256(codes_bytes(M, K)), qn = up256(codes_bytes(M, N));
   w.q_scales = qk > qn ? qk : qn;
@@ -199,9 +200,8 @@ MxWs mx_ws(int64_t M, int64_t N, int64_t K, int r, int sms, int max_cluster) {
     w.keep = o;
     o += up256((size_t)M * ((K + 127) / 128) * 16);
     w.part = o;
-    w.prep_x = plan_mx_prep(M, K, r, sms, max_cluster);
-    w.prep_dy = plan_mx_prep(M, N, r, sms, max_cluster);
-    o += up256(std::max({w.prep_x.part_bytes, w.prep_dy.part_bytes, mx_grad_part_bound(M, K, N, r, sms)}));
+    o += up256(std::max({plan_mx_prep(M, K, r, sms, 8).part_bytes, plan_mx_prep(M, N, r, sms, 8).part_bytes,
+                         mx_grad_part_bound(M, K, N, r, sms)}));
   }
   w.total = o;
   return w;
@@ -283,8 +283,8 @@ int qlora_dropout(const void* X, int dtype, int64_t n, const qlora_dropout_confi
 size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
   if (!linear_shape_ok(M, N, K, 8) || !rank_ok(r)) return 0;
   DevInfo di;
-  const bool gpu = current_device_info(&di) == QLORA_OK;
-  return mx_ws(M, N, K, r, gpu ? di.sms : 148, gpu ? mx_prep_max_cluster() : 16).total;
+  if (current_device_info(&di)) di.sms = 148;
+  return mx_ws(M, N, K, r, di.sms).total;
 }
 
 int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, const uint16_t* L1,
@@ -300,7 +300,7 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
   if (!all16({X, w->codes, w->scales, L1, L2, Y, T_save, ws})) return QLORA_ERR_ALIGN;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  const MxWs lay = mx_ws(M, N, K, r, di.sms, mx_prep_max_cluster());
+  const MxWs lay = mx_ws(M, N, K, r, di.sms);
   if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* wb = static_cast<uint8_t*>(ws);
@@ -316,7 +316,8 @@ int qlora_mx_linear_fwd(const uint16_t* X, int64_t M, const qlora_mx_tensor* w, 
     f.out = sT;
     f.terms = kLoraTerms;
     f.beta = s * d.inv;
-    if (int rc = prep(X, M, K, L1, 1, r, d, wb, wb + lay.q_scales, part, lay.prep_x, f, status_dev, st)) return rc;
+    const MxPrepPlan p = plan_mx_prep(M, K, r, di.sms, mx_prep_max_cluster());
+    if (int rc = prep(X, M, K, L1, 1, r, d, wb, wb + lay.q_scales, part, p, f, status_dev, st)) return rc;
   } else if (launch_mx_quantize(X, QLORA_DTYPE_BF16, M, K, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
     return QLORA_ERR_CUDA;
   }
@@ -345,7 +346,7 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
   if (dX && ((dL1 && overlap(dX, mk, X, mk)) || (dL2 && overlap(dX, mk, dY, mn)))) return QLORA_ERR_OVERLAP;
   DevInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  const MxWs lay = mx_ws(M, N, K, r, di.sms, mx_prep_max_cluster());
+  const MxWs lay = mx_ws(M, N, K, r, di.sms);
   if (ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* wb = static_cast<uint8_t*>(ws);
@@ -365,8 +366,8 @@ int qlora_mx_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const 
     f.T_in = dL2 ? T_saved : nullptr;
     f.out2 = sT;
     f.gamma = s;
-    if (int rc = prep(dY, M, N, L2, 0, r, DropArgs{}, wb, wb + lay.q_scales, part, lay.prep_dy, f, status_dev, st))
-      return rc;
+    const MxPrepPlan p = plan_mx_prep(M, N, r, di.sms, mx_prep_max_cluster());
+    if (int rc = prep(dY, M, N, L2, 0, r, DropArgs{}, wb, wb + lay.q_scales, part, p, f, status_dev, st)) return rc;
   } else if (dX &&
              launch_mx_quantize(dY, QLORA_DTYPE_BF16, M, N, wb, wb + lay.q_scales, status_dev, st) != cudaSuccess) {
     return QLORA_ERR_CUDA;

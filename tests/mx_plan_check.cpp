@@ -62,6 +62,7 @@ int main() {
                   [&](int64_t c) { return prep_unit(p.units, p.grid, c); },
                   [&](int64_t u) { return prep_owner(p.units, p.grid, u); });
     }
+    NEED(plan_mx_prep(M, C, r, sms, 8).part_bytes >= p.part_bytes);  // the workspace holds either
     NEED(plan_mx_prep(M + 1 + std::rand() % 300, C, r, sms, most).part_bytes >= p.part_bytes);
     for (int k = 0; k < 9; ++k) {
       const int64_t c0 = k % 3 == 2 ? 0 : C, c1 = k % 3 == 1 ? 0 : N;

@@ -5,6 +5,9 @@ paths that long reductions take, buffers that the caller gives.
 Bounds as in test_gpu_mx.py: half a bf16 step of a bf16 result, and one unit
 lost to truncation a step of the tensor cores' fp32 sums."""
 
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -100,7 +103,8 @@ def test_infinities_in_the_adapter_gradients(lib, where, M, p):
     keep = O.dropout_keep(M * K, p, 3, 4).reshape(M, K)
     m = M - 7
     if where == "X":
-        X[m, int(np.flatnonzero(keep[m])[2])], X[m - 3, int(np.flatnonzero(keep[m - 3])[4])] = float("inf"), float("-inf")
+        X[m, int(np.flatnonzero(keep[m])[2])] = float("inf")
+        X[m - 3, int(np.flatnonzero(keep[m - 3])[4])] = float("-inf")
     elif where == "dY":
         dY[m, 5] = float("-inf")         # where L2 has no column: dT meets 0 Inf
     elif where == "T":
@@ -290,8 +294,8 @@ def test_matrices_without_rows(lib, dtype):
 
 # ------------------------------------------------------ long adapter reductions
 @pytest.mark.parametrize("p", [0.0, 0.1])
-@pytest.mark.parametrize("M,N,K,r", [(1, 64, 22016, 16), (1, 22016, 64, 128), (70, 4128, 22016, 64), (70, 22016, 4128, 8),
-                                     (600, 64, 8224, 128), (1100, 4128, 4128, 64), (4500, 128, 96, 16)])
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 22016, 16), (1, 22016, 64, 128), (70, 4128, 22016, 64),
+                                     (70, 22016, 4128, 8), (600, 64, 8224, 128), (1100, 4128, 4128, 64), (4500, 128, 96, 16)])
 def test_long_adapter_sums_are_those_of_fp32(lib, M, N, K, r, p):
     """T, dL1 and dL2 over long reductions, by the kernels that finish a tile in
     a cluster and by those that leave partial sums, with dropout and without.
@@ -317,7 +321,8 @@ def test_long_adapter_sums_are_those_of_fp32(lib, M, N, K, r, p):
     alone = lib.mx_linear_bwd(dY, X, T, w, L1, L2, 0.5, dropout=drop, need_dX=False)
     Xm = X.double() * m
     refs = (Xm @ L1.double(), Xm.t() @ (0.5 * dY.double() @ L2.double().t()), 0.5 * T.double().t() @ dY.double())
-    for got, ref, bound, what in ((T, refs[0], 1.25e-6, "T"), (dL1, refs[1], 2.5e-6, "dL1"), (dL2, refs[2], 1.25e-6, "dL2"),
+    for got, ref, bound, what in ((T, refs[0], 1.25e-6, "T"),
+                                  (dL1, refs[1], 2.5e-6, "dL1"), (dL2, refs[2], 1.25e-6, "dL2"),
                                   (alone[1], refs[1], 2.5e-6, "dL1 alone"), (alone[2], refs[2], 1.25e-6, "dL2 alone")):
         err = float((got.double() - ref).norm() / ref.norm())
         assert err <= bound, f"{what}: {err:.2e}"
@@ -451,3 +456,17 @@ def test_product_of_large_scales_with_small_ones(lib):
     plain = (e >= -122) & (e <= 115)     # 32 products of at most 36 fit, and the least of 1/4 is normal
     assert np.array_equal(got[plain], ref[plain]) and plain.mean() > 0.6
     assert (size[plain] < 2.0 ** 127).all()
+
+
+def test_asking_for_a_size_makes_no_context(lib):
+    """A launcher may ask for workspace sizes before each rank picks its GPU."""
+    code = ("import ctypes, bit_nf4_quantized_15_b200 as q\n"
+            "assert q.mx_linear_workspace_bytes(16, 4096, 8192, 16) > 0\n"
+            "assert q.mx_storage_bytes(128, 128) == (8192, 512)\n"
+            "cu, flags, active = ctypes.CDLL('libcuda.so.1'), ctypes.c_uint(), ctypes.c_int(-1)\n"
+            "assert cu.cuInit(0) == 0\n"
+            "assert cu.cuDevicePrimaryCtxGetState(0, ctypes.byref(flags), ctypes.byref(active)) == 0\n"
+            "print('active', active.value)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "active 0", out.stdout + out.stderr

@@ -136,7 +136,8 @@ def test_binding_refuses_what_is_not_a_cuda_tensor(q):
 def test_workspace_never_falls_with_the_tokens(q):
     """One buffer for the largest batch serves the smaller ones."""
     n = q.mx_linear_workspace_bytes
-    for N, K, r in ((4096, 4096, 64), (1024, 1024, 128), (64, 22016, 8), (22016, 8192, 16), (96, 64, 128), (4096, 64, 0)):
+    for N, K, r in ((4096, 4096, 64), (1024, 1024, 128), (64, 22016, 8), (22016, 8192, 16), (96, 64, 128),
+                    (4096, 64, 0)):
         sizes = [n(M, N, K, r) for M in [*range(1, 4097), *range(4097, 20000, 61)]]
         falls = [i + 1 for i in range(len(sizes) - 1) if sizes[i + 1] < sizes[i]]
         assert not falls, (N, K, r, falls[:5])
