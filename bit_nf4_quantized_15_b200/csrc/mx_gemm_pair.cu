@@ -21,13 +21,13 @@
 // during the previous tile's main loop).
 //
 // Measured, 8192^3: 201 us in a burst (5.47 PFLOP/s), 235 us sustained, where
-// the 1000 W cap holds the SM clock down.  (The rest was measured when the
-// burst was 213 us.)  A stage of 256 reduction steps takes about 640 cycles of which the MMAs need 512: with half of the
-// MMA work taken out (N = 128 instructions) the kernel was 9 % faster, so the
-// loads, 11 TB/s out of L2, weigh as much as the tensor cores.  A tile ends
-// with some 3000 cycles in which the MMAs wait: 2300 are the drain itself (128
-// KB of tensor memory at 57 bytes a cycle, whatever the load width).  Two
-// accumulators of 192 columns hide it but pull 15 % more bytes per FLOP:
+// the 1000 W cap holds the SM clock down.  (What follows was measured when the
+// burst was 213 us.)  A stage of 256 reduction steps takes about 640 cycles of
+// which the MMAs need 512: with half of the MMA work taken out (N = 128
+// instructions) the kernel was 9 % faster, so the loads, 11 TB/s out of L2,
+// weigh as much as the tensor cores.  A tile ends with some 3000 cycles in
+// which the MMAs wait: 2300 are the drain itself (128 KB of tensor memory at 57
+// bytes a cycle, whatever the load width).  Two accumulators of 192 columns hide it but pull 15 % more bytes per FLOP:
 // 262 us against 213.
 //
 // Barriers (same offsets in both CTAs; "even" ones are used in the even CTA):
@@ -281,6 +281,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
             ph ^= 1u;
           }
         }
+      }
+      if (!ok) {  // what has been issued, for the error path to wait for
+        if (one) umma_commit_both(accum);
+        committed = true;
+        last_ph = ph;
       }
     }
     __syncwarp();
