@@ -470,3 +470,41 @@ def test_asking_for_a_size_makes_no_context(lib):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and out.stdout.strip() == "active 0", out.stdout + out.stderr
+
+
+def test_linear_past_32_bits_of_elements(lib):
+    """More than 2^32 activations: the mask's counters, its bits, T, dX and the
+    gradients of the last rows, the only ones that are not zero."""
+    M, K, N, r, tail, s = 131077, 32800, 64, 8, 300, 0.5
+    g = torch.Generator("cuda").manual_seed(2)
+    rnd = lambda *shape: torch.randn(shape, generator=g, device="cuda")  # noqa: E731
+    X = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    X[-tail:] = rnd(tail, K).bfloat16()
+    w = lib.mx_weight(rnd(N, K) * 0.02)
+    L1, L2, dY = (rnd(K, r) * K ** -0.5).bfloat16(), (rnd(r, N) * 0.05).bfloat16(), rnd(M, N).bfloat16()
+    drop = lib.Dropout(0.5, 3, 1)
+    q = np.arange((M - tail) * K // 8, M * K // 8, dtype=np.uint64)
+    lo, one = np.uint64(0xFFFFFFFF), np.ones_like(q)
+    words = O.philox4x32([q & lo, q >> np.uint64(32), one, 0 * one], (3, 0))
+    keep = np.stack([h for x in words for h in (x & np.uint64(0xFFFF), x >> np.uint64(16))], 1).reshape(-1) >= 32768
+    keep = torch.from_numpy(keep.reshape(tail, K)).cuda()
+
+    def near(got, ref, bound):
+        err = float((got.double() - ref).norm() / ref.norm())
+        assert err <= bound, f"{err:.2e}"
+
+    Y, T = lib.mx_linear_fwd(X, w, L1, L2, s, dropout=drop)
+    Xm, g64 = X[-tail:].double() * keep * 2, dY[-tail:].double()
+    assert not T[:-tail].any() and not Y[:-tail].any()
+    near(T[-tail:], Xm @ L1.double(), 1.5e-6)    # 0.92e-6, and 65 additions of pieces at random
+    ref1, ref2 = Xm.t() @ (s * g64 @ L2.double().t()), s * T[-tail:].double().t() @ g64
+    dX, dL1, dL2 = lib.mx_linear_bwd(dY, X, T, w, L1, L2, s, dropout=drop)
+    near(dL1, ref1, 2.5e-6)
+    near(dL2, ref2, 1.25e-6)
+    base = lib.mx_matmul(lib.mx_quantize(dY[-tail:].contiguous()), w.bwd)
+    assert torch.equal(dX[-tail:][~keep], base[~keep])
+    assert (dX[-tail:][keep] != base[keep]).float().mean() > 0.9
+    del dX, Y
+    _, dL1, _ = lib.mx_linear_bwd(dY, X, T, w, L1, L2, s, dropout=drop, need_dX=False, need_dL2=False)
+    near(dL1, ref1, 2.5e-6)
+    assert lib.read_status() == 0
