@@ -20,8 +20,8 @@
 // or, without them (dL1 alone, few tokens), by evaluating the generator.
 //
 // Measured, dL2 of 8192 x 8192 with r = 64: 36 us (35 before infinities were told
-// apart), 134 MB at 3.8 TB/s (4.5 by the slope over longer ones).  Without the loads of the terms the
-// slope is 5.9 TB/s: of a stage's 40 KB the terms are 24, and L2 gives them
+// apart), 134 MB at 3.8 TB/s (4.5 by the slope over longer ones).  Without the
+// loads of the terms the slope is 5.9 TB/s: of a stage's 40 KB the terms are 24, and L2 gives them
 // out at about 11 TB/s.  An evaluated mask costs 1024 evaluations a stage, 90
 // cycles each for a warp and scheduler, on the pipes of the masking: backward
 // of 4096 x 4096 x 4096 with dropout 96 us, with the bits 93.5 (95 since dX takes

@@ -12,10 +12,10 @@
 // tile as the A operand of D.
 //
 // Work is cut into units of 128 rows x 256 columns.  While clusters of up to 8
-// CTAs (16 for up to 4 row tiles) for every row tile run at once, a cluster takes a row tile, adds its
-// CTAs' sums in rank order through distributed shared memory and forms T and
-// the bf16 terms of the scaled D itself (two for the products, three where the
-// adapter gradients take them too).  For more rows
+// CTAs (16 for up to 4 row tiles) for every row tile run at once, a cluster
+// takes a row tile, adds its CTAs' sums in rank order through distributed
+// shared memory and forms T and the bf16 terms of the scaled D itself (two for
+// the products, three where the adapter gradients take them too).  For more rows
 // one CTA per SM takes an equal run of units in order (the last units of a row
 // tile and the first of the next may share a CTA); a run's rows of D go to a
 // partial slot, and a small second kernel adds the slots of a row tile in
