@@ -258,7 +258,7 @@ cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64
 cudaError_t launch_dropout(const void* X, int dtype, int64_t n, const DropArgs& d, void* out, int sms, cudaStream_t st);
 
 // bf16 terms of the LoRA term's token side (s T or the scaled dT) in a product.
-// One, its rounding to bf16, would leave an error of up to 2^-9 of the LoRA
+// One, its rounding to bf16, would leave an error of up to 2^-8 of the LoRA
 // term, as large as the rounding of the result where that term carries it (1.83e-3
 // of dX of 1088 x 256 x 64, r = 16, in place of 1.65e-3); two leave 2^-16.
 constexpr int kLoraTerms = 2;

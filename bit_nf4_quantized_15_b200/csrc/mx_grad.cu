@@ -21,11 +21,11 @@
 //
 // Measured, dL2 of 8192 x 8192 with r = 64: 36 us (35 before infinities were told
 // apart), 134 MB at 3.8 TB/s (4.5 by the slope over longer ones).  Without the
-// loads of the terms the slope is 5.9 TB/s: of a stage's 40 KB the terms are 24, and L2 gives them
-// out at about 11 TB/s.  An evaluated mask costs 1024 evaluations a stage, 90
-// cycles each for a warp and scheduler, on the pipes of the masking: backward
-// of 4096 x 4096 x 4096 with dropout 96 us, with the bits 93.5 (95 since dX takes
-// two terms of dT).
+// loads of the terms the slope is 5.9 TB/s: of a stage's 40 KB the terms are 24,
+// and L2 gives them out at about 11 TB/s.  An evaluated mask costs 1024
+// evaluations a stage, 90 cycles each for a warp and scheduler, on the pipes of
+// the masking: backward of 4096 x 4096 x 4096 with dropout 96 us, with the bits
+// 93.5 (95 since dX takes two terms of dT).
 //
 // Roles: warp 0 TMA producer, 1 MMA issuer, 4-7 sum, 8-23 mask.
 #include "engine_util.cuh"

@@ -27,7 +27,7 @@ pytestmark = pytest.mark.gpu
 def test_lora_term_keeps_sixteen_bits(lib, M, N, K, r, p):
     """Where the LoRA term is as large as the base product, Y and dX are off
     by the rounding of the result and by 2^-16 of the LoRA term's sizes, not by
-    the 2^-9 of an operand rounded to bf16."""
+    the 2^-8 of an operand rounded to bf16."""
     X, w, L1, L2, dY, W64 = _problem(lib, M, N, K, r, seed=M + r)
     s = 16.0 / r
     drop = lib.Dropout(p, 5, M) if p else None
